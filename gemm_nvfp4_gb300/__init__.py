@@ -17,7 +17,9 @@ from .binding import (NVFP4_ERR_DEVICE_TIMEOUT, NVFP4_OK, NVFP4_STATUS_WORD_OFFS
                       nvfp4_noalloc_status, SkinnyJob, StreamPlan, nvfp4_stream_plan, nvfp4_stream_plan_bytes,
                       nvfp4_stream_run, nvfp4_quantize,
                       nvfp4_quantize_bf16, nvfp4_selftest_wait_timeout, nvfp4_status_string, nvfp4_version,
-                      nvfp4_workspace_bytes)
+                      nvfp4_workspace_bytes, NVFP4_ERR_DEVICE_INDEX, NVFP4_KV_E4M3, NVFP4_KV_NVFP4,
+                      NVFP4_OP_KV_APPEND, KVCache, nvfp4_kv_append, nvfp4_kv_page_bytes, nvfp4_kv_read,
+                      nvfp4_paged_attention, nvfp4_paged_attention_workspace_bytes)
 
 __all__ = [
     "NVFP4Error", "NVFP4Weight", "FP6Weight",
@@ -31,4 +33,7 @@ __all__ = [
     "nvfp4_device_status", "nvfp4_selftest_wait_timeout", "NVFP4_OK", "NVFP4_ERR_DEVICE_TIMEOUT",
     "NVFP4_STATUS_WORD_OFFSET", "nvfp4_noalloc_status", "nvfp4_noalloc_selftest_wait_timeout",
     "SkinnyJob", "StreamPlan", "nvfp4_stream_plan", "nvfp4_stream_plan_bytes", "nvfp4_stream_run",
+    "KVCache", "nvfp4_kv_page_bytes", "nvfp4_kv_append", "nvfp4_kv_read", "nvfp4_paged_attention",
+    "nvfp4_paged_attention_workspace_bytes", "NVFP4_KV_E4M3", "NVFP4_KV_NVFP4", "NVFP4_OP_KV_APPEND",
+    "NVFP4_ERR_DEVICE_INDEX",
 ]

@@ -23,6 +23,7 @@ NVFP4_ERR_UNSUPPORTED_SHAPE = 2
 NVFP4_ERR_WORKSPACE = 3
 NVFP4_ERR_CUDA = 4
 NVFP4_ERR_DEVICE_TIMEOUT = 5
+NVFP4_ERR_DEVICE_INDEX = 6
 
 NVFP4_STATUS_WORD_OFFSET = 128
 
@@ -32,9 +33,13 @@ NVFP4_OP_GATEUP_SWIGLU = 2
 NVFP4_OP_GEMM_PREFILL = 3
 NVFP4_OP_FP6_GEMM = 4
 NVFP4_OP_FP6_GATEUP_SWIGLU = 5
+NVFP4_OP_KV_APPEND = 6
 
 NVFP4_OUT_F32 = 0
 NVFP4_OUT_BF16 = 1
+
+NVFP4_KV_E4M3 = 0
+NVFP4_KV_NVFP4 = 1
 
 _lock = threading.Lock()
 _lib = None
@@ -46,6 +51,22 @@ class SkinnyJobC(ctypes.Structure):
                 ("n_weights", ctypes.c_int32), ("codes", ctypes.c_void_p * 2), ("scales", ctypes.c_void_p * 2),
                 ("tensor_scale", ctypes.c_void_p * 2), ("M", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("y", ctypes.c_void_p), ("out_dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class KVCacheC(ctypes.Structure):
+    """nvfp4_kv_cache of include/nvfp4.h."""
+    _fields_ = [("pool", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_size", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class PagedAttentionArgsC(ctypes.Structure):
+    """nvfp4_paged_attention_args of include/nvfp4.h."""
+    _fields_ = [("cache", KVCacheC), ("q", ctypes.c_void_p), ("q_ld", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_ld", ctypes.c_int64), ("block_table", ctypes.c_void_p), ("table_width", ctypes.c_int64),
+                ("kv_lens", ctypes.c_void_p), ("q_offsets", ctypes.c_void_p), ("tree", ctypes.c_void_p),
+                ("n_seqs", ctypes.c_int64), ("total_q", ctypes.c_int64), ("max_q_len", ctypes.c_int64),
+                ("window", ctypes.c_int64), ("n_q_heads", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("causal", ctypes.c_int32), ("scale", ctypes.c_float)]
 
 
 class NVFP4Error(RuntimeError):
@@ -111,6 +132,16 @@ def load_library():
         lib.nvfp4_noalloc_status.argtypes = [i32, ctypes.POINTER(ctypes.c_uint32), P]
         lib.nvfp4_noalloc_selftest_wait_timeout.restype = i32
         lib.nvfp4_noalloc_selftest_wait_timeout.argtypes = [P]
+        cache_p, args_p = ctypes.POINTER(KVCacheC), ctypes.POINTER(PagedAttentionArgsC)
+        lib.nvfp4_kv_page_bytes.restype = sz
+        lib.nvfp4_kv_page_bytes.argtypes = [ctypes.c_int32] * 4
+        for f in (lib.nvfp4_kv_append, lib.nvfp4_kv_read):
+            f.restype = i32
+            f.argtypes = [cache_p, P, i64, P, i64, P, i64, P, sz, P]
+        lib.nvfp4_paged_attention_workspace_bytes.restype = sz
+        lib.nvfp4_paged_attention_workspace_bytes.argtypes = [args_p]
+        lib.nvfp4_paged_attention.restype = i32
+        lib.nvfp4_paged_attention.argtypes = [args_p, P, sz, P]
         lib.nvfp4_device_status.restype = i32
         lib.nvfp4_device_status.argtypes = [P, sz, i32, ctypes.POINTER(ctypes.c_uint32), P]
         lib.nvfp4_selftest_wait_timeout.restype = i32
@@ -293,12 +324,13 @@ def nvfp4_gemm_prefill(x: torch.Tensor, W: NVFP4Weight, out_dtype=torch.float32,
 def nvfp4_device_status(workspace: torch.Tensor, clear: bool = True, stream=None) -> tuple[int, int]:
     """(status, code) of the device status word in a product call's workspace:
     (NVFP4_OK, 0), or (NVFP4_ERR_DEVICE_TIMEOUT, code) when a kernel's bounded
-    wait gave up since the word was last cleared.  Synchronises the stream;
+    wait gave up since the word was last cleared, or (NVFP4_ERR_DEVICE_INDEX,
+    code) when a KV-cache call met an index outside its bounds.  Synchronises the stream;
     with clear=True a nonzero word is reset."""
     code = ctypes.c_uint32(0)
     st = load_library().nvfp4_device_status(_ptr(workspace), workspace.numel() * workspace.element_size(),
                                             int(bool(clear)), ctypes.byref(code), _stream(stream))
-    if st not in (NVFP4_OK, NVFP4_ERR_DEVICE_TIMEOUT):
+    if st not in (NVFP4_OK, NVFP4_ERR_DEVICE_TIMEOUT, NVFP4_ERR_DEVICE_INDEX):
         raise NVFP4Error(st, "nvfp4_device_status")
     return st, code.value
 
@@ -492,3 +524,172 @@ def nvfp4_stream_run(plan: StreamPlan, stream=None) -> None:
     st = load_library().nvfp4_stream_run(_ptr(plan.buffer), plan.nbytes(), _stream(stream))
     _check(st, "nvfp4_stream_run")
 
+
+
+# ---------------------------------------------------------------------------
+# Quantised paged KV cache and attention over it
+# ---------------------------------------------------------------------------
+
+def nvfp4_kv_page_bytes(page_size: int, n_kv_heads: int, head_dim: int, format: int) -> int:
+    return load_library().nvfp4_kv_page_bytes(int(page_size), int(n_kv_heads), int(head_dim), int(format))
+
+
+@dataclass
+class KVCache:
+    """One layer's quantised paged KV cache (include/nvfp4.h has the layout)."""
+    pool: torch.Tensor   # uint8 [n_pages, n_kv_heads, 2 (K, V), block]
+    page_size: int       # tokens of a page: 16, 32, 64, 128 or 256
+    head_dim: int        # 64 or 128
+    format: int          # NVFP4_KV_E4M3 or NVFP4_KV_NVFP4
+
+    @classmethod
+    def empty(cls, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int, format: int = NVFP4_KV_E4M3,
+              device="cuda") -> "KVCache":
+        """A cache of n_pages pages; its slots hold nothing until they are appended to."""
+        size = nvfp4_kv_page_bytes(page_size, n_kv_heads, head_dim, format)
+        if size == 0:
+            raise NVFP4Error(NVFP4_ERR_UNSUPPORTED_SHAPE, "KVCache.empty")
+        return cls(torch.empty(n_pages, n_kv_heads, 2, size // (2 * n_kv_heads), dtype=torch.uint8, device=device),
+                   page_size, head_dim, format)
+
+    @property
+    def n_pages(self) -> int:
+        return self.pool.shape[0]
+
+    @property
+    def n_kv_heads(self) -> int:
+        return self.pool.shape[1]
+
+    def c(self) -> KVCacheC:
+        pool = self.pool
+        n_pages, heads = pool.shape[:2]
+        if pool.dtype != torch.uint8 or not pool.is_contiguous() or pool.numel() != n_pages * nvfp4_kv_page_bytes(
+                self.page_size, heads, self.head_dim, self.format):
+            raise ValueError("pool is not a contiguous uint8 [n_pages, n_kv_heads, 2, block] of this cache's format")
+        return KVCacheC(pool.data_ptr(), n_pages, self.page_size, heads, self.head_dim, self.format)
+
+
+def _buffer(t):
+    """(address, bytes) of a workspace tensor, or of none."""
+    return (None, 0) if t is None else (t.data_ptr(), t.numel() * t.element_size())
+
+
+def _head_rows(t, heads, head_dim, dtypes, what):
+    """Token stride (elements) of [tokens, heads, head_dim] rows whose heads lie side by side."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or t.dtype not in dtypes:
+        raise ValueError(f"{what} must be {' or '.join(str(d) for d in dtypes)} [tokens, {heads}, {head_dim}], "
+                         f"got {t.dtype} {list(t.shape)}")
+    tokens, by_head, by_elem = t.stride()
+    if by_elem != 1 or (heads > 1 and by_head != head_dim):
+        raise ValueError(f"{what}: the heads of a token must lie side by side (strides {t.stride()})")
+    return tokens if t.shape[0] > 1 else max(tokens, heads * head_dim)
+
+
+_BF16 = (torch.bfloat16,)
+
+
+def _check_slots(slots, tokens):
+    if slots.dtype != torch.int64 or slots.shape != (tokens,) or not slots.is_contiguous():
+        raise ValueError(f"slots must be a contiguous int64 [{tokens}], got {slots.dtype} {list(slots.shape)}")
+
+
+def nvfp4_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                    workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Quantise bf16 k, v [tokens, n_kv_heads, head_dim] (token rows may be
+    strided, as column ranges of a QKV output are) into the cache's slots.  A
+    negative slot leaves its token out."""
+    c = cache.c()
+    k_ld = _head_rows(k, c.n_kv_heads, c.head_dim, _BF16, "k")
+    v_ld = _head_rows(v, c.n_kv_heads, c.head_dim, _BF16, "v")
+    if v.shape[0] != k.shape[0]:
+        raise ValueError(f"k has {k.shape[0]} tokens, v {v.shape[0]}")
+    _check_slots(slots, k.shape[0])
+    ws, ws_bytes = _buffer(workspace)
+    st = load_library().nvfp4_kv_append(ctypes.byref(c), k.data_ptr(), k_ld, v.data_ptr(), v_ld, slots.data_ptr(),
+                                        k.shape[0], ws, ws_bytes, _stream(stream))
+    _check(st, "nvfp4_kv_append")
+
+
+def nvfp4_kv_read(cache: KVCache, slots: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None,
+                  workspace: torch.Tensor | None = None, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """(k, v) of the cache's slots as bf16 [tokens, n_kv_heads, head_dim]; rows
+    of negative slots are zero."""
+    c = cache.c()
+    if out is None:
+        out = tuple(torch.empty(slots.numel(), c.n_kv_heads, c.head_dim, dtype=torch.bfloat16, device=slots.device)
+                    for _ in range(2))
+    k, v = out
+    k_ld = _head_rows(k, c.n_kv_heads, c.head_dim, _BF16, "k")
+    v_ld = _head_rows(v, c.n_kv_heads, c.head_dim, _BF16, "v")
+    _check_slots(slots, k.shape[0])
+    _check_slots(slots, v.shape[0])
+    ws, ws_bytes = _buffer(workspace)
+    st = load_library().nvfp4_kv_read(ctypes.byref(c), k.data_ptr(), k_ld, v.data_ptr(), v_ld, slots.data_ptr(),
+                                      k.shape[0], ws, ws_bytes, _stream(stream))
+    _check(st, "nvfp4_kv_read")
+    return out
+
+
+def nvfp4_paged_attention_workspace_bytes(cache: KVCache, q: torch.Tensor, n_seqs: int, max_q_len: int) -> int:
+    """Bytes of workspace for attention of q [total_q, n_q_heads, head_dim] over the cache."""
+    a = PagedAttentionArgsC(cache=cache.c(), n_seqs=n_seqs, total_q=q.shape[0], max_q_len=max_q_len,
+                            n_q_heads=q.shape[1])
+    return load_library().nvfp4_paged_attention_workspace_bytes(ctypes.byref(a))
+
+
+def _device_ints(t, dtype, shape, what):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
+    return t.data_ptr()
+
+
+def nvfp4_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, kv_lens: torch.Tensor,
+                          q_offsets: torch.Tensor | None = None, max_q_len: int | None = None,
+                          scale: float | None = None, causal: bool = True, window: int = 0,
+                          tree: torch.Tensor | None = None, out_dtype=torch.bfloat16,
+                          out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                          stream=None) -> torch.Tensor:
+    """Attention of new tokens q (bf16 [total_q, n_q_heads, head_dim]) over the cache.
+
+    block_table int32 [n_seqs, width], kv_lens int32 [n_seqs] (keys in the
+    cache, the new tokens' own among them when causal); q_offsets int32
+    [n_seqs + 1] for sequences with different numbers of new tokens, with
+    max_q_len their largest; tree int64 [total_q], bit j of a token's word:
+    it sees the sequence's new token j.  scale defaults to head_dim ** -0.5."""
+    c = cache.c()
+    if q.dim() != 3:
+        raise ValueError(f"q must be [total_q, n_q_heads, head_dim], got {list(q.shape)}")
+    total_q, heads, head_dim = q.shape
+    q_ld = _head_rows(q, heads, c.head_dim, _BF16, "q")
+    n_seqs = kv_lens.shape[0]
+    if block_table.dim() != 2:
+        raise ValueError(f"block_table must be [n_seqs, width], got {list(block_table.shape)}")
+    width = block_table.shape[1]
+    if max_q_len is None:
+        if q_offsets is not None:
+            raise ValueError("q_offsets needs max_q_len")
+        if n_seqs == 0 or total_q % n_seqs:
+            raise ValueError(f"{total_q} tokens are not the same number for each of {n_seqs} sequences: give q_offsets")
+        max_q_len = total_q // n_seqs
+    if out is None:
+        out = torch.empty(total_q, heads, head_dim, dtype=out_dtype, device=q.device)
+    out_ld = _head_rows(out, heads, c.head_dim, (torch.bfloat16, torch.float32), "out")
+    if out.shape[0] != total_q:
+        raise ValueError(f"q has {total_q} tokens, out {out.shape[0]}")
+    a = PagedAttentionArgsC(
+        c, q.data_ptr(), q_ld, out.data_ptr(), out_ld,
+        _device_ints(block_table, torch.int32, (n_seqs, width), "block_table"), width,
+        _device_ints(kv_lens, torch.int32, (n_seqs,), "kv_lens"),
+        None if q_offsets is None else _device_ints(q_offsets, torch.int32, (n_seqs + 1,), "q_offsets"),
+        None if tree is None else _device_ints(tree, torch.int64, (total_q,), "tree"),
+        n_seqs, total_q, max_q_len, window, heads, _out_code(out.dtype), 1 if causal else 0,
+        head_dim ** -0.5 if scale is None else scale)
+    lib = load_library()
+    if workspace is None:
+        # zero-filled: the call keeps arrival counters in it
+        workspace = torch.zeros(lib.nvfp4_paged_attention_workspace_bytes(ctypes.byref(a)), dtype=torch.uint8,
+                                device=q.device)
+    st = lib.nvfp4_paged_attention(ctypes.byref(a), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                   _stream(stream))
+    _check(st, "nvfp4_paged_attention")
+    return out

@@ -118,3 +118,18 @@ int check_skinny_call(const uint16_t *x, int64_t N, const uint8_t *codes, const 
                       bool *nothing_to_do);
 
 }  // namespace nvfp4
+
+namespace nvfp4 {
+
+// ---------------------------------------------------------------------------
+// Quantised paged KV cache (kv_cache.cu) and attention over it (attention.cu).
+// ---------------------------------------------------------------------------
+
+constexpr uint32_t kStatusKvFirst = 41;
+constexpr uint32_t kStatusKvAppendSlot = 41;  // append: slot beyond the pool
+constexpr uint32_t kStatusKvReadSlot = 42;    // read: slot beyond the pool
+constexpr uint32_t kStatusKvAttention = 43;   // attention: page, length or offset outside its bounds
+constexpr uint32_t kStatusKvLast = 43;
+constexpr size_t kKvWorkspaceBytes = 256;     // append and read: the status word
+
+}  // namespace nvfp4

@@ -138,6 +138,8 @@ const char *nvfp4_status_string(int status)
     case NVFP4_ERR_DEVICE_TIMEOUT:
         return "NVFP4_ERR_DEVICE_TIMEOUT: a kernel's bounded pipeline wait gave up; outputs since the status "
                "word was last cleared are undefined";
+    case NVFP4_ERR_DEVICE_INDEX:
+        return "NVFP4_ERR_DEVICE_INDEX: a KV-cache kernel met a slot, page, length or offset outside its bounds";
     default: return "NVFP4 unknown status";
     }
 }
@@ -146,6 +148,8 @@ int nvfp4_version(void) { return 100; }
 
 size_t nvfp4_workspace_bytes(int op, int64_t N, int64_t M, int64_t K)
 {
+    if (op == NVFP4_OP_KV_APPEND)
+        return kKvWorkspaceBytes;
     if (N < 0 || M < 0 || K < 0 || K % 16 != 0)
         return 0;
     switch (op) {
@@ -418,6 +422,8 @@ int nvfp4_device_status(const void *workspace, size_t workspace_bytes, int clear
         return NVFP4_ERR_CUDA;
     if (code)
         *code = v;
+    if (v >= kStatusKvFirst && v <= kStatusKvLast)
+        return NVFP4_ERR_DEVICE_INDEX;
     return v == 0 ? NVFP4_OK : NVFP4_ERR_DEVICE_TIMEOUT;
 }
 

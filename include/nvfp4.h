@@ -94,7 +94,8 @@ typedef enum {
     NVFP4_ERR_UNSUPPORTED_SHAPE = 2, /* K % 16 != 0, N outside the call's range, size overflow */
     NVFP4_ERR_WORKSPACE = 3,         /* workspace smaller than nvfp4_workspace_bytes() */
     NVFP4_ERR_CUDA = 4,              /* a CUDA runtime call or kernel launch failed */
-    NVFP4_ERR_DEVICE_TIMEOUT = 5     /* a kernel's bounded wait gave up (nvfp4_device_status) */
+    NVFP4_ERR_DEVICE_TIMEOUT = 5,    /* a kernel's bounded wait gave up (nvfp4_device_status) */
+    NVFP4_ERR_DEVICE_INDEX = 6       /* a KV-cache kernel met an index outside the cache (nvfp4_device_status) */
 } nvfp4_status;
 
 /* Operation ids for nvfp4_workspace_bytes. */
@@ -104,7 +105,8 @@ typedef enum {
     NVFP4_OP_GATEUP_SWIGLU = 2,
     NVFP4_OP_GEMM_PREFILL = 3,
     NVFP4_OP_FP6_GEMM = 4,
-    NVFP4_OP_FP6_GATEUP_SWIGLU = 5
+    NVFP4_OP_FP6_GATEUP_SWIGLU = 5,
+    NVFP4_OP_KV_APPEND = 6 /* and nvfp4_kv_read: the status word alone; N, M, K are not looked at */
 } nvfp4_op;
 
 /* Output element types. */
@@ -349,6 +351,143 @@ int nvfp4_fp6_gateup_swiglu(const uint16_t *x, int64_t N,
                             int64_t M, int64_t K, void *h, int out_dtype,
                             void *workspace, size_t workspace_bytes, nvfp4_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Quantised paged KV cache, and the attention that reads it: what a decoder
+ * layer needs between its QKV product and its O product.  (The pages keep
+ * their caches in 8 and 4 bits and attend to them in decode, in verify and in
+ * chunked prefill; they print no layout: bw24 wiki Home, feature list;
+ * qwentin README, "How it works".)
+ *
+ * A row is one token's K or V of one KV head: head_dim elements (64 or 128),
+ * stored with one power of two and
+ *   NVFP4_KV_E4M3   one E4M3 code per element:
+ *                   x = e4m3(code) * 2^(e - 127), head_dim + 1 bytes;
+ *   NVFP4_KV_NVFP4  one E2M1 code per element (element 2j in the low nibble of
+ *                   byte j) and one E4M3 scale per 16 elements:
+ *                   x = e2m1(code) * e4m3(scale) * 2^(e - 127),
+ *                   head_dim / 2 + head_dim / 16 + 1 bytes.
+ * The quantiser (nvfp4_kv_append; all steps exact but those marked, which are
+ * fp32 divisions rounded to nearest even):
+ *   k     = the smallest integer with max |x| <= T * 2^k, T = 448 (E4M3) or
+ *           2688 (NVFP4), and at least -100;  e = k + 127;
+ *   E4M3:   code  = nearest E4M3 to x / 2^k, ties to the even code;
+ *   NVFP4:  scale = nearest E4M3 to (block max |x| / 6 [rounded]) / 2^k,
+ *           code  = nearest E2M1 to (x / 2^k) / e4m3(scale) [rounded], ties to
+ *           the even code, magnitudes above 6 to 6; all zero if scale = 0.
+ * Every stored value is a bf16 number.  A row that holds an infinity or a NaN,
+ * or that would need k > 100, is stored as e = 255 with all codes zero: it
+ * reads back as NaN, and a query that sees it gets NaN.
+ *
+ * pool is uint8 [n_pages][n_kv_heads][2][block]: [0] K, [1] V; block =
+ * page_size * (bytes of a row), which holds page_size rows of codes, then
+ * (NVFP4) page_size rows of head_dim / 16 scales, then page_size bytes e.
+ * Slot s of a cache is row s % page_size of page s / page_size.
+ * Slots that no append has written hold whatever the pool held.
+ * ------------------------------------------------------------------------- */
+typedef enum { NVFP4_KV_E4M3 = 0, NVFP4_KV_NVFP4 = 1 } nvfp4_kv_format;
+
+typedef struct {
+    void *pool;         /* device, n_pages * nvfp4_kv_page_bytes(...) bytes, 16-byte aligned */
+    int64_t n_pages;    /* at most 2^31 - 1 */
+    int32_t page_size;  /* tokens of a page: 16, 32, 64, 128 or 256 */
+    int32_t n_kv_heads; /* 1 to 1024 */
+    int32_t head_dim;   /* 64 or 128 */
+    int32_t format;     /* nvfp4_kv_format */
+} nvfp4_kv_cache;
+
+/* Bytes of one page of a pool (every head, K and V); 0 for values the calls
+ * below reject.  Host only. */
+size_t nvfp4_kv_page_bytes(int32_t page_size, int32_t n_kv_heads, int32_t head_dim, int32_t format);
+
+/* Quantise new tokens into the cache.
+ * k, v       device bf16 bits [n_tokens][k_ld], [n_tokens][v_ld]: n_kv_heads rows
+ *            of head_dim elements side by side per token, so that both can be
+ *            column ranges of one QKV product's output.  16-byte aligned, k_ld
+ *            and v_ld multiples of 8 and at least n_kv_heads * head_dim.
+ * slots      device int64 [n_tokens]: the slot of each token; a negative slot
+ *            leaves its token out.  Two tokens of a call with one slot race.
+ * workspace  NULL, or nvfp4_workspace_bytes(NVFP4_OP_KV_APPEND, ...) bytes
+ *            with the status word.  A slot beyond the pool is never written;
+ *            it stores code 41 in that word.
+ * n_tokens * n_kv_heads below 2^30. */
+int nvfp4_kv_append(const nvfp4_kv_cache *cache, const uint16_t *k, int64_t k_ld, const uint16_t *v, int64_t v_ld,
+                    const int64_t *slots, int64_t n_tokens, void *workspace, size_t workspace_bytes,
+                    nvfp4_stream_t stream);
+
+/* Read rows of the cache back as bf16 (exactly their stored values): arguments
+ * as for nvfp4_kv_append, with k and v the outputs.  A negative slot gives a row of
+ * zeros, and so does a slot beyond the pool, which also stores code 42. */
+int nvfp4_kv_read(const nvfp4_kv_cache *cache, uint16_t *k, int64_t k_ld, uint16_t *v, int64_t v_ld,
+                  const int64_t *slots, int64_t n_tokens, void *workspace, size_t workspace_bytes,
+                  nvfp4_stream_t stream);
+
+/* Attention of new tokens over the cache.  Sequence b has kv_lens[b] keys in the
+ * cache: key j is row j % page_size of page block_table[b][j / page_size].  Its
+ * new tokens are rows q_offsets[b] .. q_offsets[b + 1] - 1 of q and out.  With
+ * n of them, token i (from 0) is at position p = kv_lens[b] - n + i when
+ * causal (append its K and V first: the new tokens are the last n keys), and sees
+ *   causal                     keys j <= p; with window > 0 only j > p - window;
+ *   causal with `tree`         keys j < kv_lens[b] - n, and the new token j' if bit
+ *                              j' of tree[row of i] is set (a speculative tree:
+ *                              each token's ancestors and itself);
+ *   not causal                 every key (cross attention).
+ * out = sum_j softmax_j(scale * q . k_j) v_j over the keys it sees, query head
+ * h reading KV head h / (n_q_heads / n_kv_heads).  A token that sees no key
+ * gets zeros; a query that holds an infinity or a NaN gets NaN; K and V of keys that a token does not see never reach its output,
+ * whatever they hold.
+ *
+ * Numerics: q . k_j is exact in its products (q scaled by a power of two to
+ * f16, K's codes in f16) with fp32 accumulation; softmax statistics are fp32
+ * (2^x by the hardware's approximation, relative error about 2^-22); the weights
+ * enter the second product in f16, rounded to nearest (relative error at most
+ * 2^-11 each), with fp32 accumulation:
+ * |out - exact| <= (2^-10 + 2^-15 * S) * sum_j softmax_j |v_j|, plus the rounding
+ * of out, with S = max_j |scale| * sum_d |q_d k_jd| (the fp32 sums of scores).
+ *
+ * Requirements: q, out 16-byte aligned; q_ld and out_ld multiples of 8, at
+ * least n_q_heads * head_dim; n_q_heads a multiple of n_kv_heads; tree only
+ * with causal, without window and with max_q_len <= 64.
+ * Lengths and tables stay on the device: the call never synchronises and can
+ * be captured in a CUDA graph and replayed with other lengths.  What they hold is
+ * checked in the kernel: a page outside the pool, a kv_len above table_width *
+ * page_size, more new tokens than max_q_len or (causal) than kv_len, or
+ * offsets that do not ascend within total_q store code 43 in the status word;
+ * the keys and tokens beyond are left out.  Table entries of pages that no
+ * query of a call sees (beyond kv_len, or before the window) are not looked at.
+ * workspace  nvfp4_paged_attention_workspace_bytes(args) bytes, zero-filled
+ *            before its first use; each call leaves its counters zero, so one
+ *            buffer serves calls of any shapes, ordered on one stream.
+ * Determinism: a token's result depends on the shapes and lengths of the call,
+ * never on timing. */
+typedef struct {
+    nvfp4_kv_cache cache;
+    const uint16_t *q;          /* device bf16 bits [total_q][q_ld] */
+    int64_t q_ld;
+    void *out;                  /* device [total_q][out_ld], fp32 or bf16 bits */
+    int64_t out_ld;
+    const int32_t *block_table; /* device [n_seqs][table_width]: page numbers */
+    int64_t table_width;
+    const int32_t *kv_lens;     /* device [n_seqs] */
+    const int32_t *q_offsets;   /* device [n_seqs + 1]; NULL: every sequence has max_q_len new tokens */
+    const uint64_t *tree;       /* device [total_q] or NULL */
+    int64_t n_seqs;             /* at most 65535 */
+    int64_t total_q;            /* rows of q and out; n_seqs * max_q_len without q_offsets */
+    int64_t max_q_len;          /* at least every sequence's number of new tokens */
+    int64_t window;             /* 0: none */
+    int32_t n_q_heads;
+    int32_t out_dtype;          /* nvfp4_out_dtype */
+    int32_t causal;             /* 0 or 1 */
+    float scale;                /* finite */
+} nvfp4_paged_attention_args;
+
+/* Bytes of workspace for these args (cache shape, n_q_heads, n_seqs, total_q and
+ * max_q_len are looked at; pointers are not); 0 for sizes the call rejects.
+ * Host only; does not depend on the device, nor on any length of a sequence. */
+size_t nvfp4_paged_attention_workspace_bytes(const nvfp4_paged_attention_args *args);
+
+int nvfp4_paged_attention(const nvfp4_paged_attention_args *args, void *workspace, size_t workspace_bytes,
+                          nvfp4_stream_t stream);
+
 /* Skinny product without a caller workspace, for callers that cannot allocate
  * device memory.  The source pages have no counterpart for this call: it is an
  * addition of this library.  A plain C or Fortran host program with no
@@ -418,9 +557,10 @@ int nvfp4_noalloc_selftest_wait_timeout(nvfp4_stream_t stream);
 /* Read the status word of `workspace` (device, at least
  * NVFP4_STATUS_WORD_OFFSET + 4 bytes, 16-byte aligned) after the work enqueued
  * on `stream` so far: synchronises `stream`, stores the word in *code (if
- * code is not NULL) and returns NVFP4_OK when it is zero, else
- * NVFP4_ERR_DEVICE_TIMEOUT.  With clear != 0 a nonzero word is reset to zero
- * on `stream` afterwards.  NVFP4_ERR_INVALID_ARG for a null, misaligned or too
+ * code is not NULL) and returns NVFP4_OK when it is zero,
+ * NVFP4_ERR_DEVICE_INDEX when it holds one of the codes 41..43 of the KV-cache
+ * calls, else NVFP4_ERR_DEVICE_TIMEOUT.  With clear != 0 a nonzero word is
+ * reset to zero on `stream` afterwards.  NVFP4_ERR_INVALID_ARG for a null, misaligned or too
  * small workspace; NVFP4_ERR_CUDA if the copy or the synchronisation fails. */
 int nvfp4_device_status(const void *workspace, size_t workspace_bytes, int clear, uint32_t *code,
                         nvfp4_stream_t stream);
