@@ -1,0 +1,177 @@
+// attention_plan.cuh -- how the attention kernels share a call's work out.
+//
+// An item is a block of query rows of one sequence and KV head: rows r of the
+// sequence's new tokens times the query heads of one KV head (row r = token
+// r / group, head r % group), RB at a time.  Its work is its key range in
+// tiles of TK keys.  All items of all sequences form one list of tiles (heads
+// fastest, then row blocks, then sequences), and CTA c of P takes the c-th of
+// P equal ranges of it, whatever the lengths: long sequences are split over
+// many CTAs, short ones share one, and every CTA has the same number of tiles
+// to within one.  The lengths are on the device, so each CTA finds its range
+// itself.
+//
+// A CTA that holds a whole item writes its output rows.  Otherwise it leaves
+// its partial result (accumulators, maximum and sum) in one of its two slots
+// of the workspace (an item can reach into a CTA's range from the left or out
+// of it to the right), and the last CTA of the item to arrive adds all partials
+// in CTA order, so that the result does not depend on who was last.
+#pragma once
+
+#include "attention.h"
+
+namespace nvfp4 {
+namespace attn {
+
+// Workspace: the status word (in the first 256 bytes), an arrival counter per
+// CTA at byte 256, then two partial slots per CTA.
+constexpr int kMaxCtas = 320;
+constexpr size_t kCounterOffset = 256;
+constexpr size_t kPartialOffset = kCounterOffset + kMaxCtas * sizeof(uint32_t);
+
+// Rows of an item of the decode kernel, and the CTAs that it may have at most
+// (two on an SM while a thread's accumulators leave room for them).
+constexpr int decode_block(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+constexpr int decode_max_ctas(int block) { return block <= 16 ? kMaxCtas : kMaxCtas / 2; }
+
+struct Item {
+    Seq seq;
+    int b, rb, head;    // sequence, row block, KV head
+    int row0, rows;     // rows of the block
+    int lo, hi;         // keys that some row of the block may see
+    int tile0, tiles;   // first tile (in units of TK keys from key 0) and their number
+};
+
+// Rows and key range of row block rb of an item's sequence.
+template <int RB, int TK>
+NVFP4_DEVINL void set_block(const Call &c, Item &it)
+{
+    it.row0 = it.rb * RB;
+    it.rows = min(RB, it.seq.n * c.group - it.row0);
+    int unused;
+    key_range(c, it.seq, it.row0 / c.group, &it.lo, &unused);
+    key_range(c, it.seq, (it.row0 + it.rows - 1) / c.group, &unused, &it.hi);
+    it.tile0 = it.lo / TK;
+    // an item without keys still has its zeros to write
+    it.tiles = max(1, (it.hi + TK - 1) / TK - it.tile0);
+}
+
+template <int RB>
+NVFP4_DEVINL int row_blocks(const Call &c, const Seq &s) { return (s.n * c.group + RB - 1) / RB; }
+
+// Tiles of a sequence, over all its row blocks and KV heads.
+template <int RB, int TK>
+NVFP4_DEVINL int64_t seq_tiles(const Call &c, int b)
+{
+    Item it;
+    it.seq = load_seq(c, b);
+    const int blocks = row_blocks<RB>(c, it.seq);
+    int64_t n = 0;
+    for (it.rb = 0; it.rb < blocks; ++it.rb) {
+        set_block<RB, TK>(c, it);
+        n += it.tiles;
+    }
+    return n * c.pool.heads;
+}
+
+struct Range {
+    int64_t total;       // tiles of the call
+    int64_t begin, end;  // of this CTA
+    int ctas;            // that have a range
+};
+
+NVFP4_DEVINL int64_t range_start(int64_t total, int ctas, int cta) { return total * cta / ctas; }
+// The CTA whose range holds tile u.
+NVFP4_DEVINL int range_owner(int64_t total, int ctas, int64_t u)
+{
+    return (int)(((u + 1) * ctas + total - 1) / total) - 1;
+}
+
+// Every thread of the CTA calls this: this CTA's range, its first item, and
+// the list position of that item's first tile.  `scratch`: shared memory,
+// THREADS / 32 + 4 words of 64 bits.  Returns false if the CTA has no work.
+template <int RB, int TK, int THREADS>
+__device__ bool find_range(const Call &c, int64_t *scratch, Range *range, Item *item, int64_t *item_begin)
+{
+    const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
+    // thread t sums the t-th run of consecutive sequences; a scan over the threads follows
+    const int per = (c.n_seqs + THREADS - 1) / THREADS;
+    const int b0 = min(tid * per, c.n_seqs), b1 = min(b0 + per, c.n_seqs);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b)
+        mine += seq_tiles<RB, TK>(c, b);
+    int64_t upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int64_t v = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+        if (lane >= o)
+            upto += v;
+    }
+    if (lane == 31)
+        scratch[warp] = upto;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        const int64_t v = scratch[w];
+        before += w < warp ? v : 0;
+        total += v;
+    }
+    upto += before;
+    range->total = total;
+    range->ctas = (int)min((int64_t)gridDim.x, total);
+    if ((int)blockIdx.x >= range->ctas)
+        return false;
+    range->begin = range_start(total, range->ctas, blockIdx.x);
+    range->end = range_start(total, range->ctas, blockIdx.x + 1);
+    if (range->begin >= upto - mine && range->begin < upto) {  // exactly one thread
+        int64_t at = upto - mine;
+        int b = b0;
+        for (;; ++b) {
+            const int64_t n = seq_tiles<RB, TK>(c, b);
+            if (range->begin < at + n)
+                break;
+            at += n;
+        }
+        Item it;
+        it.seq = load_seq(c, b);
+        for (it.rb = 0;; ++it.rb) {
+            set_block<RB, TK>(c, it);
+            const int64_t n = (int64_t)it.tiles * c.pool.heads;
+            if (range->begin < at + n)
+                break;
+            at += n;
+        }
+        const int head = (int)((range->begin - at) / it.tiles);
+        int64_t *out = scratch + THREADS / 32;
+        out[0] = (int64_t)b << 32 | it.rb;
+        out[1] = head;
+        out[2] = at + (int64_t)head * it.tiles;
+    }
+    __syncthreads();
+    const int64_t *out = scratch + THREADS / 32;
+    item->b = (int)(out[0] >> 32);
+    item->rb = (int)(out[0] & 0x7FFFFFFF);
+    item->head = (int)out[1];
+    *item_begin = out[2];
+    item->seq = load_seq(c, item->b);
+    set_block<RB, TK>(c, *item);
+    return true;
+}
+
+// The item after `item` in the list (there is one: the range has tiles left).
+template <int RB, int TK>
+NVFP4_DEVINL void next_item(const Call &c, Item *item)
+{
+    if (++item->head < c.pool.heads)
+        return;
+    item->head = 0;
+    if (++item->rb >= row_blocks<RB>(c, item->seq)) {
+        item->rb = 0;
+        do
+            item->seq = load_seq(c, ++item->b);
+        while (item->seq.n == 0);
+    }
+    set_block<RB, TK>(c, *item);
+}
+
+}  // namespace attn
+}  // namespace nvfp4

@@ -132,4 +132,7 @@ constexpr uint32_t kStatusKvAttention = 43;   // attention: page, length or offs
 constexpr uint32_t kStatusKvLast = 43;
 constexpr size_t kKvWorkspaceBytes = 256;     // append and read: the status word
 
+// Streaming multiprocessors of the current device, cached per device; an nvfp4_status.
+int current_num_sms(int *out);
+
 }  // namespace nvfp4

@@ -10,14 +10,7 @@
 #include "../../include/nvfp4.h"
 #include "kernels.h"
 
-namespace {
-
-using namespace nvfp4;
-
-constexpr int kMaxSkinnyN = 16;
-static_assert(kStatusWordOffset == NVFP4_STATUS_WORD_OFFSET, "status word offset differs from the header");
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+namespace nvfp4 {
 
 // Streaming multiprocessors of the current device (cached per device id).
 int current_num_sms(int *out)
@@ -41,6 +34,17 @@ int current_num_sms(int *out)
     *out = n;
     return NVFP4_OK;
 }
+
+}  // namespace nvfp4
+
+namespace {
+
+using namespace nvfp4;
+
+constexpr int kMaxSkinnyN = 16;
+static_assert(kStatusWordOffset == NVFP4_STATUS_WORD_OFFSET, "status word offset differs from the header");
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 size_t skinny_ws(int64_t M, int64_t K, int n_weights) { return skinny_workspace_bytes(M, K, n_weights); }
 
