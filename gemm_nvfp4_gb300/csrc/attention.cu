@@ -13,6 +13,9 @@ namespace {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Which kernel: by the rows that share a KV head's keys.
+bool use_chunk(int64_t rows, int out_dtype) { return rows > 32 && out_dtype == NVFP4_OUT_BF16; }
+
 // Sizes alone; what nvfp4_paged_attention_workspace_bytes looks at.
 int check_sizes(const nvfp4_paged_attention_args *a)
 {
@@ -74,9 +77,11 @@ size_t nvfp4_paged_attention_workspace_bytes(const nvfp4_paged_attention_args *a
 {
     if (!args || attn::check_sizes(args) != NVFP4_OK)
         return 0;
-    const int block = attn::decode_block(args->max_q_len * (args->n_q_heads / args->cache.n_kv_heads));
-    return attn::kPartialOffset +
-           (size_t)attn::decode_max_ctas(block) * 2 * block * (args->cache.head_dim + 2) * sizeof(float);
+    const int64_t rows = args->max_q_len * (args->n_q_heads / args->cache.n_kv_heads);
+    const bool chunk = attn::use_chunk(rows, NVFP4_OUT_BF16);  // the larger of the two types' needs
+    const int block = !chunk ? attn::decode_block(rows) : rows <= 128 ? 128 : 256;
+    const int ctas = chunk ? attn::kMaxChunkCtas : attn::decode_max_ctas(block);
+    return attn::kPartialOffset + (size_t)ctas * 2 * block * (args->cache.head_dim + 2) * sizeof(float);
 }
 
 int nvfp4_paged_attention(const nvfp4_paged_attention_args *args, void *workspace, size_t workspace_bytes,
@@ -115,8 +120,10 @@ int nvfp4_paged_attention(const nvfp4_paged_attention_args *args, void *workspac
     rc = current_num_sms(&sms);
     if (rc != NVFP4_OK)
         return rc;
-    const auto launch =
-        args->cache.format == NVFP4_KV_E4M3 ? attn::launch_decode_e4m3 : attn::launch_decode_nvfp4;
+    const bool e4m3 = args->cache.format == NVFP4_KV_E4M3;
+    const auto launch = attn::use_chunk((int64_t)c.max_q_len * c.group, args->out_dtype)
+                            ? (e4m3 ? attn::launch_chunk_e4m3 : attn::launch_chunk_nvfp4)
+                            : (e4m3 ? attn::launch_decode_e4m3 : attn::launch_decode_nvfp4);
     const cudaError_t e = launch(c, args->cache.head_dim, workspace, sms, (cudaStream_t)stream);
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }

@@ -91,6 +91,9 @@ NVFP4_DEVINL int page_of(const Call &c, int b, int j)
 // Few rows per KV head (attention_decode.cuh), by cache format.
 cudaError_t launch_decode_e4m3(const Call &c, int head_dim, void *workspace, int num_sms, cudaStream_t stream);
 cudaError_t launch_decode_nvfp4(const Call &c, int head_dim, void *workspace, int num_sms, cudaStream_t stream);
+// Many rows per KV head, bf16 outputs (attention_chunk.cuh).
+cudaError_t launch_chunk_e4m3(const Call &c, int head_dim, void *workspace, int num_sms, cudaStream_t stream);
+cudaError_t launch_chunk_nvfp4(const Call &c, int head_dim, void *workspace, int num_sms, cudaStream_t stream);
 
 }  // namespace attn
 }  // namespace nvfp4

@@ -1,0 +1,888 @@
+// attention_chunk.cuh -- attention of many query rows per KV head (prefill
+// chunks, wide verifies) over the quantised paged cache, on tcgen05.
+//
+// With n new tokens and G query heads per KV head every cached element is used by
+// n * G rows, so the two products bound the kernel, with the softmax's 2^x close
+// behind (one per score: 16 a clock and SM, the time of the two products of
+// that score).  One CTA per SM, two row tiles of 128 in flight so that the tensor
+// pipe works on one while the other is in its softmax; warps by role:
+//
+//   warps 0-3, 4-7  softmax of row tile 0 and 1: a thread has one row.  Scores
+//                   come from tensor memory and the weights P go back there as
+//                   the f16 A operand of the second product, over the scores.
+//   warps 8-15      codes to f16: a tile of 128 keys is read from the pages into
+//                   registers one tile ahead, converted, and written to shared
+//                   memory in the layout of the MMA's B operands (K with the
+//                   head dimension contiguous; V likewise, read transposed).
+//   warps 16, 17    MMA issue for row tile 0 and 1: S = Q K^T, O += P V.
+//
+// SPLIT: when a sequence has at most 128 rows, both softmax groups take the same
+// row tile, one the even and the other the odd key tiles, and their results
+// are joined at the end; otherwise half the pipeline would idle.
+//
+// f16 holds codes exactly.  A row's power of two is applied relative to the
+// largest in its tile of 128 keys, whose exponent goes to the softmax as one
+// factor (K) and one addend (V; see attention_decode.cuh): exact as long as the
+// rows of a tile lie within 2^14 of each other; smaller rows are rounded to a
+// multiple of 2^-24 of the tile's unit (its largest value is between 224 and
+// 2688 units), below what bf16 outputs show.  Outputs are bf16 only.
+#pragma once
+
+#include <cstdint>
+
+#include "attention_plan.cuh"
+#include "skinny.cuh"
+
+namespace nvfp4 {
+namespace attn {
+namespace chunk {
+
+constexpr int kTile = 128;                      // keys of a tile
+constexpr int kRowTile = 128;                   // rows of a row tile
+constexpr int kSoftmaxWarps = 8, kConvertWarps = 8;
+constexpr int kConvertThreads = 32 * kConvertWarps;
+constexpr int kThreads = 32 * (kSoftmaxWarps + kConvertWarps + 4);  // whole warpgroups; warps 18, 19 idle
+constexpr int kStages = 2;
+constexpr int kInfos = 4;
+constexpr float kHeadroom = 7.f, kSlack = 15.f;
+constexpr float kSumUnit = 0x1p-32f;
+
+// Codes of the status word (waits that ran out).
+enum : uint32_t { kTimeoutSoftmax = 51, kTimeoutConvert = 52, kTimeoutMma = 53 };
+
+template <int FMT, int D, bool SPLIT>
+struct Cfg {
+    using R = kv::Row<FMT, D>;
+    static constexpr int kRows = SPLIT ? kRowTile : 2 * kRowTile;
+    static constexpr int kOperand = 128 * D * 2;  // Q, K or V tile in f16
+    static constexpr int kQAt = 0, kKAt = (SPLIT ? 1 : 2) * kOperand, kVAt = kKAt + kStages * kOperand;
+    static constexpr int kBarAt = kVAt + kStages * kOperand;
+    static constexpr int kSmem = kBarAt + 4096;
+    static constexpr int kSlotFloats = kRows * (D + 2);
+    // tensor memory columns
+    static constexpr int kScoreCols = 0, kOutCols = 2 * kTile;
+    // 16-byte chunks of codes: of a 64-element column block of a row, of a thread per tile
+    static constexpr int kPerBlock = FMT == NVFP4_KV_E4M3 ? 4 : 2;
+    static constexpr int kMine = D / 64 * kTile * kPerBlock / kConvertThreads;
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+};
+
+// What a converted tile tells the softmax.
+struct TileInfo {
+    float k_unit;      // 2^(exponent of K's unit)
+    float v_exp;       // exponent of V's unit
+    uint32_t present;  // bit g: the page of keys 16 g .. 16 g + 15 is there, or no row sees them
+    uint32_t pad;
+};
+
+struct Shared {
+    uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+    uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2], drain[2];
+    TileInfo info[kInfos];
+    uint32_t tmem, last;
+    int64_t scratch[kThreads / 32 + 4];
+    float2 stats[2][kRowTile];  // largest and sum of a row, by softmax group
+};
+
+// One lane of a converged warp; unlike a test of the lane number this tells the
+// compiler that a single thread follows, and MMA operands can go to uniform
+// registers directly (measured: 83 instead of 170 clocks per tcgen05.mma
+// issued back to back by one thread, M = N = 128, A in tensor memory).
+NVFP4_DEVINL bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{ .reg .pred q; .reg .b32 r; elect.sync r|q, 0xFFFFFFFF; selp.u32 %0, 1, 0, q; }" : "=r"(p));
+    return p != 0;
+}
+
+NVFP4_DEVINL float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+NVFP4_DEVINL uint32_t f32x2_to_f16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+NVFP4_DEVINL uint32_t f32x2_to_bf16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+NVFP4_DEVINL void sts128(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+// Address of 16-byte chunk `oc` (8 elements) of row `r` of a 128-row f16
+// operand: 64-element column blocks of 128 rows x 128 bytes, chunks of a row
+// permuted by the 128-byte swizzle.
+NVFP4_DEVINL uint32_t operand_chunk(uint32_t base, int r, int oc)
+{
+    return base + (oc >> 3) * (128 * 128) + r * 128 + (((oc & 7) ^ (r & 7)) << 4);
+}
+
+// B operand read with the key index as the reduction: rows are keys, the other
+// index is contiguous.  Leading offset: between 64-element column blocks;
+// stride offset: between groups of 8 keys.
+NVFP4_DEVINL uint64_t desc_transposed(uint32_t addr)
+{
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(128 * 128 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           1ull << 46 | 2ull << 61;
+}
+
+// A softmax group's part of a tile's sequence: with SPLIT, group g takes the
+// tiles of an item whose index in the CTA's list has parity g.
+template <bool SPLIT>
+NVFP4_DEVINL bool takes(int group, uint32_t tile) { return !SPLIT || (tile & 1) == (uint32_t)group; }
+
+// Whether a segment of n tiles from `tile` on has any for the group.
+template <bool SPLIT>
+NVFP4_DEVINL bool has_tile(int group, uint32_t tile, int n) { return n >= 2 || takes<SPLIT>(group, tile); }
+
+// The CTA's segments, walked by every role in the same way: f(item, first key
+// tile, number of tiles, index of the first tile in the CTA's list, whole item?).
+template <int RB, class F>
+NVFP4_DEVINL void for_segments(const Call &c, const Range &range, Item it, int64_t item_begin, F &&f)
+{
+    uint32_t tile = 0;
+    for (int64_t u = range.begin; u < range.end;) {
+        const int64_t item_end = item_begin + it.tiles, seg_end = min(item_end, range.end);
+        const int n = (int)(seg_end - u);
+        if (!f(it, it.tile0 + (int)(u - item_begin), n, tile, item_begin, item_end))
+            return;
+        tile += n;
+        u = seg_end;
+        if (u < range.end) {
+            item_begin = item_end;
+            next_item<RB, kTile>(c, &it);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Conversion warps
+// ---------------------------------------------------------------------------
+
+// A thread's share of one tile of K or V as it lies in the pages.
+template <int FMT, int D, bool SPLIT>
+struct Raw {
+    static constexpr int kMine = Cfg<FMT, D, SPLIT>::kMine;
+    uint4 codes[kMine];
+    uint32_t scales[FMT == NVFP4_KV_NVFP4 ? kMine : 1];
+};
+
+// Row and 64-element column block of a thread's i-th chunk, and the chunk's
+// place in the block: neighbouring lanes take the chunks of one block of a row,
+// then the next row, so that their stores fall on different banks.
+template <int FMT, int D, bool SPLIT>
+NVFP4_DEVINL void chunk_of(int tid, int i, int *row, int *block, int *place)
+{
+    constexpr int per = Cfg<FMT, D, SPLIT>::kPerBlock;
+    const int id = tid + i * kConvertThreads;
+    *block = id / (kTile * per);
+    *row = id / per % kTile;
+    *place = id % per;
+}
+
+template <int FMT, int D, bool SPLIT>
+NVFP4_DEVINL void load_raw(const Call &c, const Item &it, int is_v, int key0, const int (&pages)[2], int tid,
+                           Raw<FMT, D, SPLIT> &raw)
+{
+    using R = kv::Row<FMT, D>;
+    using X = Raw<FMT, D, SPLIT>;
+    constexpr int per = Cfg<FMT, D, SPLIT>::kPerBlock;
+#pragma unroll
+    for (int i = 0; i < X::kMine; ++i) {
+        int row, block, place;
+        chunk_of<FMT, D, SPLIT>(tid, i, &row, &block, &place);
+        raw.codes[i] = make_uint4(0, 0, 0, 0);
+        if constexpr (FMT == NVFP4_KV_NVFP4)
+            raw.scales[i] = 0;
+        const int page = row >= 64 ? pages[1] : pages[0];
+        if (page >= 0) {
+            const int at = (key0 + row) & ((1 << c.pool.page_shift) - 1);
+            const uint8_t *blk = kv::block_ptr(c.pool, page, it.head, is_v);
+            raw.codes[i] = ldg_stream_v4(blk + at * R::kCode + (block * per + place) * 16);
+            if constexpr (FMT == NVFP4_KV_NVFP4)
+                raw.scales[i] = *reinterpret_cast<const uint16_t *>(blk + (R::kCode << c.pool.page_shift) +
+                                                                    at * R::kScale + (block * per + place) * 2);
+        }
+    }
+}
+
+// f16x2 of 2^x, zero below 2^-24.
+NVFP4_DEVINL uint32_t pow2_f16x2(int x)
+{
+    const float f = x < -40 ? 0.f : __uint_as_float((uint32_t)(127 + x) << 23);
+    return f32x2_to_f16x2(f, f);
+}
+
+// Writes a thread's share of a tile as f16; unit(row) is the f16x2 factor of a row.
+template <int FMT, int D, bool SPLIT, class F>
+NVFP4_DEVINL void convert(const Raw<FMT, D, SPLIT> &raw, uint32_t operand, int tid, F &&unit)
+{
+    using X = Raw<FMT, D, SPLIT>;
+#pragma unroll
+    for (int i = 0; i < X::kMine; ++i) {
+        int row, block, place;
+        chunk_of<FMT, D, SPLIT>(tid, i, &row, &block, &place);
+        const uint32_t u = unit(row);
+        const uint32_t w[4] = {raw.codes[i].x, raw.codes[i].y, raw.codes[i].z, raw.codes[i].w};
+        if constexpr (FMT == NVFP4_KV_E4M3) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
+                        : "=r"(o[2 * j]), "=r"(o[2 * j + 1])
+                        : "r"(w[2 * h + j]));
+                sts128(operand_chunk(operand, row, block * 8 + place * 2 + h),
+                       make_uint4(sk::f16x2_mul(o[0], u), sk::f16x2_mul(o[1], u), sk::f16x2_mul(o[2], u),
+                                  sk::f16x2_mul(o[3], u)));
+            }
+        } else {
+            uint32_t s[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                s[h] = sk::f16x2_mul(e4m3x2_to_f16x2((uint16_t)((raw.scales[i] >> (8 * h) & 0xFFu) * 0x101u)), u);
+#pragma unroll
+            for (int h = 0; h < 4; ++h) {
+                uint32_t o[4];
+                sk::e2m1x8_to_f16x2(w[h], o);
+                const uint32_t m = s[h / 2];
+                sts128(operand_chunk(operand, row, block * 8 + place * 4 + h),
+                       make_uint4(sk::f16x2_mul(o[0], m), sk::f16x2_mul(o[1], m), sk::f16x2_mul(o[2], m),
+                                  sk::f16x2_mul(o[3], m)));
+            }
+        }
+    }
+}
+
+// Where a tile lies: what a conversion warp knows of it before its codes are there.
+struct TileRows {
+    int pages[2];             // of a thread's chunks: rows below 64, and from 64 on; -1: none
+    uint32_t k_exps, v_exps;  // of rows 4 lane .. 4 lane + 3 (a byte each; 0: no such key)
+    uint32_t present;         // TileInfo
+};
+
+template <int FMT, int D, bool SPLIT>
+NVFP4_DEVINL void fetch_rows(const Call &c, const Item &it, int key0, int tid, TileRows &f)
+{
+    using R = kv::Row<FMT, D>;
+    const int lane = tid % 32, shift = c.pool.page_shift;
+    const int32_t *const table = c.table + (int64_t)it.b * c.table_width;
+    const auto page_of_row = [&](int row) {
+        const int key = key0 + row;
+        if (key < it.lo || key >= it.hi)
+            return -1;
+        const int page = table[key >> shift];
+        return page >= 0 && page < c.pool.n_pages ? page : -1;
+    };
+    int row, block, place;
+    chunk_of<FMT, D, SPLIT>(tid, 0, &row, &block, &place);
+    f.pages[0] = page_of_row(row);
+    // with four chunks to a block the next one lies 64 rows on, else in the same row
+    f.pages[1] = Cfg<FMT, D, SPLIT>::kPerBlock == 4 ? page_of_row(row + 64) : f.pages[0];
+    // exponents of four rows; pages hold at least 16, but [lo, hi) can cut through the four
+    const int first = key0 + 4 * lane;
+    f.k_exps = f.v_exps = 0;
+    bool there = true;
+    if (first + 3 >= it.lo && first < it.hi) {
+        const int page = table[first >> shift];
+        there = page >= 0 && page < c.pool.n_pages;
+        if (there) {
+            const int at = first & ((1 << shift) - 1);
+            const int64_t exps = ((R::kCode + R::kScale) << shift) + at;
+            f.k_exps = *reinterpret_cast<const uint32_t *>(kv::block_ptr(c.pool, page, it.head, 0) + exps);
+            f.v_exps = *reinterpret_cast<const uint32_t *>(kv::block_ptr(c.pool, page, it.head, 1) + exps);
+            uint32_t keep = 0xFFFFFFFFu;
+            if (first < it.lo)
+                keep = keep << (8 * (it.lo - first));
+            if (first + 4 > it.hi)
+                keep &= 0xFFFFFFFFu >> (8 * (first + 4 - it.hi));
+            f.k_exps &= keep;
+            f.v_exps &= keep;
+        } else if (tid < 32) {
+            kv::report(c.pool.status, kStatusKvAttention);
+        }
+    }
+    // one bit per 4 keys -> per 16 keys (a group of 16 lies in one page)
+    const uint32_t quads = __ballot_sync(0xFFFFFFFFu, there);
+    f.present = 0;
+#pragma unroll
+    for (int g = 0; g < 8; ++g)
+        f.present |= ((quads >> (4 * g) & 15u) == 15u ? 1u : 0u) << g;
+}
+
+// Largest exponent byte of the rows that hold numbers; 127 if there is none.
+NVFP4_DEVINL int largest_exp(uint32_t four)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t e = four >> (8 * j) & 0xFFu;
+        m = max(m, e == kv::kNanRow ? 0u : e);
+    }
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    return m == 0 ? 127 : (int)m;
+}
+
+// The tiles of a CTA's range, one by one.
+template <int RB>
+struct TileCursor {
+    Item it;
+    int64_t item_begin, u, end;
+
+    NVFP4_DEVINL int key0() const { return (it.tile0 + (int)(u - item_begin)) * kTile; }
+    NVFP4_DEVINL bool at_end() const { return u >= end; }
+    NVFP4_DEVINL void step(const Call &c)
+    {
+        if (++u < end && u == item_begin + it.tiles) {
+            item_begin = u;
+            next_item<RB, kTile>(c, &it);
+        }
+    }
+};
+
+// Per tile: K and its exponents, then V, each from the registers that were
+// loaded while the tile before was converted.
+template <int FMT, int D, bool SPLIT>
+NVFP4_DEVINL bool convert_role(const Call &c, const Range &range, const Item &first, int64_t item_begin, Shared *sh,
+                               uint32_t smem, int tid)
+{
+    using C = Cfg<FMT, D, SPLIT>;
+    const int lane = tid % 32;
+    TileCursor<C::kRows> cur{first, item_begin, range.begin, range.end};
+    TileRows now, next;
+    Raw<FMT, D, SPLIT> k, v;
+    fetch_rows<FMT, D, SPLIT>(c, cur.it, cur.key0(), tid, now);
+    load_raw<FMT, D, SPLIT>(c, cur.it, 0, cur.key0(), now.pages, tid, k);
+    load_raw<FMT, D, SPLIT>(c, cur.it, 1, cur.key0(), now.pages, tid, v);
+    const auto exp_of = [&](uint32_t mine, int row) {
+        return __shfl_sync(0xFFFFFFFFu, mine, row >> 2) >> (8 * (row & 3)) & 0xFFu;
+    };
+    for (uint32_t tile = 0;; ++tile) {
+        const uint32_t st = tile % kStages, ph = (tile / kStages) & 1;
+        cur.step(c);
+        const bool more = !cur.at_end();
+        if (more)
+            fetch_rows<FMT, D, SPLIT>(c, cur.it, cur.key0(), tid, next);
+        const int ku = largest_exp(now.k_exps), vu = largest_exp(now.v_exps);
+        bool ok = tile < kStages || tc::mbar_wait(&sh->k_empty[st], ph ^ 1);
+        if (!__all_sync(0xFFFFFFFFu, ok))
+            return false;
+        convert<FMT, D, SPLIT>(k, smem + C::kKAt + st * C::kOperand, tid, [&](int row) {
+            const uint32_t ek = exp_of(now.k_exps, row), ev = exp_of(now.v_exps, row);
+            // a row that is not a number makes its scores NaN, whichever of K and V it is
+            return ek == kv::kNanRow || ev == kv::kNanRow ? 0x7FFF7FFFu : pow2_f16x2((int)ek - ku);
+        });
+        if (tid == 0)
+            sh->info[tile % kInfos] = {kv::exp2_byte(ku), (float)(vu - 127), now.present, 0};
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            tc::mbar_arrive(&sh->k_full[st]);
+        if (more)
+            load_raw<FMT, D, SPLIT>(c, cur.it, 0, cur.key0(), next.pages, tid, k);
+        ok = tile < kStages || tc::mbar_wait(&sh->v_empty[st], ph ^ 1);
+        if (!__all_sync(0xFFFFFFFFu, ok))
+            return false;
+        convert<FMT, D, SPLIT>(v, smem + C::kVAt + st * C::kOperand, tid, [&](int row) {
+            const uint32_t ev = exp_of(now.v_exps, row);
+            return ev == kv::kNanRow ? 0u : pow2_f16x2((int)ev - vu);
+        });
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+            tc::mbar_arrive(&sh->v_full[st]);
+        if (!more)
+            return true;
+        load_raw<FMT, D, SPLIT>(c, cur.it, 1, cur.key0(), next.pages, tid, v);
+        now = next;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// MMA warps
+// ---------------------------------------------------------------------------
+
+template <int FMT, int D, bool SPLIT>
+NVFP4_DEVINL bool mma_role(const Call &c, const Range &range, const Item &first, int64_t item_begin, Shared *sh,
+                           uint32_t smem, uint32_t tmem, int group)
+{
+    using C = Cfg<FMT, D, SPLIT>;
+    constexpr uint32_t score_idesc = tc::idesc_f16kind(128, kTile, 0);
+    constexpr uint32_t out_idesc = tc::idesc_f16kind(128, D, 0) | 1u << 16;  // B transposed
+    const uint32_t scores = tmem + C::kScoreCols + group * kTile, out = tmem + C::kOutCols + group * D;
+    const uint32_t q = smem + C::kQAt + (SPLIT ? 0 : group) * C::kOperand;
+    bool ok = true;
+    uint32_t items = 0, mine = 0;  // segments and tiles of this group so far
+    for_segments<C::kRows>(c, range, first, item_begin, [&](const Item &, int, int n, uint32_t tile, int64_t, int64_t) {
+        if (!has_tile<SPLIT>(group, tile, n))
+            return true;
+        ok = tc::mbar_wait(&sh->q_ready[group], items++ & 1);
+        bool begun = false;
+        for (int i = 0; i < n && ok; ++i, ++tile) {
+            if (!takes<SPLIT>(group, tile))
+                continue;
+            const uint32_t st = tile % kStages, ph = (tile / kStages) & 1;
+            ok = tc::mbar_wait(&sh->k_full[st], ph) && (mine == 0 || tc::mbar_wait(&sh->pv_done[group], (mine - 1) & 1));
+            if (!ok)
+                break;
+            tc::fence_after_sync();
+            const uint32_t k = smem + C::kKAt + st * C::kOperand;
+#pragma unroll
+            for (int d = 0; d < D / 16; ++d) {
+                const uint32_t at = (d / 4) * (128 * 128) + (d % 4) * 32;
+                const uint64_t base = 1ull << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+                tc::mma_bf16_ss(scores, base | ((q + at) & 0x3FFFFu) >> 4, base | ((k + at) & 0x3FFFFu) >> 4, score_idesc,
+                                d > 0);
+            }
+            tc::mma_commit(&sh->s_full[group]);
+            tc::mma_commit(&sh->k_empty[st]);
+            ok = tc::mbar_wait(&sh->v_full[st], ph) && tc::mbar_wait(&sh->p_ready[group], mine & 1);
+            if (!ok)
+                break;
+            tc::fence_after_sync();
+            const uint32_t v = smem + C::kVAt + st * C::kOperand;
+#pragma unroll
+            for (int j = 0; j < kTile / 16; ++j)
+                tc::mma_f16_ts(out, scores + 8 * j, desc_transposed(v + j * 2048), out_idesc, begun || j > 0);
+            tc::mma_commit(&sh->pv_done[group]);
+            tc::mma_commit(&sh->v_empty[st]);
+            begun = true;
+            ++mine;
+        }
+        return ok;
+    });
+    // nothing of this thread's is in flight when it leaves
+    tc::mma_commit(&sh->drain[group]);
+    return tc::mbar_wait(&sh->drain[group], 0) && ok;
+}
+
+// ---------------------------------------------------------------------------
+// Softmax warps
+// ---------------------------------------------------------------------------
+
+// Bits j of a word for keys first + j that lie in [lo, hi).
+NVFP4_DEVINL uint32_t range_bits(int first, int lo, int hi)
+{
+    const int a = max(lo - first, 0), b = min(hi - first, 32);
+    return a >= b ? 0u : (0xFFFFFFFFu << a) & (0xFFFFFFFFu >> (32 - b));
+}
+
+// Keys first .. first + 31 that a row sees.
+NVFP4_DEVINL uint32_t seen_bits(int first, int lo, int hi, bool tree, uint64_t word, int past)
+{
+    uint32_t m = range_bits(first, lo, hi);
+    if (tree) {
+        const int o = first - past;  // of key `first` among the new tokens
+        uint32_t t;
+        if (o >= 64)
+            t = 0;
+        else if (o >= 0)
+            t = (uint32_t)(word >> o);
+        else
+            t = o <= -32 ? 0xFFFFFFFFu : (uint32_t)(word << -o) | ((1u << -o) - 1);
+        m &= t;
+    }
+    return m;
+}
+
+template <int FMT, int D, bool SPLIT>
+NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, const Item &first, int64_t item_begin, Shared *sh,
+                               uint32_t smem, uint32_t tmem, uint8_t *workspace, int tid)
+{
+    using C = Cfg<FMT, D, SPLIT>;
+    constexpr int kBar = 1, kAll = 32 * kSoftmaxWarps;
+    const int group = tid / 128, r = tid % 128;       // row of the row tile, and lane of tensor memory
+    const int warp_lane = (r / 32) * 32;
+    const uint32_t lanes = (uint32_t)warp_lane << 16;
+    const uint32_t scores = tmem + C::kScoreCols + group * kTile + lanes;
+    const uint32_t out = tmem + C::kOutCols + group * D + lanes;
+    uint32_t *const counters = reinterpret_cast<uint32_t *>(workspace + kCounterOffset);
+    float *const partials = reinterpret_cast<float *>(workspace + kPartialOffset);
+    bool ok = true;
+    uint32_t mine = 0;
+
+    for_segments<C::kRows>(c, range, first, item_begin, [&](const Item &it, int tile0, int n, uint32_t tile,
+                                                            int64_t begin, int64_t end) {
+        const int row = (SPLIT ? 0 : group * kRowTile) + r;  // row of the item
+        const bool live = row < it.rows;
+        const int tok = live ? (it.row0 + row) / c.group : 0;
+        const int hq = it.head * c.group + (live ? (it.row0 + row) % c.group : 0);
+        const int64_t q_row = it.seq.q_begin + tok;
+        int lo = 0, hi = 0;
+        uint64_t word = 0;
+        if (live) {
+            key_range(c, it.seq, tok, &lo, &hi);
+            if (c.tree)
+                word = c.tree[q_row];
+        }
+        // Q to f16, times a power of two that puts its largest element at 2^14 (and the scale's sign)
+        float factor = 0.f;
+        if (!SPLIT || group == 0) {
+            const uint32_t q_at = smem + C::kQAt + (SPLIT ? 0 : group) * C::kOperand;
+            const uint4 *src = reinterpret_cast<const uint4 *>(c.q + q_row * c.q_ld + (int64_t)hq * D);
+            uint32_t m2 = 0;
+            if (live) {
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const uint4 x = src[i];
+                    m2 = __vmaxu2(__vmaxu2(m2, x.x & 0x7FFF7FFFu), x.y & 0x7FFF7FFFu);
+                    m2 = __vmaxu2(__vmaxu2(m2, x.z & 0x7FFF7FFFu), x.w & 0x7FFF7FFFu);
+                }
+            }
+            const int e = max((int)(max(m2 & 0xFFFFu, m2 >> 16) >> 7), 15);
+            const float up = (e == 255 ? NAN : __uint_as_float((uint32_t)(268 - e) << 23)) * (c.scale_log2 < 0 ? -1.f : 1.f);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                const uint4 x = live ? src[i] : make_uint4(0, 0, 0, 0);
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint32_t h[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    h[j] = f32x2_to_f16x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xFFFF0000u) * up);
+                sts128(operand_chunk(q_at, r, i), make_uint4(h[0], h[1], h[2], h[3]));
+            }
+            factor = fabsf(c.scale_log2) * __uint_as_float((uint32_t)(e - 14) << 23);
+            if (SPLIT)
+                sh->stats[0][r].x = factor;
+            tc::fence_proxy_async_smem();
+            // a group waits once for each segment in which it has a tile
+            for (int g = SPLIT ? 0 : group; g <= (SPLIT ? 1 : group); ++g) {
+                if (has_tile<SPLIT>(g, tile, n))
+                    tc::mbar_arrive(&sh->q_ready[g]);
+            }
+        }
+        if (SPLIT) {
+            tc::named_bar_sync(kBar, kAll);
+            factor = sh->stats[0][r].x;
+        }
+
+        const uint32_t tile0_index = tile;
+        float top = -INFINITY, sum = 0.f;
+        bool begun = false;
+        for (int i = 0; i < n && ok; ++i, ++tile) {
+            if (!takes<SPLIT>(group, tile))
+                continue;
+            const int key0 = (tile0 + i) * kTile;
+            ok = tc::mbar_wait(&sh->s_full[group], mine & 1);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok)
+                break;
+            tc::fence_after_sync();
+            const TileInfo info = sh->info[tile % kInfos];
+            const float f = factor * info.k_unit;
+            const bool whole = __all_sync(0xFFFFFFFFu, key0 >= lo && key0 + kTile <= (c.tree ? min(hi, it.seq.past) : hi) &&
+                                                           info.present == 0xFFu);
+            uint32_t s[32];
+            // largest score
+            float m = -INFINITY;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                tc::tmem_ld_32x32b_x32(scores + 32 * q, s);
+                tc::tmem_ld_wait();
+                uint32_t see = 0xFFFFFFFFu;
+                if (!whole) {
+                    see = seen_bits(key0 + 32 * q, lo, hi, c.tree != nullptr, word, it.seq.past);
+                    see &= (info.present >> (2 * q) & 1 ? 0x0000FFFFu : 0u) | (info.present >> (2 * q + 1) & 1 ? 0xFFFF0000u : 0u);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        m = see >> j & 1 ? fmaxf(m, __uint_as_float(s[j])) : m;
+                } else {
+                    float m1 = __uint_as_float(s[0]), m2 = __uint_as_float(s[1]);
+#pragma unroll
+                    for (int j = 2; j < 32; j += 2) {
+                        m1 = fmaxf(m1, __uint_as_float(s[j]));
+                        m2 = fmaxf(m2, __uint_as_float(s[j + 1]));
+                    }
+                    m = fmaxf(m, fmaxf(m1, m2));
+                }
+            }
+            const float z = m == -INFINITY ? -INFINITY : fmaf(m, f, info.v_exp);
+            const bool over = z > top + kSlack;
+            if (__any_sync(0xFFFFFFFFu, over)) {
+                const float next = over ? z - kHeadroom : top;
+                const float shrink = over ? ex2(top - next) : 1.f;
+                top = next;
+                sum *= shrink;
+                if (begun) {
+#pragma unroll 1
+                    for (int q = 0; q < D / 32; ++q) {
+                        tc::tmem_ld_32x32b_x32(out + 32 * q, s);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            s[j] = __float_as_uint(__uint_as_float(s[j]) * shrink);
+                        tc::tmem_st_32x32b_x32(out + 32 * q, s);
+                    }
+                }
+            }
+            // weights
+            const float add = info.v_exp - (top == -INFINITY ? 0.f : top);
+            float l[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                tc::tmem_ld_32x32b_x32(scores + 32 * q, s);
+                tc::tmem_ld_wait();
+                uint32_t p[16];
+                if (whole) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float a = ex2(fmaf(__uint_as_float(s[2 * j]), f, add));
+                        const float b = ex2(fmaf(__uint_as_float(s[2 * j + 1]), f, add));
+                        l[2 * (j & 1)] += a;
+                        l[2 * (j & 1) + 1] += b;
+                        p[j] = f32x2_to_f16x2(a, b);
+                    }
+                } else {
+                    uint32_t see = seen_bits(key0 + 32 * q, lo, hi, c.tree != nullptr, word, it.seq.past);
+                    see &= (info.present >> (2 * q) & 1 ? 0x0000FFFFu : 0u) | (info.present >> (2 * q + 1) & 1 ? 0xFFFF0000u : 0u);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float a = see >> (2 * j) & 1 ? ex2(fmaf(__uint_as_float(s[2 * j]), f, add)) : 0.f;
+                        const float b = see >> (2 * j + 1) & 1 ? ex2(fmaf(__uint_as_float(s[2 * j + 1]), f, add)) : 0.f;
+                        l[2 * (j & 1)] += a;
+                        l[2 * (j & 1) + 1] += b;
+                        p[j] = f32x2_to_f16x2(a, b);
+                    }
+                }
+                tc::tmem_st_32x32b_x16(scores + 16 * q, p);
+            }
+            tc::tmem_st_wait();
+            sum = fmaf((l[0] + l[1]) + (l[2] + l[3]), ex2(-info.v_exp) * kSumUnit, sum);
+            tc::fence_before_sync();
+            tc::mbar_arrive(&sh->p_ready[group]);
+            begun = true;
+            ++mine;
+        }
+        if (ok && begun)
+            ok = tc::mbar_wait(&sh->pv_done[group], (mine - 1) & 1);
+        ok = tc::bar_and(kBar, kAll, ok);
+        if (!ok)
+            return false;
+        tc::fence_after_sync();
+
+        // The row's result: with SPLIT, the two groups' joined, each group taking half of the elements.
+        constexpr int kCols = SPLIT ? D / 2 : D;
+        const int col0 = SPLIT ? group * kCols : 0;
+        float w_other = 0.f, w_mine = 1.f;
+        if (SPLIT) {
+            sh->stats[group][r] = make_float2(begun ? top : -INFINITY, begun ? sum : 0.f);
+            tc::named_bar_sync(kBar, kAll);
+            const float2 a = sh->stats[0][r], b = sh->stats[1][r];
+            top = fmaxf(a.x, b.x);
+            // groups without a tile have nothing in tensor memory; 0 * NaN stays NaN in the others
+            const float wa = a.x == -INFINITY ? 0.f : ex2(a.x - top), wb = b.x == -INFINITY ? 0.f : ex2(b.x - top);
+            sum = fmaf(wa, a.y, wb * b.y);
+            w_mine = wa;
+            w_other = wb;
+        }
+        const bool has0 = !SPLIT || has_tile<SPLIT>(0, tile0_index, n), has1 = SPLIT && has_tile<SPLIT>(1, tile0_index, n);
+        const uint32_t out0 = SPLIT ? tmem + C::kOutCols + lanes : out, out1 = tmem + C::kOutCols + D + lanes;
+        const auto result = [&](int q, float (&x)[32]) {  // elements col0 + 32 q ..
+            uint32_t s[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                x[j] = 0.f;
+            if (has0) {
+                tc::tmem_ld_32x32b_x32(out0 + col0 + 32 * q, s);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    x[j] = __uint_as_float(s[j]) * w_mine;
+            }
+            if (has1) {
+                tc::tmem_ld_32x32b_x32(out1 + col0 + 32 * q, s);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    x[j] = fmaf(__uint_as_float(s[j]), w_other, x[j]);
+            }
+        };
+        const auto store = [&](int q, const float (&x)[32], float l) {
+            if (!live)
+                return;
+            const float inv = l == 0.f ? 0.f : kSumUnit / l;
+            uint16_t *dst = static_cast<uint16_t *>(c.out) + q_row * c.out_ld + (int64_t)hq * D + col0 + 32 * q;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[k] = f32x2_to_bf16x2(x[8 * j + 2 * k] * inv, x[8 * j + 2 * k + 1] * inv);
+                reinterpret_cast<uint4 *>(dst)[j] = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+        };
+        if (begin >= range.begin && end <= range.end) {
+            for (int q = 0; q < kCols / 32; ++q) {
+                float x[32];
+                result(q, x);
+                store(q, x, sum);
+            }
+        } else {
+            // partial result: [element / 4][row][4], then [row] (largest, sum)
+            const int first_cta = range_owner(range.total, range.ctas, begin);
+            const int last_cta = range_owner(range.total, range.ctas, end - 1);
+            float *slot = partials + ((int64_t)blockIdx.x * 2 + (begin < range.begin ? 0 : 1)) * C::kSlotFloats;
+            for (int q = 0; q < kCols / 32; ++q) {
+                float x[32];
+                result(q, x);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    reinterpret_cast<float4 *>(slot)[(col0 / 4 + 8 * q + j) * C::kRows + row] =
+                        make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+            }
+            if (!SPLIT || group == 0)
+                reinterpret_cast<float2 *>(slot + C::kRows * D)[row] = make_float2(top, sum);
+            __threadfence();
+            tc::named_bar_sync(kBar, kAll);
+            if (tid == 0) {
+                const bool done = atomicAdd(counters + first_cta, 1u) == (uint32_t)(last_cta - first_cta);
+                if (done)
+                    counters[first_cta] = 0;
+                sh->last = done;
+                __threadfence();
+            }
+            tc::named_bar_sync(kBar, kAll);
+            if (sh->last) {
+                const int count = last_cta - first_cta + 1;
+                const float *const from = partials + (int64_t)first_cta * 2 * C::kSlotFloats;
+                const auto slot_of = [&](int i) { return from + (int64_t)(i == 0 ? 1 : 2 * i) * C::kSlotFloats; };
+                float m = -INFINITY;
+                for (int i = 0; i < count; ++i)
+                    m = fmaxf(m, __ldcg(reinterpret_cast<const float2 *>(slot_of(i) + C::kRows * D) + row).x);
+                float l = 0.f;
+                for (int i = 0; i < count; ++i) {
+                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(slot_of(i) + C::kRows * D) + row);
+                    l = fmaf(ml.x == -INFINITY ? 0.f : ex2(ml.x - m), ml.y, l);
+                }
+                for (int q = 0; q < kCols / 32; ++q) {
+                    float x[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        x[j] = 0.f;
+#pragma unroll 1
+                    for (int i = 0; i < count; ++i) {
+                        const float tw = __ldcg(reinterpret_cast<const float2 *>(slot_of(i) + C::kRows * D) + row).x;
+                        const float w = tw == -INFINITY ? 0.f : ex2(tw - m);
+                        const float4 *v = reinterpret_cast<const float4 *>(slot_of(i)) + (col0 / 4 + 8 * q) * C::kRows + row;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 y = __ldcg(v + j * C::kRows);
+                            x[4 * j] = fmaf(w, y.x, x[4 * j]);
+                            x[4 * j + 1] = fmaf(w, y.y, x[4 * j + 1]);
+                            x[4 * j + 2] = fmaf(w, y.z, x[4 * j + 2]);
+                            x[4 * j + 3] = fmaf(w, y.w, x[4 * j + 3]);
+                        }
+                    }
+                    store(q, x, l);
+                }
+            }
+        }
+        tc::fence_before_sync();
+        tc::named_bar_sync(kBar, kAll);  // both groups are done with tensor memory, Q and the statistics
+        return true;
+    });
+    return ok;
+}
+
+template <int FMT, int D, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *workspace)
+{
+    using C = Cfg<FMT, D, SPLIT>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    Shared *const sh = reinterpret_cast<Shared *>(smem_raw + C::kBarAt);
+    static_assert(sizeof(Shared) <= C::kSmem - C::kBarAt, "barriers");
+    const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid / 32, 0);
+
+    Range range;
+    Item item;
+    int64_t item_begin;
+    if (!find_range<C::kRows, kTile, kThreads>(c, sh->scratch, &range, &item, &item_begin))
+        return;
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(&sh->k_full[i], kConvertWarps);
+            tc::mbar_init(&sh->v_full[i], kConvertWarps);
+            tc::mbar_init(&sh->k_empty[i], SPLIT ? 1 : 2);
+            tc::mbar_init(&sh->v_empty[i], SPLIT ? 1 : 2);
+        }
+        for (int g = 0; g < 2; ++g) {
+            tc::mbar_init(&sh->q_ready[g], kRowTile);
+            tc::mbar_init(&sh->s_full[g], 1);
+            tc::mbar_init(&sh->p_ready[g], kRowTile);
+            tc::mbar_init(&sh->pv_done[g], 1);
+            tc::mbar_init(&sh->drain[g], 1);
+        }
+        tc::fence_mbar_init();
+    }
+    if (warp == kSoftmaxWarps + kConvertWarps + 2)
+        tc::tmem_alloc(&sh->tmem, 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t smem = tc::smem_addr(smem_raw), tmem = sh->tmem;
+
+    bool ok = true;
+    uint32_t code = 0;
+    if (warp < kSoftmaxWarps) {
+        ok = softmax_role<FMT, D, SPLIT>(c, range, item, item_begin, sh, smem, tmem, workspace, tid);
+        code = kTimeoutSoftmax;
+    } else if (warp < kSoftmaxWarps + kConvertWarps) {
+        ok = convert_role<FMT, D, SPLIT>(c, range, item, item_begin, sh, smem, tid - 32 * kSoftmaxWarps);
+        code = kTimeoutConvert;
+    } else if (warp < kSoftmaxWarps + kConvertWarps + 2) {
+        if (elect_one()) {
+            ok = mma_role<FMT, D, SPLIT>(c, range, item, item_begin, sh, smem, tmem, warp - kSoftmaxWarps - kConvertWarps);
+            code = kTimeoutMma;
+        }
+        __syncwarp();
+    }
+    if (!ok)
+        kv::report(c.pool.status, code);
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == kSoftmaxWarps + kConvertWarps + 2)
+        tc::tmem_dealloc(tmem, 512);
+}
+
+template <int FMT, int D, bool SPLIT>
+cudaError_t launch(const Call &c, uint8_t *workspace, int num_sms, cudaStream_t stream)
+{
+    using C = Cfg<FMT, D, SPLIT>;
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t results[kMaxDevices];
+    const auto kernel = chunk_kernel<FMT, D, SPLIT>;
+    const cudaError_t e = once_per_device(once, results, [kernel] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    });
+    if (e != cudaSuccess)
+        return e;
+    kernel<<<num_sms < kMaxChunkCtas ? num_sms : kMaxChunkCtas, kThreads, C::kSmem, stream>>>(c, workspace);
+    return cudaGetLastError();
+}
+
+template <int FMT>
+cudaError_t launch_format(const Call &c, int head_dim, void *workspace, int num_sms, cudaStream_t stream)
+{
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    if ((int64_t)c.max_q_len * c.group <= kRowTile)
+        return head_dim == 64 ? launch<FMT, 64, true>(c, ws, num_sms, stream) : launch<FMT, 128, true>(c, ws, num_sms, stream);
+    return head_dim == 64 ? launch<FMT, 64, false>(c, ws, num_sms, stream) : launch<FMT, 128, false>(c, ws, num_sms, stream);
+}
+
+}  // namespace chunk
+}  // namespace attn
+}  // namespace nvfp4

@@ -31,6 +31,7 @@ constexpr size_t kPartialOffset = kCounterOffset + kMaxCtas * sizeof(uint32_t);
 // Rows of an item of the decode kernel, and the CTAs that it may have at most
 // (two on an SM while a thread's accumulators leave room for them).
 constexpr int decode_block(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+constexpr int kMaxChunkCtas = kMaxCtas / 2;  // of the chunk kernel, one on an SM
 constexpr int decode_max_ctas(int block) { return block <= 16 ? kMaxCtas : kMaxCtas / 2; }
 
 struct Item {

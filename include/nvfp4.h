@@ -439,10 +439,13 @@ int nvfp4_kv_read(const nvfp4_kv_cache *cache, uint16_t *k, int64_t k_ld, uint16
  * Numerics: q . k_j is exact in its products (q scaled by a power of two to
  * f16, K's codes in f16) with fp32 accumulation; softmax statistics are fp32
  * (2^x by the hardware's approximation, relative error about 2^-22); the weights
- * enter the second product in f16, rounded to nearest (relative error at most
- * 2^-11 each), with fp32 accumulation:
+ * enter the second product rounded to nearest, with a relative error of at most
+ * 2^-11 each (f16), and fp32 accumulation:
  * |out - exact| <= (2^-10 + 2^-15 * S) * sum_j softmax_j |v_j|, plus the rounding
  * of out, with S = max_j |scale| * sum_d |q_d k_jd| (the fp32 sums of scores).
+ * For bf16 outputs f16 loses what is below 2^-32 of a row's largest weight:
+ * n * 2^-28 * max |V| over the n keys comes on top.  For fp32 outputs the weights
+ * keep fp32's range (as two bf16 numbers each).
  *
  * Requirements: q, out 16-byte aligned; q_ld and out_ld multiples of 8, at
  * least n_q_heads * head_dim; n_q_heads a multiple of n_kv_heads; tree only
@@ -547,7 +550,7 @@ int nvfp4_noalloc_selftest_wait_timeout(nvfp4_stream_t stream);
  * whose bounded pipeline wait runs out (2 s) stores a nonzero code there and
  * returns: 1..8 from the prefill kernel, 10 from its split-mode reduction
  * (a contributor or tile outside the plan, which the host's plan rules out),
- * 11..25 from the skinny kernel, 127 from nvfp4_selftest_wait_timeout.  No
+ * 11..25 from the skinny kernel, 51..53 from nvfp4_paged_attention, 127 from nvfp4_selftest_wait_timeout.  No
  * kernel clears the word, so it reports
  * any failure since it was last cleared; it starts clean when the workspace is
  * zero-filled (required for the skinny calls; do it for a prefill workspace
