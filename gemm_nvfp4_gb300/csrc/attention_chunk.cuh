@@ -10,11 +10,15 @@
 //   warps 0-3, 4-7  softmax of row tile 0 and 1: a thread has one row.  Scores
 //                   come from tensor memory and the weights P go back there as
 //                   the f16 A operand of the second product, over the scores.
-//   warps 8-15      codes to f16: a tile of 128 keys is read from the pages into
-//                   registers one tile ahead, converted, and written to shared
-//                   memory in the layout of the MMA's B operands (K with the
-//                   head dimension contiguous; V likewise, read transposed).
-//   warps 16, 17    MMA issue for row tile 0 and 1: S = Q K^T, O += P V.
+//   warp 14         bulk copies of a tile's codes, scales and exponents from the
+//                   pages to shared memory, ahead of their conversion.
+//   warps 8-11      codes to f16, from there to the layout of the MMA's B operands
+//                   (K with the head dimension contiguous; V likewise, read
+//                   transposed).
+//   warps 12, 13    MMA issue for row tile 0 and 1: S = Q K^T, O += P V.
+//
+// Registers go where the scores are: a softmax thread keeps its row's 128 scores
+// and reads tensor memory once per tile.
 //
 // SPLIT: when a sequence has at most 128 rows, both softmax groups take the same
 // row tile, one the even and the other the odd key tiles, and their results
@@ -39,16 +43,20 @@ namespace chunk {
 
 constexpr int kTile = 128;                      // keys of a tile
 constexpr int kRowTile = 128;                   // rows of a row tile
-constexpr int kSoftmaxWarps = 8, kConvertWarps = 8;
+constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
 constexpr int kConvertThreads = 32 * kConvertWarps;
-constexpr int kThreads = 32 * (kSoftmaxWarps + kConvertWarps + 4);  // whole warpgroups; warps 18, 19 idle
+constexpr int kThreads = 32 * (kSoftmaxWarps + kConvertWarps + 4);  // whole warpgroups; warp 15 idles
+// Registers of a thread by role: what the launch gives every thread, shared out anew.
+constexpr int kSoftmaxRegs = 176, kConvertRegs = 96, kMmaRegs = 56, kLaunchRegs = 128;
+static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kConvertWarps * kConvertRegs + 4 * kMmaRegs) <= kThreads * kLaunchRegs,
+              "setmaxnreg would wait for registers that nobody gives back");
 constexpr int kStages = 2;
 constexpr int kInfos = 4;
 constexpr float kHeadroom = 7.f, kSlack = 15.f;
 constexpr float kSumUnit = 0x1p-32f;
 
 // Codes of the status word (waits that ran out).
-enum : uint32_t { kTimeoutSoftmax = 51, kTimeoutConvert = 52, kTimeoutMma = 53 };
+enum : uint32_t { kTimeoutSoftmax = 51, kTimeoutConvert = 52, kTimeoutMma = 53, kTimeoutLoad = 54 };
 
 template <int FMT, int D, bool SPLIT>
 struct Cfg {
@@ -56,14 +64,20 @@ struct Cfg {
     static constexpr int kRows = SPLIT ? kRowTile : 2 * kRowTile;
     static constexpr int kOperand = 128 * D * 2;  // Q, K or V tile in f16
     static constexpr int kQAt = 0, kKAt = (SPLIT ? 1 : 2) * kOperand, kVAt = kKAt + kStages * kOperand;
-    static constexpr int kBarAt = kVAt + kStages * kOperand;
-    static constexpr int kSmem = kBarAt + 4096;
+    // a tile's bytes as they lie in the pages: K's codes, scales, exponents and V's exponents; V's codes and scales
+    static constexpr int kRawRows = kTile * (R::kCode + R::kScale);
+    static constexpr int kRawKAt = kVAt + kStages * kOperand, kRawVAt = kRawKAt + kRawRows + 2 * kTile;
+    static constexpr int kBarAt = kRawVAt + kRawRows;
+    static constexpr int kSmem = kBarAt + 2816;
     static constexpr int kSlotFloats = kRows * (D + 2);
     // tensor memory columns
     static constexpr int kScoreCols = 0, kOutCols = 2 * kTile;
-    // 16-byte chunks of codes: of a 64-element column block of a row, of a thread per tile
+    // 16-byte chunks of codes: of a 64-element column block of a row, of a thread per tile of K or V.
+    // A thread's chunks lie in kPerBlock rows, kRowStep apart.
     static constexpr int kPerBlock = FMT == NVFP4_KV_E4M3 ? 4 : 2;
     static constexpr int kMine = D / 64 * kTile * kPerBlock / kConvertThreads;
+    static constexpr int kRowStep = kConvertThreads / kPerBlock;
+    static_assert(kTile / kRowStep == kPerBlock, "rows of a thread");
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -75,10 +89,18 @@ struct TileInfo {
     uint32_t pad;
 };
 
+// Where the tile in the raw buffers lies.
+struct RawInfo {
+    int key0, lo, hi;
+    uint32_t present;
+};
+
 struct Shared {
+    uint64_t raw_k_full, raw_k_empty, raw_v_full, raw_v_empty;
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2], drain[2];
     TileInfo info[kInfos];
+    RawInfo raw;
     uint32_t tmem, last;
     int64_t scratch[kThreads / 32 + 4];
     float2 stats[2][kRowTile];  // largest and sum of a row, by softmax group
@@ -114,6 +136,54 @@ NVFP4_DEVINL uint32_t f32x2_to_bf16x2(float lo, float hi)
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+template <int N>
+NVFP4_DEVINL void take_regs()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+NVFP4_DEVINL void give_regs()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// Pairs of fp32 in one instruction.
+NVFP4_DEVINL uint64_t pack2(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+NVFP4_DEVINL float2 unpack2(uint64_t v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+NVFP4_DEVINL uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+NVFP4_DEVINL uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Holds every later use of loaded registers behind the wait before it.
+NVFP4_DEVINL void settle(uint32_t (&r)[32])
+{
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 
 NVFP4_DEVINL void sts128(uint32_t addr, uint4 v)
@@ -168,175 +238,6 @@ NVFP4_DEVINL void for_segments(const Call &c, const Range &range, Item it, int64
     }
 }
 
-// ---------------------------------------------------------------------------
-// Conversion warps
-// ---------------------------------------------------------------------------
-
-// A thread's share of one tile of K or V as it lies in the pages.
-template <int FMT, int D, bool SPLIT>
-struct Raw {
-    static constexpr int kMine = Cfg<FMT, D, SPLIT>::kMine;
-    uint4 codes[kMine];
-    uint32_t scales[FMT == NVFP4_KV_NVFP4 ? kMine : 1];
-};
-
-// Row and 64-element column block of a thread's i-th chunk, and the chunk's
-// place in the block: neighbouring lanes take the chunks of one block of a row,
-// then the next row, so that their stores fall on different banks.
-template <int FMT, int D, bool SPLIT>
-NVFP4_DEVINL void chunk_of(int tid, int i, int *row, int *block, int *place)
-{
-    constexpr int per = Cfg<FMT, D, SPLIT>::kPerBlock;
-    const int id = tid + i * kConvertThreads;
-    *block = id / (kTile * per);
-    *row = id / per % kTile;
-    *place = id % per;
-}
-
-template <int FMT, int D, bool SPLIT>
-NVFP4_DEVINL void load_raw(const Call &c, const Item &it, int is_v, int key0, const int (&pages)[2], int tid,
-                           Raw<FMT, D, SPLIT> &raw)
-{
-    using R = kv::Row<FMT, D>;
-    using X = Raw<FMT, D, SPLIT>;
-    constexpr int per = Cfg<FMT, D, SPLIT>::kPerBlock;
-#pragma unroll
-    for (int i = 0; i < X::kMine; ++i) {
-        int row, block, place;
-        chunk_of<FMT, D, SPLIT>(tid, i, &row, &block, &place);
-        raw.codes[i] = make_uint4(0, 0, 0, 0);
-        if constexpr (FMT == NVFP4_KV_NVFP4)
-            raw.scales[i] = 0;
-        const int page = row >= 64 ? pages[1] : pages[0];
-        if (page >= 0) {
-            const int at = (key0 + row) & ((1 << c.pool.page_shift) - 1);
-            const uint8_t *blk = kv::block_ptr(c.pool, page, it.head, is_v);
-            raw.codes[i] = ldg_stream_v4(blk + at * R::kCode + (block * per + place) * 16);
-            if constexpr (FMT == NVFP4_KV_NVFP4)
-                raw.scales[i] = *reinterpret_cast<const uint16_t *>(blk + (R::kCode << c.pool.page_shift) +
-                                                                    at * R::kScale + (block * per + place) * 2);
-        }
-    }
-}
-
-// f16x2 of 2^x, zero below 2^-24.
-NVFP4_DEVINL uint32_t pow2_f16x2(int x)
-{
-    const float f = x < -40 ? 0.f : __uint_as_float((uint32_t)(127 + x) << 23);
-    return f32x2_to_f16x2(f, f);
-}
-
-// Writes a thread's share of a tile as f16; unit(row) is the f16x2 factor of a row.
-template <int FMT, int D, bool SPLIT, class F>
-NVFP4_DEVINL void convert(const Raw<FMT, D, SPLIT> &raw, uint32_t operand, int tid, F &&unit)
-{
-    using X = Raw<FMT, D, SPLIT>;
-#pragma unroll
-    for (int i = 0; i < X::kMine; ++i) {
-        int row, block, place;
-        chunk_of<FMT, D, SPLIT>(tid, i, &row, &block, &place);
-        const uint32_t u = unit(row);
-        const uint32_t w[4] = {raw.codes[i].x, raw.codes[i].y, raw.codes[i].z, raw.codes[i].w};
-        if constexpr (FMT == NVFP4_KV_E4M3) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t o[4];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
-                        : "=r"(o[2 * j]), "=r"(o[2 * j + 1])
-                        : "r"(w[2 * h + j]));
-                sts128(operand_chunk(operand, row, block * 8 + place * 2 + h),
-                       make_uint4(sk::f16x2_mul(o[0], u), sk::f16x2_mul(o[1], u), sk::f16x2_mul(o[2], u),
-                                  sk::f16x2_mul(o[3], u)));
-            }
-        } else {
-            uint32_t s[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                s[h] = sk::f16x2_mul(e4m3x2_to_f16x2((uint16_t)((raw.scales[i] >> (8 * h) & 0xFFu) * 0x101u)), u);
-#pragma unroll
-            for (int h = 0; h < 4; ++h) {
-                uint32_t o[4];
-                sk::e2m1x8_to_f16x2(w[h], o);
-                const uint32_t m = s[h / 2];
-                sts128(operand_chunk(operand, row, block * 8 + place * 4 + h),
-                       make_uint4(sk::f16x2_mul(o[0], m), sk::f16x2_mul(o[1], m), sk::f16x2_mul(o[2], m),
-                                  sk::f16x2_mul(o[3], m)));
-            }
-        }
-    }
-}
-
-// Where a tile lies: what a conversion warp knows of it before its codes are there.
-struct TileRows {
-    int pages[2];             // of a thread's chunks: rows below 64, and from 64 on; -1: none
-    uint32_t k_exps, v_exps;  // of rows 4 lane .. 4 lane + 3 (a byte each; 0: no such key)
-    uint32_t present;         // TileInfo
-};
-
-template <int FMT, int D, bool SPLIT>
-NVFP4_DEVINL void fetch_rows(const Call &c, const Item &it, int key0, int tid, TileRows &f)
-{
-    using R = kv::Row<FMT, D>;
-    const int lane = tid % 32, shift = c.pool.page_shift;
-    const int32_t *const table = c.table + (int64_t)it.b * c.table_width;
-    const auto page_of_row = [&](int row) {
-        const int key = key0 + row;
-        if (key < it.lo || key >= it.hi)
-            return -1;
-        const int page = table[key >> shift];
-        return page >= 0 && page < c.pool.n_pages ? page : -1;
-    };
-    int row, block, place;
-    chunk_of<FMT, D, SPLIT>(tid, 0, &row, &block, &place);
-    f.pages[0] = page_of_row(row);
-    // with four chunks to a block the next one lies 64 rows on, else in the same row
-    f.pages[1] = Cfg<FMT, D, SPLIT>::kPerBlock == 4 ? page_of_row(row + 64) : f.pages[0];
-    // exponents of four rows; pages hold at least 16, but [lo, hi) can cut through the four
-    const int first = key0 + 4 * lane;
-    f.k_exps = f.v_exps = 0;
-    bool there = true;
-    if (first + 3 >= it.lo && first < it.hi) {
-        const int page = table[first >> shift];
-        there = page >= 0 && page < c.pool.n_pages;
-        if (there) {
-            const int at = first & ((1 << shift) - 1);
-            const int64_t exps = ((R::kCode + R::kScale) << shift) + at;
-            f.k_exps = *reinterpret_cast<const uint32_t *>(kv::block_ptr(c.pool, page, it.head, 0) + exps);
-            f.v_exps = *reinterpret_cast<const uint32_t *>(kv::block_ptr(c.pool, page, it.head, 1) + exps);
-            uint32_t keep = 0xFFFFFFFFu;
-            if (first < it.lo)
-                keep = keep << (8 * (it.lo - first));
-            if (first + 4 > it.hi)
-                keep &= 0xFFFFFFFFu >> (8 * (first + 4 - it.hi));
-            f.k_exps &= keep;
-            f.v_exps &= keep;
-        } else if (tid < 32) {
-            kv::report(c.pool.status, kStatusKvAttention);
-        }
-    }
-    // one bit per 4 keys -> per 16 keys (a group of 16 lies in one page)
-    const uint32_t quads = __ballot_sync(0xFFFFFFFFu, there);
-    f.present = 0;
-#pragma unroll
-    for (int g = 0; g < 8; ++g)
-        f.present |= ((quads >> (4 * g) & 15u) == 15u ? 1u : 0u) << g;
-}
-
-// Largest exponent byte of the rows that hold numbers; 127 if there is none.
-NVFP4_DEVINL int largest_exp(uint32_t four)
-{
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t e = four >> (8 * j) & 0xFFu;
-        m = max(m, e == kv::kNanRow ? 0u : e);
-    }
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
-    return m == 0 ? 127 : (int)m;
-}
-
 // The tiles of a CTA's range, one by one.
 template <int RB>
 struct TileCursor {
@@ -354,62 +255,248 @@ struct TileCursor {
     }
 };
 
-// Per tile: K and its exponents, then V, each from the registers that were
-// loaded while the tile before was converted.
+// ---------------------------------------------------------------------------
+// Load warp
+// ---------------------------------------------------------------------------
+
+// A tile is cut into runs that lie in one page each (16 keys at least); lane i
+// copies run i.  Runs that no row sees, and pages that are not there, are not
+// copied.
 template <int FMT, int D, bool SPLIT>
-NVFP4_DEVINL bool convert_role(const Call &c, const Range &range, const Item &first, int64_t item_begin, Shared *sh,
-                               uint32_t smem, int tid)
+NVFP4_DEVINL bool load_role(const Call &c, const Range &range, const Item &first, int64_t item_begin, Shared *sh,
+                            uint32_t smem, int lane)
 {
     using C = Cfg<FMT, D, SPLIT>;
-    const int lane = tid % 32;
+    using R = kv::Row<FMT, D>;
+    const int shift = c.pool.page_shift, run = min(1 << shift, kTile), runs = kTile / run;
     TileCursor<C::kRows> cur{first, item_begin, range.begin, range.end};
-    TileRows now, next;
-    Raw<FMT, D, SPLIT> k, v;
-    fetch_rows<FMT, D, SPLIT>(c, cur.it, cur.key0(), tid, now);
-    load_raw<FMT, D, SPLIT>(c, cur.it, 0, cur.key0(), now.pages, tid, k);
-    load_raw<FMT, D, SPLIT>(c, cur.it, 1, cur.key0(), now.pages, tid, v);
-    const auto exp_of = [&](uint32_t mine, int row) {
-        return __shfl_sync(0xFFFFFFFFu, mine, row >> 2) >> (8 * (row & 3)) & 0xFFu;
+    const uint32_t tiles = (uint32_t)(range.end - range.begin);
+    const auto sees = [&](int key) { return lane < runs && key < cur.it.hi && key + run > cur.it.lo; };
+    const auto look_up = [&](int key) {
+        return sees(key) ? c.table[(int64_t)cur.it.b * c.table_width + (key >> shift)] : -1;
     };
-    for (uint32_t tile = 0;; ++tile) {
-        const uint32_t st = tile % kStages, ph = (tile / kStages) & 1;
+    int page = look_up(cur.key0() + lane * run);
+    const uint32_t k_full = tc::smem_addr(&sh->raw_k_full), v_full = tc::smem_addr(&sh->raw_v_full);
+    bool ok = true;
+    uint32_t tile = 0;
+    for (; tile < tiles; ++tile) {
+        const int key0 = cur.key0(), key = key0 + lane * run, head = cur.it.head;
+        const bool want = sees(key), there = want && page >= 0 && page < c.pool.n_pages;
+        if (want && !there)
+            kv::report(c.pool.status, kStatusKvAttention);
+        const uint32_t missing = __ballot_sync(0xFFFFFFFFu, want && !there);
+        const uint32_t copied = __popc(__ballot_sync(0xFFFFFFFFu, there));
+        RawInfo info{key0, cur.it.lo, cur.it.hi, 0};
+#pragma unroll
+        for (int g = 0; g < kTile / 16; ++g)
+            info.present |= (missing >> (g * 16 / run) & 1 ? 0u : 1u) << g;
+        const uint8_t *const k = kv::block_ptr(c.pool, there ? page : 0, head, 0);
+        const uint8_t *const v = k + c.pool.block_bytes;
+        const int at = key & ((1 << shift) - 1);
+        const int64_t scales = (int64_t)R::kCode << shift, exps = (int64_t)(R::kCode + R::kScale) << shift;
         cur.step(c);
-        const bool more = !cur.at_end();
-        if (more)
-            fetch_rows<FMT, D, SPLIT>(c, cur.it, cur.key0(), tid, next);
-        const int ku = largest_exp(now.k_exps), vu = largest_exp(now.v_exps);
-        bool ok = tile < kStages || tc::mbar_wait(&sh->k_empty[st], ph ^ 1);
-        if (!__all_sync(0xFFFFFFFFu, ok))
-            return false;
-        convert<FMT, D, SPLIT>(k, smem + C::kKAt + st * C::kOperand, tid, [&](int row) {
-            const uint32_t ek = exp_of(now.k_exps, row), ev = exp_of(now.v_exps, row);
-            // a row that is not a number makes its scores NaN, whichever of K and V it is
-            return ek == kv::kNanRow || ev == kv::kNanRow ? 0x7FFF7FFFu : pow2_f16x2((int)ek - ku);
-        });
-        if (tid == 0)
-            sh->info[tile % kInfos] = {kv::exp2_byte(ku), (float)(vu - 127), now.present, 0};
-        tc::fence_proxy_async_smem();
+        if (!cur.at_end())
+            page = look_up(cur.key0() + lane * run);
+
+        ok = tile == 0 || tc::mbar_wait(&sh->raw_k_empty, (tile - 1) & 1);
+        if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
+            break;
+        if (lane == 0) {
+            sh->raw = info;
+            tc::mbar_arrive_expect_tx(&sh->raw_k_full, copied * run * (R::kCode + R::kScale + 2));
+        }
         __syncwarp();
+        if (there) {
+            const uint32_t dst = smem + C::kRawKAt;
+            tc::bulk_load_a(dst + lane * run * R::kCode, k + at * R::kCode, run * R::kCode, k_full);
+            if (R::kScale)
+                tc::bulk_load_a(dst + kTile * R::kCode + lane * run * R::kScale, k + scales + at * R::kScale,
+                                run * R::kScale, k_full);
+            tc::bulk_load_a(dst + C::kRawRows + lane * run, k + exps + at, run, k_full);
+            tc::bulk_load_a(dst + C::kRawRows + kTile + lane * run, v + exps + at, run, k_full);
+        }
+        ok = tile == 0 || tc::mbar_wait(&sh->raw_v_empty, (tile - 1) & 1);
+        if (!(ok = __all_sync(0xFFFFFFFFu, ok))) {
+            ++tile;  // K's copies of this tile are in flight
+            break;
+        }
         if (lane == 0)
-            tc::mbar_arrive(&sh->k_full[st]);
-        if (more)
-            load_raw<FMT, D, SPLIT>(c, cur.it, 0, cur.key0(), next.pages, tid, k);
-        ok = tile < kStages || tc::mbar_wait(&sh->v_empty[st], ph ^ 1);
-        if (!__all_sync(0xFFFFFFFFu, ok))
-            return false;
-        convert<FMT, D, SPLIT>(v, smem + C::kVAt + st * C::kOperand, tid, [&](int row) {
-            const uint32_t ev = exp_of(now.v_exps, row);
-            return ev == kv::kNanRow ? 0u : pow2_f16x2((int)ev - vu);
-        });
-        tc::fence_proxy_async_smem();
+            tc::mbar_arrive_expect_tx(&sh->raw_v_full, copied * run * (R::kCode + R::kScale));
         __syncwarp();
-        if (lane == 0)
-            tc::mbar_arrive(&sh->v_full[st]);
-        if (!more)
-            return true;
-        load_raw<FMT, D, SPLIT>(c, cur.it, 1, cur.key0(), next.pages, tid, v);
-        now = next;
+        if (there) {
+            const uint32_t dst = smem + C::kRawVAt;
+            tc::bulk_load_a(dst + lane * run * R::kCode, v + at * R::kCode, run * R::kCode, v_full);
+            if (R::kScale)
+                tc::bulk_load_a(dst + kTile * R::kCode + lane * run * R::kScale, v + scales + at * R::kScale,
+                                run * R::kScale, v_full);
+        }
     }
+    // nothing is in flight when the warp leaves
+    if (tile > 0)
+        ok = tc::mbar_wait(&sh->raw_k_full, (tile - 1) & 1) && ok;
+    if (tile > 0 && ok)
+        ok = tc::mbar_wait(&sh->raw_v_full, (tile - 1) & 1);
+    else if (tile > 1)
+        tc::mbar_wait(&sh->raw_v_full, (tile - 2) & 1);
+    return ok;
+}
+
+// ---------------------------------------------------------------------------
+// Conversion warps
+// ---------------------------------------------------------------------------
+
+// f16x2 of 2^x, zero below 2^-24.
+NVFP4_DEVINL uint32_t pow2_f16x2(int x)
+{
+    const float f = x < -40 ? 0.f : __uint_as_float((uint32_t)(127 + x) << 23);
+    return f32x2_to_f16x2(f, f);
+}
+
+// Largest exponent byte of the rows that hold numbers; 127 if there is none.
+NVFP4_DEVINL int largest_exp(uint32_t four)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t e = four >> (8 * j) & 0xFFu;
+        m = max(m, e == kv::kNanRow ? 0u : e);
+    }
+    m = __reduce_max_sync(0xFFFFFFFFu, m);
+    return m == 0 ? 127 : (int)m;
+}
+
+// A thread converts kMine 16-byte chunks of codes of a tile of K or V: in each
+// of its kPerBlock rows (kRowStep apart), one chunk of every 64-element column
+// block.  Neighbouring lanes take the chunks of a block, then the next row; every
+// other group of rows begins with the other block, so that both the reads (rows
+// of codes) and the writes (swizzled rows of f16) of 8 lanes lie on different
+// banks.  unit[i]: f16x2 factor of row i.  CUT: rows with bit i of `live` off are
+// written as zeros, whatever lies in the buffer.
+template <int FMT, int D, bool SPLIT, bool CUT>
+NVFP4_DEVINL void convert(uint32_t raw, uint32_t operand, int tid, const uint32_t (&unit)[Cfg<FMT, D, SPLIT>::kPerBlock],
+                          uint32_t live)
+{
+    using C = Cfg<FMT, D, SPLIT>;
+    using R = kv::Row<FMT, D>;
+    constexpr int per = C::kPerBlock, kOut = 8 / per;  // 16-byte chunks of f16 from one of codes
+    const int row0 = tid / per, place = tid % per;
+    const int flip = D == 64 ? 0 : per == 4 ? row0 & 1 : row0 >> 1 & 1;
+    uint32_t swizzled[kOut];
+#pragma unroll
+    for (int h = 0; h < kOut; ++h)
+        swizzled[h] = operand + row0 * 128 + (((place * kOut + h) ^ (row0 & 7)) << 4);
+#pragma unroll
+    for (int b = 0; b < D / 64; ++b) {
+        const int block = b ^ flip;
+        const uint32_t from = raw + row0 * R::kCode + (block * per + place) * 16;
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+            const uint4 code = tc::lds128(from + i * C::kRowStep * R::kCode);
+            uint32_t w[4] = {code.x, code.y, code.z, code.w};
+            const bool on = !CUT || (live >> i & 1);
+            if constexpr (CUT) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = on ? w[j] : 0u;
+            }
+            const uint32_t to = block * (128 * 128) + i * C::kRowStep * 128;
+            if constexpr (FMT == NVFP4_KV_E4M3) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
+                            : "=r"(o[2 * j]), "=r"(o[2 * j + 1])
+                            : "r"(w[2 * h + j]));
+                    sts128(swizzled[h] + to, make_uint4(sk::f16x2_mul(o[0], unit[i]), sk::f16x2_mul(o[1], unit[i]),
+                                                        sk::f16x2_mul(o[2], unit[i]), sk::f16x2_mul(o[3], unit[i])));
+                }
+            } else {
+                uint32_t two = tc::lds16(raw + kTile * R::kCode + (row0 + i * C::kRowStep) * R::kScale +
+                                         (block * per + place) * 2);
+                if constexpr (CUT)
+                    two = on ? two : 0u;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const uint32_t s =
+                        sk::f16x2_mul(e4m3x2_to_f16x2((uint16_t)((two >> (h / 2 * 8) & 0xFFu) * 0x101u)), unit[i]);
+                    uint32_t o[4];
+                    sk::e2m1x8_to_f16x2(w[h], o);
+                    sts128(swizzled[h] + to, make_uint4(sk::f16x2_mul(o[0], s), sk::f16x2_mul(o[1], s),
+                                                        sk::f16x2_mul(o[2], s), sk::f16x2_mul(o[3], s)));
+                }
+            }
+        }
+    }
+}
+
+template <int FMT, int D, bool SPLIT>
+NVFP4_DEVINL bool convert_role(uint32_t tiles, Shared *sh, uint32_t smem, int tid)
+{
+    using C = Cfg<FMT, D, SPLIT>;
+    constexpr int per = C::kPerBlock;
+    const int lane = tid % 32;
+    for (uint32_t tile = 0; tile < tiles; ++tile) {
+        const uint32_t st = tile % kStages, ph = (tile / kStages) & 1;
+        bool ok = tc::mbar_wait(&sh->raw_k_full, tile & 1);
+        ok = ok && (tile < kStages || tc::mbar_wait(&sh->k_empty[st], ph ^ 1));
+        if (!__all_sync(0xFFFFFFFFu, ok))
+            return false;
+        // exponents of rows 4 lane .. 4 lane + 3, a byte each; 0: no row that anyone sees
+        const RawInfo info = sh->raw;
+        uint32_t ek = tc::lds32(smem + C::kRawKAt + C::kRawRows + 4 * lane);
+        uint32_t ev = tc::lds32(smem + C::kRawKAt + C::kRawRows + kTile + 4 * lane);
+        const int first = info.key0 + 4 * lane;
+        uint32_t keep = info.present >> (lane / 4) & 1 ? 0xFFFFFFFFu : 0u;
+        if (first < info.lo)
+            keep = first + 4 <= info.lo ? 0u : keep << (8 * (info.lo - first));
+        if (first + 4 > info.hi)
+            keep &= first >= info.hi ? 0u : 0xFFFFFFFFu >> (8 * (first + 4 - info.hi));
+        ek &= keep;
+        ev &= keep;
+        const int ku = largest_exp(ek), vu = largest_exp(ev);
+        const bool all = __all_sync(0xFFFFFFFFu, keep == 0xFFFFFFFFu);
+        uint32_t k_unit[per], v_unit[per], live = 0;
+#pragma unroll
+        for (int i = 0; i < per; ++i) {
+            const int row = tid / per + i * C::kRowStep, sh8 = 8 * (row & 3);
+            const uint32_t a = __shfl_sync(0xFFFFFFFFu, ek, row >> 2) >> sh8 & 0xFFu;
+            const uint32_t b = __shfl_sync(0xFFFFFFFFu, ev, row >> 2) >> sh8 & 0xFFu;
+            // a row that is not a number makes its scores NaN, whichever of K and V it is
+            k_unit[i] = a == kv::kNanRow || b == kv::kNanRow ? 0x7FFF7FFFu : pow2_f16x2((int)a - ku);
+            v_unit[i] = b == kv::kNanRow ? 0u : pow2_f16x2((int)b - vu);
+            live |= (a != 0 ? 1u : 0u) << i;
+        }
+        const uint32_t k_to = smem + C::kKAt + st * C::kOperand, v_to = smem + C::kVAt + st * C::kOperand;
+        if (all)
+            convert<FMT, D, SPLIT, false>(smem + C::kRawKAt, k_to, tid, k_unit, live);
+        else
+            convert<FMT, D, SPLIT, true>(smem + C::kRawKAt, k_to, tid, k_unit, live);
+        if (tid == 0)
+            sh->info[tile % kInfos] = {kv::exp2_byte(ku), (float)(vu - 127), info.present, 0};
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tc::mbar_arrive(&sh->k_full[st]);
+            tc::mbar_arrive(&sh->raw_k_empty);
+        }
+        ok = tc::mbar_wait(&sh->raw_v_full, tile & 1);
+        ok = ok && (tile < kStages || tc::mbar_wait(&sh->v_empty[st], ph ^ 1));
+        if (!__all_sync(0xFFFFFFFFu, ok))
+            return false;
+        if (all)
+            convert<FMT, D, SPLIT, false>(smem + C::kRawVAt, v_to, tid, v_unit, live);
+        else
+            convert<FMT, D, SPLIT, true>(smem + C::kRawVAt, v_to, tid, v_unit, live);
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tc::mbar_arrive(&sh->v_full[st]);
+            tc::mbar_arrive(&sh->raw_v_empty);
+        }
+    }
+    return true;
 }
 
 // ---------------------------------------------------------------------------
@@ -586,30 +673,36 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, const Item &fi
             const float f = factor * info.k_unit;
             const bool whole = __all_sync(0xFFFFFFFFu, key0 >= lo && key0 + kTile <= (c.tree ? min(hi, it.seq.past) : hi) &&
                                                            info.present == 0xFFu);
-            uint32_t s[32];
-            // largest score
-            float m = -INFINITY;
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                tc::tmem_ld_32x32b_x32(scores + 32 * q, s);
-                tc::tmem_ld_wait();
-                uint32_t see = 0xFFFFFFFFu;
-                if (!whole) {
-                    see = seen_bits(key0 + 32 * q, lo, hi, c.tree != nullptr, word, it.seq.past);
-                    see &= (info.present >> (2 * q) & 1 ? 0x0000FFFFu : 0u) | (info.present >> (2 * q + 1) & 1 ? 0xFFFF0000u : 0u);
+            uint32_t s[4][32];
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                tc::tmem_ld_32x32b_x32(scores + 32 * q, s[q]);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                settle(s[q]);
+            uint32_t see[4];
+            if (!whole) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    see[q] = seen_bits(key0 + 32 * q, lo, hi, c.tree != nullptr, word, it.seq.past);
+                    see[q] &= (info.present >> (2 * q) & 1 ? 0x0000FFFFu : 0u) |
+                              (info.present >> (2 * q + 1) & 1 ? 0xFFFF0000u : 0u);
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        m = see >> j & 1 ? fmaxf(m, __uint_as_float(s[j])) : m;
-                } else {
-                    float m1 = __uint_as_float(s[0]), m2 = __uint_as_float(s[1]);
-#pragma unroll
-                    for (int j = 2; j < 32; j += 2) {
-                        m1 = fmaxf(m1, __uint_as_float(s[j]));
-                        m2 = fmaxf(m2, __uint_as_float(s[j + 1]));
-                    }
-                    m = fmaxf(m, fmaxf(m1, m2));
+                        s[q][j] = see[q] >> j & 1 ? s[q][j] : 0xFF800000u;  // -infinity
                 }
             }
+            // largest score
+            float best[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                best[q] = __uint_as_float(s[q][0]);
+#pragma unroll
+                for (int j = 1; j < 32; ++j)
+                    best[q] = fmaxf(best[q], __uint_as_float(s[q][j]));
+            }
+            const float m = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
             const float z = m == -INFINITY ? -INFINITY : fmaf(m, f, info.v_exp);
             const bool over = z > top + kSlack;
             if (__any_sync(0xFFFFFFFFu, over)) {
@@ -619,49 +712,47 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, const Item &fi
                 sum *= shrink;
                 if (begun) {
 #pragma unroll 1
-                    for (int q = 0; q < D / 32; ++q) {
-                        tc::tmem_ld_32x32b_x32(out + 32 * q, s);
+                    for (int q = 0; q < D / 16; ++q) {
+                        uint32_t x[16];
+                        tc::tmem_ld_32x32b_x16(out + 16 * q, x);
                         tc::tmem_ld_wait();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            s[j] = __float_as_uint(__uint_as_float(s[j]) * shrink);
-                        tc::tmem_st_32x32b_x32(out + 32 * q, s);
+                        for (int j = 0; j < 16; ++j)
+                            asm volatile("mul.rn.f32 %0, %0, %1;" : "+r"(x[j]) : "f"(shrink));
+                        tc::tmem_st_32x32b_x16(out + 16 * q, x);
                     }
                 }
             }
             // weights
             const float add = info.v_exp - (top == -INFINITY ? 0.f : top);
-            float l[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                tc::tmem_ld_32x32b_x32(scores + 32 * q, s);
-                tc::tmem_ld_wait();
-                uint32_t p[16];
-                if (whole) {
+            const uint64_t f2 = pack2(f, f), add_2 = pack2(add, add);
+            uint64_t l2[2] = {0, 0};
+            const auto weights = [&](auto masked) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t p[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float a = ex2(fmaf(__uint_as_float(s[2 * j]), f, add));
-                        const float b = ex2(fmaf(__uint_as_float(s[2 * j + 1]), f, add));
-                        l[2 * (j & 1)] += a;
-                        l[2 * (j & 1) + 1] += b;
+                        const float2 e = unpack2(
+                            fma2(pack2(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])), f2, add_2));
+                        float a = ex2(e.x), b = ex2(e.y);
+                        if constexpr (masked.value) {
+                            a = see[q] >> (2 * j) & 1 ? a : 0.f;
+                            b = see[q] >> (2 * j + 1) & 1 ? b : 0.f;
+                        }
+                        l2[j & 1] = add2(l2[j & 1], pack2(a, b));
                         p[j] = f32x2_to_f16x2(a, b);
                     }
-                } else {
-                    uint32_t see = seen_bits(key0 + 32 * q, lo, hi, c.tree != nullptr, word, it.seq.past);
-                    see &= (info.present >> (2 * q) & 1 ? 0x0000FFFFu : 0u) | (info.present >> (2 * q + 1) & 1 ? 0xFFFF0000u : 0u);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float a = see >> (2 * j) & 1 ? ex2(fmaf(__uint_as_float(s[2 * j]), f, add)) : 0.f;
-                        const float b = see >> (2 * j + 1) & 1 ? ex2(fmaf(__uint_as_float(s[2 * j + 1]), f, add)) : 0.f;
-                        l[2 * (j & 1)] += a;
-                        l[2 * (j & 1) + 1] += b;
-                        p[j] = f32x2_to_f16x2(a, b);
-                    }
+                    tc::tmem_st_32x32b_x16(scores + 16 * q, p);
                 }
-                tc::tmem_st_32x32b_x16(scores + 16 * q, p);
-            }
+            };
+            if (whole)
+                weights(std::false_type{});
+            else
+                weights(std::true_type{});
+            const float2 la = unpack2(l2[0]), lb = unpack2(l2[1]);
             tc::tmem_st_wait();
-            sum = fmaf((l[0] + l[1]) + (l[2] + l[3]), ex2(-info.v_exp) * kSumUnit, sum);
+            sum = fmaf((la.x + la.y) + (lb.x + lb.y), ex2(-info.v_exp) * kSumUnit, sum);
             tc::fence_before_sync();
             tc::mbar_arrive(&sh->p_ready[group]);
             begun = true;
@@ -826,6 +917,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
             tc::mbar_init(&sh->pv_done[g], 1);
             tc::mbar_init(&sh->drain[g], 1);
         }
+        tc::mbar_init(&sh->raw_k_full, 1);
+        tc::mbar_init(&sh->raw_v_full, 1);
+        tc::mbar_init(&sh->raw_k_empty, kConvertWarps);
+        tc::mbar_init(&sh->raw_v_empty, kConvertWarps);
         tc::fence_mbar_init();
     }
     if (warp == kSoftmaxWarps + kConvertWarps + 2)
@@ -838,17 +933,26 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
     bool ok = true;
     uint32_t code = 0;
     if (warp < kSoftmaxWarps) {
+        take_regs<kSoftmaxRegs>();
         ok = softmax_role<FMT, D, SPLIT>(c, range, item, item_begin, sh, smem, tmem, workspace, tid);
         code = kTimeoutSoftmax;
     } else if (warp < kSoftmaxWarps + kConvertWarps) {
-        ok = convert_role<FMT, D, SPLIT>(c, range, item, item_begin, sh, smem, tid - 32 * kSoftmaxWarps);
+        give_regs<kConvertRegs>();
+        ok = convert_role<FMT, D, SPLIT>((uint32_t)(range.end - range.begin), sh, smem, tid - 32 * kSoftmaxWarps);
         code = kTimeoutConvert;
-    } else if (warp < kSoftmaxWarps + kConvertWarps + 2) {
-        if (elect_one()) {
-            ok = mma_role<FMT, D, SPLIT>(c, range, item, item_begin, sh, smem, tmem, warp - kSoftmaxWarps - kConvertWarps);
-            code = kTimeoutMma;
+    } else {
+        give_regs<kMmaRegs>();
+        if (warp < kSoftmaxWarps + kConvertWarps + 2) {
+            if (elect_one()) {
+                ok = mma_role<FMT, D, SPLIT>(c, range, item, item_begin, sh, smem, tmem,
+                                             warp - kSoftmaxWarps - kConvertWarps);
+                code = kTimeoutMma;
+            }
+            __syncwarp();
+        } else if (warp == kSoftmaxWarps + kConvertWarps + 2) {
+            ok = load_role<FMT, D, SPLIT>(c, range, item, item_begin, sh, smem, tid % 32);
+            code = kTimeoutLoad;
         }
-        __syncwarp();
     }
     if (!ok)
         kv::report(c.pool.status, code);
@@ -866,6 +970,12 @@ cudaError_t launch(const Call &c, uint8_t *workspace, int num_sms, cudaStream_t 
     static cudaError_t results[kMaxDevices];
     const auto kernel = chunk_kernel<FMT, D, SPLIT>;
     const cudaError_t e = once_per_device(once, results, [kernel] {
+        cudaFuncAttributes attr;
+        const cudaError_t got = cudaFuncGetAttributes(&attr, kernel);
+        if (got != cudaSuccess)
+            return got;
+        if (attr.numRegs != kLaunchRegs)  // the roles share out what the launch gives: never launch with less
+            return cudaErrorInvalidConfiguration;
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (e != cudaSuccess)
