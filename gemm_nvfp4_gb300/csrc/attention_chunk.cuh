@@ -17,8 +17,9 @@
 //                   transposed).
 //   warps 12, 13    MMA issue for row tile 0 and 1: S = Q K^T, O += P V.
 //
-// Registers go where the scores are: a softmax thread keeps its row's 128 scores
-// and reads tensor memory once per tile.
+// The roles share one instruction cache: each one's loop is kept short (half a
+// tile's scores at a time, one loop body for K and V), because straight-line
+// code for whole tiles, with variants for masked ones, ran out of it.
 //
 // SPLIT: when a sequence has at most 128 rows, both softmax groups take the same
 // row tile, one the even and the other the odd key tiles, and their results
@@ -46,13 +47,10 @@ constexpr int kRowTile = 128;                   // rows of a row tile
 constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
 constexpr int kConvertThreads = 32 * kConvertWarps;
 constexpr int kThreads = 32 * (kSoftmaxWarps + kConvertWarps + 4);  // whole warpgroups; warp 15 idles
-// Registers of a thread by role: what the launch gives every thread, shared out anew.
-constexpr int kSoftmaxRegs = 176, kConvertRegs = 96, kMmaRegs = 56, kLaunchRegs = 128;
-static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kConvertWarps * kConvertRegs + 4 * kMmaRegs) <= kThreads * kLaunchRegs,
-              "setmaxnreg would wait for registers that nobody gives back");
 constexpr int kStages = 2;
 constexpr int kInfos = 4;
-constexpr float kHeadroom = 7.f, kSlack = 15.f;
+constexpr float kHeadroom = 7.f;
+constexpr float kMostWeight = 0x1p15f;  // of the weights of half a tile, in sum
 constexpr float kSumUnit = 0x1p-32f;
 
 // Codes of the status word (waits that ran out).
@@ -98,7 +96,7 @@ struct RawInfo {
 struct Shared {
     uint64_t raw_k_full, raw_k_empty, raw_v_full, raw_v_empty;
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    uint64_t q_ready[2], s_full[2], p_ready[2], pv_done[2], drain[2];
+    uint64_t q_ready[2], s_full[2], p_ready[2][2], pv_half[2], pv_done[2], drain[2];  // p_ready: by half of the keys
     TileInfo info[kInfos];
     RawInfo raw;
     uint32_t tmem, last;
@@ -138,17 +136,6 @@ NVFP4_DEVINL uint32_t f32x2_to_bf16x2(float lo, float hi)
     return r;
 }
 
-template <int N>
-NVFP4_DEVINL void take_regs()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-NVFP4_DEVINL void give_regs()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 // Pairs of fp32 in one instruction.
 NVFP4_DEVINL uint64_t pack2(float lo, float hi)
 {
@@ -172,6 +159,13 @@ NVFP4_DEVINL uint64_t add2(uint64_t a, uint64_t b)
 {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+NVFP4_DEVINL float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
@@ -370,11 +364,11 @@ NVFP4_DEVINL int largest_exp(uint32_t four)
 // block.  Neighbouring lanes take the chunks of a block, then the next row; every
 // other group of rows begins with the other block, so that both the reads (rows
 // of codes) and the writes (swizzled rows of f16) of 8 lanes lie on different
-// banks.  unit[i]: f16x2 factor of row i.  CUT: rows with bit i of `live` off are
-// written as zeros, whatever lies in the buffer.
-template <int FMT, int D, bool SPLIT, bool CUT>
+// banks.  unit[i]: f16x2 factor of row i; keep[i]: all ones, or zero for a row
+// that is written as zeros whatever lies in the buffer.
+template <int FMT, int D, bool SPLIT>
 NVFP4_DEVINL void convert(uint32_t raw, uint32_t operand, int tid, const uint32_t (&unit)[Cfg<FMT, D, SPLIT>::kPerBlock],
-                          uint32_t live)
+                          const uint32_t (&keep)[Cfg<FMT, D, SPLIT>::kPerBlock])
 {
     using C = Cfg<FMT, D, SPLIT>;
     using R = kv::Row<FMT, D>;
@@ -385,20 +379,22 @@ NVFP4_DEVINL void convert(uint32_t raw, uint32_t operand, int tid, const uint32_
 #pragma unroll
     for (int h = 0; h < kOut; ++h)
         swizzled[h] = operand + row0 * 128 + (((place * kOut + h) ^ (row0 & 7)) << 4);
-#pragma unroll
+#pragma unroll 1
     for (int b = 0; b < D / 64; ++b) {
         const int block = b ^ flip;
         const uint32_t from = raw + row0 * R::kCode + (block * per + place) * 16;
+        uint4 code[per];
+        uint32_t two[per];
 #pragma unroll
         for (int i = 0; i < per; ++i) {
-            const uint4 code = tc::lds128(from + i * C::kRowStep * R::kCode);
-            uint32_t w[4] = {code.x, code.y, code.z, code.w};
-            const bool on = !CUT || (live >> i & 1);
-            if constexpr (CUT) {
+            code[i] = tc::lds128(from + i * C::kRowStep * R::kCode);
+            if constexpr (FMT == NVFP4_KV_NVFP4)
+                two[i] = tc::lds16(raw + kTile * R::kCode + (row0 + i * C::kRowStep) * R::kScale +
+                                   (block * per + place) * 2);
+        }
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = on ? w[j] : 0u;
-            }
+        for (int i = 0; i < per; ++i) {
+            const uint32_t w[4] = {code[i].x & keep[i], code[i].y & keep[i], code[i].z & keep[i], code[i].w & keep[i]};
             const uint32_t to = block * (128 * 128) + i * C::kRowStep * 128;
             if constexpr (FMT == NVFP4_KV_E4M3) {
 #pragma unroll
@@ -413,18 +409,16 @@ NVFP4_DEVINL void convert(uint32_t raw, uint32_t operand, int tid, const uint32_
                                                         sk::f16x2_mul(o[2], unit[i]), sk::f16x2_mul(o[3], unit[i])));
                 }
             } else {
-                uint32_t two = tc::lds16(raw + kTile * R::kCode + (row0 + i * C::kRowStep) * R::kScale +
-                                         (block * per + place) * 2);
-                if constexpr (CUT)
-                    two = on ? two : 0u;
+                const uint32_t sc = two[i] & keep[i];
+                const uint32_t s[2] = {sk::f16x2_mul(e4m3x2_to_f16x2((uint16_t)((sc & 0xFFu) * 0x101u)), unit[i]),
+                                       sk::f16x2_mul(e4m3x2_to_f16x2((uint16_t)((sc >> 8) * 0x101u)), unit[i])};
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    const uint32_t s =
-                        sk::f16x2_mul(e4m3x2_to_f16x2((uint16_t)((two >> (h / 2 * 8) & 0xFFu) * 0x101u)), unit[i]);
                     uint32_t o[4];
                     sk::e2m1x8_to_f16x2(w[h], o);
-                    sts128(swizzled[h] + to, make_uint4(sk::f16x2_mul(o[0], s), sk::f16x2_mul(o[1], s),
-                                                        sk::f16x2_mul(o[2], s), sk::f16x2_mul(o[3], s)));
+                    const uint32_t m = s[h / 2];
+                    sts128(swizzled[h] + to, make_uint4(sk::f16x2_mul(o[0], m), sk::f16x2_mul(o[1], m),
+                                                        sk::f16x2_mul(o[2], m), sk::f16x2_mul(o[3], m)));
                 }
             }
         }
@@ -456,44 +450,44 @@ NVFP4_DEVINL bool convert_role(uint32_t tiles, Shared *sh, uint32_t smem, int ti
         ek &= keep;
         ev &= keep;
         const int ku = largest_exp(ek), vu = largest_exp(ev);
-        const bool all = __all_sync(0xFFFFFFFFu, keep == 0xFFFFFFFFu);
-        uint32_t k_unit[per], v_unit[per], live = 0;
+        uint32_t unit[per], v_unit[per], rows[per];
 #pragma unroll
         for (int i = 0; i < per; ++i) {
             const int row = tid / per + i * C::kRowStep, sh8 = 8 * (row & 3);
             const uint32_t a = __shfl_sync(0xFFFFFFFFu, ek, row >> 2) >> sh8 & 0xFFu;
             const uint32_t b = __shfl_sync(0xFFFFFFFFu, ev, row >> 2) >> sh8 & 0xFFu;
             // a row that is not a number makes its scores NaN, whichever of K and V it is
-            k_unit[i] = a == kv::kNanRow || b == kv::kNanRow ? 0x7FFF7FFFu : pow2_f16x2((int)a - ku);
+            unit[i] = a == kv::kNanRow || b == kv::kNanRow ? 0x7FFF7FFFu : pow2_f16x2((int)a - ku);
             v_unit[i] = b == kv::kNanRow ? 0u : pow2_f16x2((int)b - vu);
-            live |= (a != 0 ? 1u : 0u) << i;
+            rows[i] = a != 0 ? 0xFFFFFFFFu : 0u;
         }
-        const uint32_t k_to = smem + C::kKAt + st * C::kOperand, v_to = smem + C::kVAt + st * C::kOperand;
-        if (all)
-            convert<FMT, D, SPLIT, false>(smem + C::kRawKAt, k_to, tid, k_unit, live);
-        else
-            convert<FMT, D, SPLIT, true>(smem + C::kRawKAt, k_to, tid, k_unit, live);
-        if (tid == 0)
-            sh->info[tile % kInfos] = {kv::exp2_byte(ku), (float)(vu - 127), info.present, 0};
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tc::mbar_arrive(&sh->k_full[st]);
-            tc::mbar_arrive(&sh->raw_k_empty);
-        }
-        ok = tc::mbar_wait(&sh->raw_v_full, tile & 1);
-        ok = ok && (tile < kStages || tc::mbar_wait(&sh->v_empty[st], ph ^ 1));
-        if (!__all_sync(0xFFFFFFFFu, ok))
-            return false;
-        if (all)
-            convert<FMT, D, SPLIT, false>(smem + C::kRawVAt, v_to, tid, v_unit, live);
-        else
-            convert<FMT, D, SPLIT, true>(smem + C::kRawVAt, v_to, tid, v_unit, live);
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tc::mbar_arrive(&sh->v_full[st]);
-            tc::mbar_arrive(&sh->raw_v_empty);
+        // K, then V
+        uint32_t from = smem + C::kRawKAt, to = smem + C::kKAt + st * C::kOperand;
+        uint64_t *full = &sh->k_full[st], *raw_empty = &sh->raw_k_empty;
+#pragma unroll 1
+        for (int which = 0; which < 2; ++which) {
+            if (which == 1) {
+                ok = tc::mbar_wait(&sh->raw_v_full, tile & 1);
+                ok = ok && (tile < kStages || tc::mbar_wait(&sh->v_empty[st], ph ^ 1));
+                if (!__all_sync(0xFFFFFFFFu, ok))
+                    return false;
+            }
+            convert<FMT, D, SPLIT>(from, to, tid, unit, rows);
+            if (which == 0 && tid == 0)
+                sh->info[tile % kInfos] = {kv::exp2_byte(ku), (float)(vu - 127), info.present, 0};
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tc::mbar_arrive(full);
+                tc::mbar_arrive(raw_empty);
+            }
+            from = smem + C::kRawVAt;
+            to = smem + C::kVAt + st * C::kOperand;
+            full = &sh->v_full[st];
+            raw_empty = &sh->raw_v_empty;
+#pragma unroll
+            for (int i = 0; i < per; ++i)
+                unit[i] = v_unit[i];
         }
     }
     return true;
@@ -537,14 +531,23 @@ NVFP4_DEVINL bool mma_role(const Call &c, const Range &range, const Item &first,
             }
             tc::mma_commit(&sh->s_full[group]);
             tc::mma_commit(&sh->k_empty[st]);
-            ok = tc::mbar_wait(&sh->v_full[st], ph) && tc::mbar_wait(&sh->p_ready[group], mine & 1);
+            ok = tc::mbar_wait(&sh->v_full[st], ph);
+            const uint32_t v = smem + C::kVAt + st * C::kOperand;
+            // the first half's product runs while the second half's weights are made
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                ok = ok && tc::mbar_wait(&sh->p_ready[group][h], mine & 1);
+                if (!ok)
+                    break;
+                tc::fence_after_sync();
+#pragma unroll
+                for (int j = h * kTile / 32; j < (h + 1) * kTile / 32; ++j)
+                    tc::mma_f16_ts(out, scores + 8 * j, desc_transposed(v + j * 2048), out_idesc, begun || j > 0);
+                if (h == 0)
+                    tc::mma_commit(&sh->pv_half[group]);
+            }
             if (!ok)
                 break;
-            tc::fence_after_sync();
-            const uint32_t v = smem + C::kVAt + st * C::kOperand;
-#pragma unroll
-            for (int j = 0; j < kTile / 16; ++j)
-                tc::mma_f16_ts(out, scores + 8 * j, desc_transposed(v + j * 2048), out_idesc, begun || j > 0);
             tc::mma_commit(&sh->pv_done[group]);
             tc::mma_commit(&sh->v_empty[st]);
             begun = true;
@@ -631,7 +634,8 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, const Item &fi
                 }
             }
             const int e = max((int)(max(m2 & 0xFFFFu, m2 >> 16) >> 7), 15);
-            const float up = (e == 255 ? NAN : __uint_as_float((uint32_t)(268 - e) << 23)) * (c.scale_log2 < 0 ? -1.f : 1.f);
+            const float sign = c.scale_log2 < 0 ? -1.f : c.scale_log2 > 0 ? 1.f : 0.f;
+            const float up = (e == 255 ? NAN : __uint_as_float((uint32_t)(268 - e) << 23)) * sign;
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) {
                 const uint4 x = live ? src[i] : make_uint4(0, 0, 0, 0);
@@ -670,91 +674,95 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, const Item &fi
                 break;
             tc::fence_after_sync();
             const TileInfo info = sh->info[tile % kInfos];
-            const float f = factor * info.k_unit;
+            // above zero: a masked score of -infinity stays one
+            const float f = fmaxf(factor * info.k_unit, 0x1p-126f);
             const bool whole = __all_sync(0xFFFFFFFFu, key0 >= lo && key0 + kTile <= (c.tree ? min(hi, it.seq.past) : hi) &&
                                                            info.present == 0xFFu);
-            uint32_t s[4][32];
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                tc::tmem_ld_32x32b_x32(scores + 32 * q, s[q]);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                settle(s[q]);
-            uint32_t see[4];
-            if (!whole) {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    see[q] = seen_bits(key0 + 32 * q, lo, hi, c.tree != nullptr, word, it.seq.past);
-                    see[q] &= (info.present >> (2 * q) & 1 ? 0x0000FFFFu : 0u) |
-                              (info.present >> (2 * q + 1) & 1 ? 0xFFFF0000u : 0u);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        s[q][j] = see[q] >> j & 1 ? s[q][j] : 0xFF800000u;  // -infinity
-                }
-            }
-            // largest score
-            float best[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                best[q] = __uint_as_float(s[q][0]);
-#pragma unroll
-                for (int j = 1; j < 32; ++j)
-                    best[q] = fmaxf(best[q], __uint_as_float(s[q][j]));
-            }
-            const float m = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
-            const float z = m == -INFINITY ? -INFINITY : fmaf(m, f, info.v_exp);
-            const bool over = z > top + kSlack;
-            if (__any_sync(0xFFFFFFFFu, over)) {
-                const float next = over ? z - kHeadroom : top;
-                const float shrink = over ? ex2(top - next) : 1.f;
-                top = next;
-                sum *= shrink;
-                if (begun) {
+            const float sum_unit = ex2(-info.v_exp) * kSumUnit;
+            const uint64_t f2 = pack2(f, f);
 #pragma unroll 1
-                    for (int q = 0; q < D / 16; ++q) {
-                        uint32_t x[16];
-                        tc::tmem_ld_32x32b_x16(out + 16 * q, x);
-                        tc::tmem_ld_wait();
+            for (int h = 0; h < 2; ++h) {  // halves of the keys
+                uint32_t s[2][32];
+                tc::tmem_ld_32x32b_x32(scores + 64 * h, s[0]);
+                tc::tmem_ld_32x32b_x32(scores + 64 * h + 32, s[1]);
+                tc::tmem_ld_wait();
+                settle(s[0]);
+                settle(s[1]);
+                if (!whole) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            asm volatile("mul.rn.f32 %0, %0, %1;" : "+r"(x[j]) : "f"(shrink));
-                        tc::tmem_st_32x32b_x16(out + 16 * q, x);
+                    for (int q = 0; q < 2; ++q) {
+                        const int g = 4 * h + 2 * q;
+                        uint32_t see = seen_bits(key0 + 16 * g, lo, hi, c.tree != nullptr, word, it.seq.past);
+                        see &= (info.present >> g & 1 ? 0x0000FFFFu : 0u) | (info.present >> g & 2 ? 0xFFFF0000u : 0u);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            s[q][j] = see >> j & 1 ? s[q][j] : 0xFF800000u;  // -infinity
                     }
                 }
-            }
-            // weights
-            const float add = info.v_exp - (top == -INFINITY ? 0.f : top);
-            const uint64_t f2 = pack2(f, f), add_2 = pack2(add, add);
-            uint64_t l2[2] = {0, 0};
-            const auto weights = [&](auto masked) {
+                float l = 0.f;
+                bool over = top == -INFINITY;
+                // at most twice: after the move no weight is above 2^kHeadroom
+#pragma unroll 1
+                for (int pass = 0; pass < 2; ++pass) {
+                    if (__any_sync(0xFFFFFFFFu, over)) {
+                        // move the row's reference to its largest score so far, and with it what was summed up
+                        float m = -INFINITY;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    uint32_t p[16];
+                        for (int q = 0; q < 2; ++q) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float2 e = unpack2(
-                            fma2(pack2(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])), f2, add_2));
-                        float a = ex2(e.x), b = ex2(e.y);
-                        if constexpr (masked.value) {
-                            a = see[q] >> (2 * j) & 1 ? a : 0.f;
-                            b = see[q] >> (2 * j + 1) & 1 ? b : 0.f;
+                            for (int j = 0; j < 32; j += 2)
+                                m = max3(m, __uint_as_float(s[q][j]), __uint_as_float(s[q][j + 1]));
                         }
-                        l2[j & 1] = add2(l2[j & 1], pack2(a, b));
-                        p[j] = f32x2_to_f16x2(a, b);
+                        const float next = over ? fmaxf(top, fmaf(m, f, info.v_exp) - kHeadroom) : top;
+                        const float shrink = top == next ? 1.f : ex2(top - next);
+                        top = next;
+                        sum *= shrink;
+                        if (h == 1) {  // the first half's product is under way
+                            ok = ok && tc::mbar_wait(&sh->pv_half[group], mine & 1);
+                            tc::fence_after_sync();
+                        }
+                        if (begun || h == 1) {
+#pragma unroll 1
+                            for (int q = 0; q < D / 16; ++q) {
+                                uint32_t x[16];
+                                tc::tmem_ld_32x32b_x16(out + 16 * q, x);
+                                tc::tmem_ld_wait();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    asm volatile("mul.rn.f32 %0, %0, %1;" : "+r"(x[j]) : "f"(shrink));
+                                tc::tmem_st_32x32b_x16(out + 16 * q, x);
+                            }
+                        }
                     }
-                    tc::tmem_st_32x32b_x16(scores + 16 * q, p);
+                    const float add = info.v_exp - (top == -INFINITY ? 0.f : top);
+                    const uint64_t add_2 = pack2(add, add);
+                    uint64_t l2[2] = {0, 0};
+                    uint32_t p[2][16];
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            const float2 e = unpack2(fma2(
+                                pack2(__uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1])), f2, add_2));
+                            const float a = ex2(e.x), b = ex2(e.y);
+                            l2[j & 1] = add2(l2[j & 1], pack2(a, b));
+                            p[q][j] = f32x2_to_f16x2(a, b);
+                        }
+                        tc::tmem_st_32x32b_x16(scores + 32 * h + 16 * q, p[q]);
+                    }
+                    const float2 la = unpack2(l2[0]), lb = unpack2(l2[1]);
+                    l = (la.x + la.y) + (lb.x + lb.y);
+                    over = l > kMostWeight;
+                    if (!__any_sync(0xFFFFFFFFu, over))
+                        break;
                 }
-            };
-            if (whole)
-                weights(std::false_type{});
-            else
-                weights(std::true_type{});
-            const float2 la = unpack2(l2[0]), lb = unpack2(l2[1]);
-            tc::tmem_st_wait();
-            sum = fmaf((la.x + la.y) + (lb.x + lb.y), ex2(-info.v_exp) * kSumUnit, sum);
-            tc::fence_before_sync();
-            tc::mbar_arrive(&sh->p_ready[group]);
+                sum = fmaf(l, sum_unit, sum);
+                tc::tmem_st_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (r % 32 == 0)
+                    tc::mbar_arrive(&sh->p_ready[group][h]);
+            }
             begun = true;
             ++mine;
         }
@@ -913,7 +921,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
         for (int g = 0; g < 2; ++g) {
             tc::mbar_init(&sh->q_ready[g], kRowTile);
             tc::mbar_init(&sh->s_full[g], 1);
-            tc::mbar_init(&sh->p_ready[g], kRowTile);
+            tc::mbar_init(&sh->p_ready[g][0], kRowTile / 32);
+            tc::mbar_init(&sh->p_ready[g][1], kRowTile / 32);
+            tc::mbar_init(&sh->pv_half[g], 1);
             tc::mbar_init(&sh->pv_done[g], 1);
             tc::mbar_init(&sh->drain[g], 1);
         }
@@ -933,15 +943,12 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
     bool ok = true;
     uint32_t code = 0;
     if (warp < kSoftmaxWarps) {
-        take_regs<kSoftmaxRegs>();
         ok = softmax_role<FMT, D, SPLIT>(c, range, item, item_begin, sh, smem, tmem, workspace, tid);
         code = kTimeoutSoftmax;
     } else if (warp < kSoftmaxWarps + kConvertWarps) {
-        give_regs<kConvertRegs>();
         ok = convert_role<FMT, D, SPLIT>((uint32_t)(range.end - range.begin), sh, smem, tid - 32 * kSoftmaxWarps);
         code = kTimeoutConvert;
     } else {
-        give_regs<kMmaRegs>();
         if (warp < kSoftmaxWarps + kConvertWarps + 2) {
             if (elect_one()) {
                 ok = mma_role<FMT, D, SPLIT>(c, range, item, item_begin, sh, smem, tmem,
@@ -970,12 +977,6 @@ cudaError_t launch(const Call &c, uint8_t *workspace, int num_sms, cudaStream_t 
     static cudaError_t results[kMaxDevices];
     const auto kernel = chunk_kernel<FMT, D, SPLIT>;
     const cudaError_t e = once_per_device(once, results, [kernel] {
-        cudaFuncAttributes attr;
-        const cudaError_t got = cudaFuncGetAttributes(&attr, kernel);
-        if (got != cudaSuccess)
-            return got;
-        if (attr.numRegs != kLaunchRegs)  // the roles share out what the launch gives: never launch with less
-            return cudaErrorInvalidConfiguration;
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (e != cudaSuccess)

@@ -59,21 +59,6 @@ NVFP4_DEVINL void set_block(const Call &c, Item &it)
 template <int RB>
 NVFP4_DEVINL int row_blocks(const Call &c, const Seq &s) { return (s.n * c.group + RB - 1) / RB; }
 
-// Tiles of a sequence, over all its row blocks and KV heads.
-template <int RB, int TK>
-NVFP4_DEVINL int64_t seq_tiles(const Call &c, int b)
-{
-    Item it;
-    it.seq = load_seq(c, b);
-    const int blocks = row_blocks<RB>(c, it.seq);
-    int64_t n = 0;
-    for (it.rb = 0; it.rb < blocks; ++it.rb) {
-        set_block<RB, TK>(c, it);
-        n += it.tiles;
-    }
-    return n * c.pool.heads;
-}
-
 struct Range {
     int64_t total;       // tiles of the call
     int64_t begin, end;  // of this CTA
@@ -90,16 +75,44 @@ NVFP4_DEVINL int range_owner(int64_t total, int ctas, int64_t u)
 // Every thread of the CTA calls this: this CTA's range, its first item, and
 // the list position of that item's first tile.  `scratch`: shared memory,
 // THREADS / 32 + 4 words of 64 bits.  Returns false if the CTA has no work.
+//
+// Row blocks are numbered as if every sequence had as many as the longest can
+// have; thread t sums the t-th run of consecutive numbers (one long sequence
+// is spread over the threads as well as many short ones), and a scan over the
+// threads follows.
 template <int RB, int TK, int THREADS>
 __device__ bool find_range(const Call &c, int64_t *scratch, Range *range, Item *item, int64_t *item_begin)
 {
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    // thread t sums the t-th run of consecutive sequences; a scan over the threads follows
-    const int per = (c.n_seqs + THREADS - 1) / THREADS;
-    const int b0 = min(tid * per, c.n_seqs), b1 = min(b0 + per, c.n_seqs);
+    const int most = (int)(((int64_t)c.max_q_len * c.group + RB - 1) / RB);  // row blocks of a sequence
+    const int64_t numbers = (int64_t)c.n_seqs * most;
+    const int64_t per = (numbers + THREADS - 1) / THREADS;
+    const int64_t n0 = min(tid * per, numbers), n1 = min(n0 + per, numbers);
+    // f(sequence and row block of each number of the run that is there, its tiles over all heads) until it returns true
+    const auto each = [&](auto &&f) {
+        if (n0 >= n1)
+            return;
+        Item it;
+        it.b = (int)(n0 / most);
+        it.rb = (int)(n0 - (int64_t)it.b * most);
+        it.seq = load_seq(c, it.b);
+        for (int64_t i = n0; i < n1; ++i) {
+            if (it.rb < row_blocks<RB>(c, it.seq)) {
+                set_block<RB, TK>(c, it);
+                if (f(it, (int64_t)it.tiles * c.pool.heads))
+                    return;
+            }
+            if (++it.rb == most && i + 1 < n1) {
+                it.rb = 0;
+                it.seq = load_seq(c, ++it.b);
+            }
+        }
+    };
     int64_t mine = 0;
-    for (int b = b0; b < b1; ++b)
-        mine += seq_tiles<RB, TK>(c, b);
+    each([&](const Item &, int64_t n) {
+        mine += n;
+        return false;
+    });
     int64_t upto = mine;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
@@ -125,27 +138,18 @@ __device__ bool find_range(const Call &c, int64_t *scratch, Range *range, Item *
     range->end = range_start(total, range->ctas, blockIdx.x + 1);
     if (range->begin >= upto - mine && range->begin < upto) {  // exactly one thread
         int64_t at = upto - mine;
-        int b = b0;
-        for (;; ++b) {
-            const int64_t n = seq_tiles<RB, TK>(c, b);
-            if (range->begin < at + n)
-                break;
-            at += n;
-        }
-        Item it;
-        it.seq = load_seq(c, b);
-        for (it.rb = 0;; ++it.rb) {
-            set_block<RB, TK>(c, it);
-            const int64_t n = (int64_t)it.tiles * c.pool.heads;
-            if (range->begin < at + n)
-                break;
-            at += n;
-        }
-        const int head = (int)((range->begin - at) / it.tiles);
-        int64_t *out = scratch + THREADS / 32;
-        out[0] = (int64_t)b << 32 | it.rb;
-        out[1] = head;
-        out[2] = at + (int64_t)head * it.tiles;
+        each([&](const Item &it, int64_t n) {
+            if (range->begin >= at + n) {
+                at += n;
+                return false;
+            }
+            const int head = (int)((range->begin - at) / it.tiles);
+            int64_t *out = scratch + THREADS / 32;
+            out[0] = (int64_t)it.b << 32 | it.rb;
+            out[1] = head;
+            out[2] = at + (int64_t)head * it.tiles;
+            return true;
+        });
     }
     __syncthreads();
     const int64_t *out = scratch + THREADS / 32;
