@@ -10,12 +10,12 @@
 //   warps 0-3, 4-7  softmax of row tile 0 and 1: a thread has one row.  Scores
 //                   come from tensor memory and the weights P go back there as
 //                   the f16 A operand of the second product, over the scores.
-//   warp 14         bulk copies of a tile's codes, scales and exponents from the
+//   warp 18         bulk copies of a tile's codes, scales and exponents from the
 //                   pages to shared memory, ahead of their conversion.
-//   warps 8-11      codes to f16, from there to the layout of the MMA's B operands
+//   warps 8-15      codes to f16, from there to the layout of the MMA's B operands
 //                   (K with the head dimension contiguous; V likewise, read
 //                   transposed).
-//   warps 12, 13    MMA issue for row tile 0 and 1: S = Q K^T, O += P V.
+//   warps 16, 17    MMA issue for row tile 0 and 1: S = Q K^T, O += P V.
 //
 // The roles share one instruction cache: each one's loop is kept short (half a
 // tile's scores at a time, one loop body for K and V), because straight-line
@@ -44,9 +44,13 @@ namespace chunk {
 
 constexpr int kTile = 128;                      // keys of a tile
 constexpr int kRowTile = 128;                   // rows of a row tile
-constexpr int kSoftmaxWarps = 8, kConvertWarps = 4;
+constexpr int kSoftmaxWarps = 8, kConvertWarps = 8;
 constexpr int kConvertThreads = 32 * kConvertWarps;
-constexpr int kThreads = 32 * (kSoftmaxWarps + kConvertWarps + 4);  // whole warpgroups; warp 15 idles
+constexpr int kThreads = 32 * (kSoftmaxWarps + kConvertWarps + 4);  // whole warpgroups; warp 19 idles
+// Registers of a thread by role: what the launch gives every thread, shared out anew.
+constexpr int kSoftmaxRegs = 136, kConvertRegs = 64, kMmaRegs = 72, kLaunchRegs = 96;
+static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kConvertWarps * kConvertRegs + 4 * kMmaRegs) <= kThreads * kLaunchRegs,
+              "setmaxnreg would wait for registers that nobody gives back");
 constexpr int kStages = 2;
 constexpr int kInfos = 4;
 constexpr float kHeadroom = 7.f;
@@ -70,12 +74,9 @@ struct Cfg {
     static constexpr int kSlotFloats = kRows * (D + 2);
     // tensor memory columns
     static constexpr int kScoreCols = 0, kOutCols = 2 * kTile;
-    // 16-byte chunks of codes: of a 64-element column block of a row, of a thread per tile of K or V.
-    // A thread's chunks lie in kPerBlock rows, kRowStep apart.
+    // 16-byte chunks of codes of a 64-element column block of a row.  A thread's lie in kRowsMine rows, kRowStep apart.
     static constexpr int kPerBlock = FMT == NVFP4_KV_E4M3 ? 4 : 2;
-    static constexpr int kMine = D / 64 * kTile * kPerBlock / kConvertThreads;
-    static constexpr int kRowStep = kConvertThreads / kPerBlock;
-    static_assert(kTile / kRowStep == kPerBlock, "rows of a thread");
+    static constexpr int kRowStep = kConvertThreads / kPerBlock, kRowsMine = kTile / kRowStep;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -93,12 +94,22 @@ struct RawInfo {
     uint32_t present;
 };
 
+// The part of an item that a CTA works on: the softmax warps' place in the CTA's range.
+struct Segment {
+    Item it;
+    int64_t item_begin, item_end;  // of the item in the call's list
+    int64_t u;                     // first tile, in the call's list
+    int32_t tile0, n;              // first key tile, and number of tiles
+    uint32_t index;                // of the first tile among the CTA's
+};
+
 struct Shared {
     uint64_t raw_k_full, raw_k_empty, raw_v_full, raw_v_empty;
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t q_ready[2], s_full[2], p_ready[2][2], pv_half[2], pv_done[2], drain[2];  // p_ready: by half of the keys
     TileInfo info[kInfos];
     RawInfo raw;
+    Segment seg;
     uint32_t tmem, last;
     int64_t scratch[kThreads / 32 + 4];
     float2 stats[2][kRowTile];  // largest and sum of a row, by softmax group
@@ -134,6 +145,17 @@ NVFP4_DEVINL uint32_t f32x2_to_bf16x2(float lo, float hi)
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+template <int N>
+NVFP4_DEVINL void take_regs()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+NVFP4_DEVINL void give_regs()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Pairs of fp32 in one instruction.
@@ -359,20 +381,19 @@ NVFP4_DEVINL int largest_exp(uint32_t four)
     return m == 0 ? 127 : (int)m;
 }
 
-// A thread converts kMine 16-byte chunks of codes of a tile of K or V: in each
-// of its kPerBlock rows (kRowStep apart), one chunk of every 64-element column
-// block.  Neighbouring lanes take the chunks of a block, then the next row; every
+// A thread converts, in each of its kRowsMine rows of a tile of K or V, one
+// 16-byte chunk of codes of every 64-element column block.  Neighbouring lanes take the chunks of a block, then the next row; every
 // other group of rows begins with the other block, so that both the reads (rows
 // of codes) and the writes (swizzled rows of f16) of 8 lanes lie on different
 // banks.  unit[i]: f16x2 factor of row i; keep[i]: all ones, or zero for a row
 // that is written as zeros whatever lies in the buffer.
 template <int FMT, int D, bool SPLIT>
-NVFP4_DEVINL void convert(uint32_t raw, uint32_t operand, int tid, const uint32_t (&unit)[Cfg<FMT, D, SPLIT>::kPerBlock],
-                          const uint32_t (&keep)[Cfg<FMT, D, SPLIT>::kPerBlock])
+NVFP4_DEVINL void convert(uint32_t raw, uint32_t operand, int tid, const uint32_t (&unit)[Cfg<FMT, D, SPLIT>::kRowsMine],
+                          const uint32_t (&keep)[Cfg<FMT, D, SPLIT>::kRowsMine])
 {
     using C = Cfg<FMT, D, SPLIT>;
     using R = kv::Row<FMT, D>;
-    constexpr int per = C::kPerBlock, kOut = 8 / per;  // 16-byte chunks of f16 from one of codes
+    constexpr int per = C::kPerBlock, rows = C::kRowsMine, kOut = 8 / per;  // 16-byte chunks of f16 from one of codes
     const int row0 = tid / per, place = tid % per;
     const int flip = D == 64 ? 0 : per == 4 ? row0 & 1 : row0 >> 1 & 1;
     uint32_t swizzled[kOut];
@@ -383,17 +404,17 @@ NVFP4_DEVINL void convert(uint32_t raw, uint32_t operand, int tid, const uint32_
     for (int b = 0; b < D / 64; ++b) {
         const int block = b ^ flip;
         const uint32_t from = raw + row0 * R::kCode + (block * per + place) * 16;
-        uint4 code[per];
-        uint32_t two[per];
+        uint4 code[rows];
+        uint32_t two[rows];
 #pragma unroll
-        for (int i = 0; i < per; ++i) {
+        for (int i = 0; i < rows; ++i) {
             code[i] = tc::lds128(from + i * C::kRowStep * R::kCode);
             if constexpr (FMT == NVFP4_KV_NVFP4)
                 two[i] = tc::lds16(raw + kTile * R::kCode + (row0 + i * C::kRowStep) * R::kScale +
                                    (block * per + place) * 2);
         }
 #pragma unroll
-        for (int i = 0; i < per; ++i) {
+        for (int i = 0; i < rows; ++i) {
             const uint32_t w[4] = {code[i].x & keep[i], code[i].y & keep[i], code[i].z & keep[i], code[i].w & keep[i]};
             const uint32_t to = block * (128 * 128) + i * C::kRowStep * 128;
             if constexpr (FMT == NVFP4_KV_E4M3) {
@@ -429,7 +450,7 @@ template <int FMT, int D, bool SPLIT>
 NVFP4_DEVINL bool convert_role(uint32_t tiles, Shared *sh, uint32_t smem, int tid)
 {
     using C = Cfg<FMT, D, SPLIT>;
-    constexpr int per = C::kPerBlock;
+    constexpr int per = C::kPerBlock, mine = C::kRowsMine;
     const int lane = tid % 32;
     for (uint32_t tile = 0; tile < tiles; ++tile) {
         const uint32_t st = tile % kStages, ph = (tile / kStages) & 1;
@@ -450,9 +471,9 @@ NVFP4_DEVINL bool convert_role(uint32_t tiles, Shared *sh, uint32_t smem, int ti
         ek &= keep;
         ev &= keep;
         const int ku = largest_exp(ek), vu = largest_exp(ev);
-        uint32_t unit[per], v_unit[per], rows[per];
+        uint32_t unit[mine], v_unit[mine], rows[mine];
 #pragma unroll
-        for (int i = 0; i < per; ++i) {
+        for (int i = 0; i < mine; ++i) {
             const int row = tid / per + i * C::kRowStep, sh8 = 8 * (row & 3);
             const uint32_t a = __shfl_sync(0xFFFFFFFFu, ek, row >> 2) >> sh8 & 0xFFu;
             const uint32_t b = __shfl_sync(0xFFFFFFFFu, ev, row >> 2) >> sh8 & 0xFFu;
@@ -486,7 +507,7 @@ NVFP4_DEVINL bool convert_role(uint32_t tiles, Shared *sh, uint32_t smem, int ti
             full = &sh->v_full[st];
             raw_empty = &sh->raw_v_empty;
 #pragma unroll
-            for (int i = 0; i < per; ++i)
+            for (int i = 0; i < mine; ++i)
                 unit[i] = v_unit[i];
         }
     }
@@ -589,41 +610,53 @@ NVFP4_DEVINL uint32_t seen_bits(int first, int lo, int hi, bool tree, uint64_t w
     return m;
 }
 
+NVFP4_DEVINL void set_segment(const Range &range, Segment *g)
+{
+    g->item_end = g->item_begin + g->it.tiles;
+    g->tile0 = g->it.tile0 + (int)(g->u - g->item_begin);
+    g->n = (int)(min(g->item_end, range.end) - g->u);
+}
+
+// The segment lies in shared memory, not in registers: the loop over the tiles
+// needs those for the scores.
 template <int FMT, int D, bool SPLIT>
-NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, const Item &first, int64_t item_begin, Shared *sh,
-                               uint32_t smem, uint32_t tmem, uint8_t *workspace, int tid)
+NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, uint32_t smem, uint32_t tmem,
+                               uint8_t *workspace, int tid)
 {
     using C = Cfg<FMT, D, SPLIT>;
     constexpr int kBar = 1, kAll = 32 * kSoftmaxWarps;
     const int group = tid / 128, r = tid % 128;       // row of the row tile, and lane of tensor memory
-    const int warp_lane = (r / 32) * 32;
-    const uint32_t lanes = (uint32_t)warp_lane << 16;
+    const uint32_t lanes = (uint32_t)(r & ~31) << 16;
     const uint32_t scores = tmem + C::kScoreCols + group * kTile + lanes;
     const uint32_t out = tmem + C::kOutCols + group * D + lanes;
-    uint32_t *const counters = reinterpret_cast<uint32_t *>(workspace + kCounterOffset);
-    float *const partials = reinterpret_cast<float *>(workspace + kPartialOffset);
+    const Segment &g = sh->seg;
     bool ok = true;
     uint32_t mine = 0;
 
-    for_segments<C::kRows>(c, range, first, item_begin, [&](const Item &it, int tile0, int n, uint32_t tile,
-                                                            int64_t begin, int64_t end) {
+    for (;;) {
         const int row = (SPLIT ? 0 : group * kRowTile) + r;  // row of the item
-        const bool live = row < it.rows;
-        const int tok = live ? (it.row0 + row) / c.group : 0;
-        const int hq = it.head * c.group + (live ? (it.row0 + row) % c.group : 0);
-        const int64_t q_row = it.seq.q_begin + tok;
-        int lo = 0, hi = 0;
+        const bool live = row < g.it.rows;
+        const auto token = [&] { return (g.it.row0 + row) / c.group; };
+        // rows beyond the last one: no key is masked, and none has any weight
+        int lo = 0, hi = INT32_MAX;
         uint64_t word = 0;
+        float top = 1e30f;
+        const int past = g.it.seq.past;
+        int64_t q_at_elem = 0;
         if (live) {
-            key_range(c, it.seq, tok, &lo, &hi);
+            const int tok = token();
+            const int64_t q_row = g.it.seq.q_begin + tok;
+            key_range(c, g.it.seq, tok, &lo, &hi);
             if (c.tree)
                 word = c.tree[q_row];
+            top = -INFINITY;
+            q_at_elem = q_row * c.q_ld + (int64_t)(g.it.head * c.group + (g.it.row0 + row) - tok * c.group) * D;
         }
         // Q to f16, times a power of two that puts its largest element at 2^14 (and the scale's sign)
         float factor = 0.f;
         if (!SPLIT || group == 0) {
             const uint32_t q_at = smem + C::kQAt + (SPLIT ? 0 : group) * C::kOperand;
-            const uint4 *src = reinterpret_cast<const uint4 *>(c.q + q_row * c.q_ld + (int64_t)hq * D);
+            const uint4 *src = reinterpret_cast<const uint4 *>(c.q + q_at_elem);
             uint32_t m2 = 0;
             if (live) {
 #pragma unroll
@@ -651,9 +684,9 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, const Item &fi
                 sh->stats[0][r].x = factor;
             tc::fence_proxy_async_smem();
             // a group waits once for each segment in which it has a tile
-            for (int g = SPLIT ? 0 : group; g <= (SPLIT ? 1 : group); ++g) {
-                if (has_tile<SPLIT>(g, tile, n))
-                    tc::mbar_arrive(&sh->q_ready[g]);
+            for (int i = SPLIT ? 0 : group; i <= (SPLIT ? 1 : group); ++i) {
+                if (has_tile<SPLIT>(i, g.index, g.n))
+                    tc::mbar_arrive(&sh->q_ready[i]);
             }
         }
         if (SPLIT) {
@@ -661,22 +694,21 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, const Item &fi
             factor = sh->stats[0][r].x;
         }
 
-        const uint32_t tile0_index = tile;
-        float top = -INFINITY, sum = 0.f;
+        float sum = 0.f;
         bool begun = false;
-        for (int i = 0; i < n && ok; ++i, ++tile) {
-            if (!takes<SPLIT>(group, tile))
-                continue;
+        const int n = g.n, tile0 = g.tile0;
+        const uint32_t index = g.index;
+        for (int i = SPLIT ? (int)((index ^ group) & 1) : 0; i < n && ok; i += SPLIT ? 2 : 1) {
             const int key0 = (tile0 + i) * kTile;
             ok = tc::mbar_wait(&sh->s_full[group], mine & 1);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok)
                 break;
             tc::fence_after_sync();
-            const TileInfo info = sh->info[tile % kInfos];
+            const TileInfo info = sh->info[(index + i) % kInfos];
             // above zero: a masked score of -infinity stays one
             const float f = fmaxf(factor * info.k_unit, 0x1p-126f);
-            const bool whole = __all_sync(0xFFFFFFFFu, key0 >= lo && key0 + kTile <= (c.tree ? min(hi, it.seq.past) : hi) &&
+            const bool whole = __all_sync(0xFFFFFFFFu, key0 >= lo && key0 + kTile <= (c.tree && live ? min(hi, past) : hi) &&
                                                            info.present == 0xFFu);
             const float sum_unit = ex2(-info.v_exp) * kSumUnit;
             const uint64_t f2 = pack2(f, f);
@@ -688,19 +720,22 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, const Item &fi
                 tc::tmem_ld_wait();
                 settle(s[0]);
                 settle(s[1]);
+                bool sees = true;
                 if (!whole) {
+                    sees = false;
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        const int g = 4 * h + 2 * q;
-                        uint32_t see = seen_bits(key0 + 16 * g, lo, hi, c.tree != nullptr, word, it.seq.past);
-                        see &= (info.present >> g & 1 ? 0x0000FFFFu : 0u) | (info.present >> g & 2 ? 0xFFFF0000u : 0u);
+                        const int at = 4 * h + 2 * q;
+                        uint32_t see = seen_bits(key0 + 16 * at, lo, hi, c.tree && live, word, past);
+                        see &= (info.present >> at & 1 ? 0x0000FFFFu : 0u) | (info.present >> at & 2 ? 0xFFFF0000u : 0u);
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             s[q][j] = see >> j & 1 ? s[q][j] : 0xFF800000u;  // -infinity
+                        sees |= see != 0;
                     }
                 }
                 float l = 0.f;
-                bool over = top == -INFINITY;
+                bool over = top == -INFINITY && sees;
                 // at most twice: after the move no weight is above 2^kHeadroom
 #pragma unroll 1
                 for (int pass = 0; pass < 2; ++pass) {
@@ -714,14 +749,16 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, const Item &fi
                                 m = max3(m, __uint_as_float(s[q][j]), __uint_as_float(s[q][j + 1]));
                         }
                         const float next = over ? fmaxf(top, fmaf(m, f, info.v_exp) - kHeadroom) : top;
-                        const float shrink = top == next ? 1.f : ex2(top - next);
+                        // (nothing has been summed before the first reference)
+                        const float shrink = top == next || top == -INFINITY ? 1.f : ex2(top - next);
                         top = next;
                         sum *= shrink;
-                        if (h == 1) {  // the first half's product is under way
+                        const bool move = __any_sync(0xFFFFFFFFu, shrink != 1.f);
+                        if (move && h == 1) {  // the first half's product is under way
                             ok = ok && tc::mbar_wait(&sh->pv_half[group], mine & 1);
                             tc::fence_after_sync();
                         }
-                        if (begun || h == 1) {
+                        if (move && (begun || h == 1)) {
 #pragma unroll 1
                             for (int q = 0; q < D / 16; ++q) {
                                 uint32_t x[16];
@@ -788,7 +825,7 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, const Item &fi
             w_mine = wa;
             w_other = wb;
         }
-        const bool has0 = !SPLIT || has_tile<SPLIT>(0, tile0_index, n), has1 = SPLIT && has_tile<SPLIT>(1, tile0_index, n);
+        const bool has0 = !SPLIT || has_tile<SPLIT>(0, g.index, g.n), has1 = SPLIT && has_tile<SPLIT>(1, g.index, g.n);
         const uint32_t out0 = SPLIT ? tmem + C::kOutCols + lanes : out, out1 = tmem + C::kOutCols + D + lanes;
         const auto result = [&](int q, float (&x)[32]) {  // elements col0 + 32 q ..
             uint32_t s[32];
@@ -814,7 +851,9 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, const Item &fi
             if (!live)
                 return;
             const float inv = l == 0.f ? 0.f : kSumUnit / l;
-            uint16_t *dst = static_cast<uint16_t *>(c.out) + q_row * c.out_ld + (int64_t)hq * D + col0 + 32 * q;
+            const int tok = token();
+            uint16_t *dst = static_cast<uint16_t *>(c.out) + (g.it.seq.q_begin + tok) * c.out_ld +
+                            (int64_t)(g.it.head * c.group + (g.it.row0 + row) - tok * c.group) * D + col0 + 32 * q;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t v[4];
@@ -824,7 +863,7 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, const Item &fi
                 reinterpret_cast<uint4 *>(dst)[j] = make_uint4(v[0], v[1], v[2], v[3]);
             }
         };
-        if (begin >= range.begin && end <= range.end) {
+        if (g.item_begin >= range.begin && g.item_end <= range.end) {
             for (int q = 0; q < kCols / 32; ++q) {
                 float x[32];
                 result(q, x);
@@ -832,9 +871,11 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, const Item &fi
             }
         } else {
             // partial result: [element / 4][row][4], then [row] (largest, sum)
-            const int first_cta = range_owner(range.total, range.ctas, begin);
-            const int last_cta = range_owner(range.total, range.ctas, end - 1);
-            float *slot = partials + ((int64_t)blockIdx.x * 2 + (begin < range.begin ? 0 : 1)) * C::kSlotFloats;
+            uint32_t *const counters = reinterpret_cast<uint32_t *>(workspace + kCounterOffset);
+            float *const partials = reinterpret_cast<float *>(workspace + kPartialOffset);
+            const int first_cta = range_owner(range.total, range.ctas, g.item_begin);
+            const int last_cta = range_owner(range.total, range.ctas, g.item_end - 1);
+            float *slot = partials + ((int64_t)blockIdx.x * 2 + (g.item_begin < range.begin ? 0 : 1)) * C::kSlotFloats;
             for (int q = 0; q < kCols / 32; ++q) {
                 float x[32];
                 result(q, x);
@@ -891,10 +932,23 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, const Item &fi
             }
         }
         tc::fence_before_sync();
-        tc::named_bar_sync(kBar, kAll);  // both groups are done with tensor memory, Q and the statistics
-        return true;
-    });
-    return ok;
+        tc::named_bar_sync(kBar, kAll);  // both groups are done with tensor memory, Q, the statistics and the segment
+        const bool more = g.u + g.n < range.end;
+        if (!more)
+            return true;
+        tc::named_bar_sync(kBar, kAll);
+        if (tid == 0) {
+            Segment *w = &sh->seg;
+            w->u += w->n;
+            w->index += w->n;
+            w->item_begin = w->item_end;
+            Item it = w->it;
+            next_item<C::kRows, kTile>(c, &it);
+            w->it = it;
+            set_segment(range, w);
+        }
+        tc::named_bar_sync(kBar, kAll);
+    }
 }
 
 template <int FMT, int D, bool SPLIT>
@@ -912,6 +966,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
     if (!find_range<C::kRows, kTile, kThreads>(c, sh->scratch, &range, &item, &item_begin))
         return;
     if (tid == 0) {
+        sh->seg.it = item;
+        sh->seg.item_begin = item_begin;
+        sh->seg.u = range.begin;
+        sh->seg.index = 0;
+        set_segment(range, &sh->seg);
         for (int i = 0; i < kStages; ++i) {
             tc::mbar_init(&sh->k_full[i], kConvertWarps);
             tc::mbar_init(&sh->v_full[i], kConvertWarps);
@@ -943,12 +1002,15 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
     bool ok = true;
     uint32_t code = 0;
     if (warp < kSoftmaxWarps) {
-        ok = softmax_role<FMT, D, SPLIT>(c, range, item, item_begin, sh, smem, tmem, workspace, tid);
+        take_regs<kSoftmaxRegs>();
+        ok = softmax_role<FMT, D, SPLIT>(c, range, sh, smem, tmem, workspace, tid);
         code = kTimeoutSoftmax;
     } else if (warp < kSoftmaxWarps + kConvertWarps) {
+        give_regs<kConvertRegs>();
         ok = convert_role<FMT, D, SPLIT>((uint32_t)(range.end - range.begin), sh, smem, tid - 32 * kSoftmaxWarps);
         code = kTimeoutConvert;
     } else {
+        give_regs<kMmaRegs>();
         if (warp < kSoftmaxWarps + kConvertWarps + 2) {
             if (elect_one()) {
                 ok = mma_role<FMT, D, SPLIT>(c, range, item, item_begin, sh, smem, tmem,
@@ -977,6 +1039,12 @@ cudaError_t launch(const Call &c, uint8_t *workspace, int num_sms, cudaStream_t 
     static cudaError_t results[kMaxDevices];
     const auto kernel = chunk_kernel<FMT, D, SPLIT>;
     const cudaError_t e = once_per_device(once, results, [kernel] {
+        cudaFuncAttributes attr;
+        const cudaError_t got = cudaFuncGetAttributes(&attr, kernel);
+        if (got != cudaSuccess)
+            return got;
+        if (attr.numRegs != kLaunchRegs)  // the roles share out what the launch gives: never launch with less
+            return cudaErrorInvalidConfiguration;
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
     if (e != cudaSuccess)
