@@ -106,7 +106,7 @@ struct Segment {
 struct Shared {
     uint64_t raw_k_full, raw_k_empty, raw_v_full, raw_v_empty;
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-    uint64_t q_ready[2], s_full[2], p_ready[2][2], pv_half[2], pv_done[2], drain[2];  // p_ready: by half of the keys
+    uint64_t q_ready[2], s_full[2][2], p_ready[2][2], pv_done[2][2], drain[2];  // by group, and half of the keys
     TileInfo info[kInfos];
     RawInfo raw;
     Segment seg;
@@ -523,56 +523,72 @@ NVFP4_DEVINL bool mma_role(const Call &c, const Range &range, const Item &first,
                            uint32_t smem, uint32_t tmem, int group)
 {
     using C = Cfg<FMT, D, SPLIT>;
-    constexpr uint32_t score_idesc = tc::idesc_f16kind(128, kTile, 0);
+    constexpr uint32_t score_idesc = tc::idesc_f16kind(128, kTile / 2, 0);
     constexpr uint32_t out_idesc = tc::idesc_f16kind(128, D, 0) | 1u << 16;  // B transposed
     const uint32_t scores = tmem + C::kScoreCols + group * kTile, out = tmem + C::kOutCols + group * D;
     const uint32_t q = smem + C::kQAt + (SPLIT ? 0 : group) * C::kOperand;
     bool ok = true;
-    uint32_t items = 0, mine = 0;  // segments and tiles of this group so far
+    uint32_t segments = 0, mine = 0;  // of this group so far: segments, and tiles whose scores were begun
+    // scores of half h of the group's tile number `t`, which is the CTA's number `tile`
+    const auto score = [&](uint32_t t, uint32_t tile, int h) {
+        const uint32_t st = tile % kStages, ph = (tile / kStages) & 1;
+        // (the half's weights of the tile before lie where its scores go)
+        ok = ok && (h == 1 || tc::mbar_wait(&sh->k_full[st], ph)) &&
+             (t == 0 || tc::mbar_wait(&sh->pv_done[group][h], (t - 1) & 1));
+        if (!ok)
+            return;
+        tc::fence_after_sync();
+        const uint32_t k = smem + C::kKAt + st * C::kOperand + h * (kTile / 2) * 128;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+            const uint32_t at = (d / 4) * (128 * 128) + (d % 4) * 32;
+            const uint64_t base = 1ull << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+            tc::mma_bf16_ss(scores + h * (kTile / 2), base | ((q + at) & 0x3FFFFu) >> 4, base | ((k + at) & 0x3FFFFu) >> 4,
+                            score_idesc, d > 0);
+        }
+        tc::mma_commit(&sh->s_full[group][h]);
+        if (h == 1)
+            tc::mma_commit(&sh->k_empty[st]);
+    };
     for_segments<C::kRows>(c, range, first, item_begin, [&](const Item &, int, int n, uint32_t tile, int64_t, int64_t) {
         if (!has_tile<SPLIT>(group, tile, n))
             return true;
-        ok = tc::mbar_wait(&sh->q_ready[group], items++ & 1);
+        ok = tc::mbar_wait(&sh->q_ready[group], segments++ & 1);
+        constexpr uint32_t step = SPLIT ? 2 : 1;
+        const uint32_t end = tile + n;
+        tile += SPLIT ? (tile ^ group) & 1 : 0;
+        score(mine, tile, 0);
         bool begun = false;
-        for (int i = 0; i < n && ok; ++i, ++tile) {
-            if (!takes<SPLIT>(group, tile))
-                continue;
+#pragma unroll 1
+        for (; tile < end && ok; tile += step, ++mine) {
             const uint32_t st = tile % kStages, ph = (tile / kStages) & 1;
-            ok = tc::mbar_wait(&sh->k_full[st], ph) && (mine == 0 || tc::mbar_wait(&sh->pv_done[group], (mine - 1) & 1));
-            if (!ok)
-                break;
-            tc::fence_after_sync();
-            const uint32_t k = smem + C::kKAt + st * C::kOperand;
-#pragma unroll
-            for (int d = 0; d < D / 16; ++d) {
-                const uint32_t at = (d / 4) * (128 * 128) + (d % 4) * 32;
-                const uint64_t base = 1ull << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
-                tc::mma_bf16_ss(scores, base | ((q + at) & 0x3FFFFu) >> 4, base | ((k + at) & 0x3FFFFu) >> 4, score_idesc,
-                                d > 0);
-            }
-            tc::mma_commit(&sh->s_full[group]);
-            tc::mma_commit(&sh->k_empty[st]);
-            ok = tc::mbar_wait(&sh->v_full[st], ph);
             const uint32_t v = smem + C::kVAt + st * C::kOperand;
-            // the first half's product runs while the second half's weights are made
-#pragma unroll
+#pragma unroll 1
             for (int h = 0; h < 2; ++h) {
-                ok = ok && tc::mbar_wait(&sh->p_ready[group][h], mine & 1);
+                // the next scores are made while the softmax is at these; those of the
+                // next tile wait behind this product if its keys are not converted yet
+                const bool more = tile + step < end;
+                const uint32_t next = tile + step;
+                bool made = true;
+                if (h == 0)
+                    score(mine, tile, 1);
+                else if (more && (made = tc::mbar_try_wait(&sh->k_full[next % kStages], (next / kStages) & 1)))
+                    score(mine + 1, next, 0);
+                ok = ok && (h == 1 || tc::mbar_wait(&sh->v_full[st], ph)) && tc::mbar_wait(&sh->p_ready[group][h], mine & 1);
                 if (!ok)
                     break;
                 tc::fence_after_sync();
 #pragma unroll
-                for (int j = h * kTile / 32; j < (h + 1) * kTile / 32; ++j)
-                    tc::mma_f16_ts(out, scores + 8 * j, desc_transposed(v + j * 2048), out_idesc, begun || j > 0);
-                if (h == 0)
-                    tc::mma_commit(&sh->pv_half[group]);
+                for (int j = 0; j < kTile / 32; ++j)
+                    tc::mma_f16_ts(out, scores + h * (kTile / 2) + 8 * j, desc_transposed(v + (h * (kTile / 32) + j) * 2048),
+                                   out_idesc, begun || j > 0);
+                tc::mma_commit(&sh->pv_done[group][h]);
+                if (h == 1)
+                    tc::mma_commit(&sh->v_empty[st]);
+                begun = true;
+                if (!made)
+                    score(mine + 1, next, 0);
             }
-            if (!ok)
-                break;
-            tc::mma_commit(&sh->pv_done[group]);
-            tc::mma_commit(&sh->v_empty[st]);
-            begun = true;
-            ++mine;
         }
         return ok;
     });
@@ -700,11 +716,10 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, ui
         const uint32_t index = g.index;
         for (int i = SPLIT ? (int)((index ^ group) & 1) : 0; i < n && ok; i += SPLIT ? 2 : 1) {
             const int key0 = (tile0 + i) * kTile;
-            ok = tc::mbar_wait(&sh->s_full[group], mine & 1);
+            ok = tc::mbar_wait(&sh->s_full[group][0], mine & 1);
             ok = __all_sync(0xFFFFFFFFu, ok);
             if (!ok)
                 break;
-            tc::fence_after_sync();
             const TileInfo info = sh->info[(index + i) % kInfos];
             // above zero: a masked score of -infinity stays one
             const float f = fmaxf(factor * info.k_unit, 0x1p-126f);
@@ -714,6 +729,13 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, ui
             const uint64_t f2 = pack2(f, f);
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {  // halves of the keys
+                if (h == 1) {
+                    ok = tc::mbar_wait(&sh->s_full[group][1], mine & 1);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok)
+                        break;
+                }
+                tc::fence_after_sync();
                 uint32_t s[2][32];
                 tc::tmem_ld_32x32b_x32(scores + 64 * h, s[0]);
                 tc::tmem_ld_32x32b_x32(scores + 64 * h + 32, s[1]);
@@ -754,11 +776,10 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, ui
                         top = next;
                         sum *= shrink;
                         const bool move = __any_sync(0xFFFFFFFFu, shrink != 1.f);
-                        if (move && h == 1) {  // the first half's product is under way
-                            ok = ok && tc::mbar_wait(&sh->pv_half[group], mine & 1);
-                            tc::fence_after_sync();
-                        }
                         if (move && (begun || h == 1)) {
+                            // the half's before product may be under way
+                            ok = ok && tc::mbar_wait(&sh->pv_done[group][h ^ 1], (h == 1 ? mine : mine - 1) & 1);
+                            tc::fence_after_sync();
 #pragma unroll 1
                             for (int q = 0; q < D / 16; ++q) {
                                 uint32_t x[16];
@@ -785,7 +806,7 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, ui
                             l2[j & 1] = add2(l2[j & 1], pack2(a, b));
                             p[q][j] = f32x2_to_f16x2(a, b);
                         }
-                        tc::tmem_st_32x32b_x16(scores + 32 * h + 16 * q, p[q]);
+                        tc::tmem_st_32x32b_x16(scores + 64 * h + 16 * q, p[q]);
                     }
                     const float2 la = unpack2(l2[0]), lb = unpack2(l2[1]);
                     l = (la.x + la.y) + (lb.x + lb.y);
@@ -804,7 +825,7 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, ui
             ++mine;
         }
         if (ok && begun)
-            ok = tc::mbar_wait(&sh->pv_done[group], (mine - 1) & 1);
+            ok = tc::mbar_wait(&sh->pv_done[group][1], (mine - 1) & 1);
         ok = tc::bar_and(kBar, kAll, ok);
         if (!ok)
             return false;
@@ -979,11 +1000,11 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
         }
         for (int g = 0; g < 2; ++g) {
             tc::mbar_init(&sh->q_ready[g], kRowTile);
-            tc::mbar_init(&sh->s_full[g], 1);
-            tc::mbar_init(&sh->p_ready[g][0], kRowTile / 32);
-            tc::mbar_init(&sh->p_ready[g][1], kRowTile / 32);
-            tc::mbar_init(&sh->pv_half[g], 1);
-            tc::mbar_init(&sh->pv_done[g], 1);
+            for (int h = 0; h < 2; ++h) {
+                tc::mbar_init(&sh->s_full[g][h], 1);
+                tc::mbar_init(&sh->p_ready[g][h], kRowTile / 32);
+                tc::mbar_init(&sh->pv_done[g][h], 1);
+            }
             tc::mbar_init(&sh->drain[g], 1);
         }
         tc::mbar_init(&sh->raw_k_full, 1);
