@@ -113,6 +113,7 @@ int nvfp4_paged_attention(const nvfp4_paged_attention_args *args, void *workspac
     c.q_heads = args->n_q_heads;
     c.group = args->n_q_heads / args->cache.n_kv_heads;
     c.window = args->window > INT32_MAX ? 0 : (int32_t)args->window;
+    c.item_cost = 0;
     c.out_bf16 = args->out_dtype == NVFP4_OUT_BF16;
     c.causal = args->causal;
     c.scale_log2 = args->scale * 1.4426950408889634f;

@@ -23,6 +23,7 @@ struct Call {
     int32_t n_seqs, total_q, max_q_len;
     int32_t q_heads, group;  // query heads, query heads of one KV head
     int32_t window;          // 0: none
+    int32_t item_cost;       // attention_plan.cuh
     int32_t out_bf16, causal;
     float scale_log2;  // scale * log2(e): the softmax works in powers of two
 };

@@ -111,7 +111,7 @@ struct Shared {
     RawInfo raw;
     Segment seg;
     uint32_t tmem, last;
-    int64_t scratch[kThreads / 32 + 4];
+    int64_t scratch[kThreads / 32 + 5];
     float2 stats[2][kRowTile];  // largest and sum of a row, by softmax group
 };
 
@@ -907,14 +907,14 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, ui
             }
             if (!SPLIT || group == 0)
                 reinterpret_cast<float2 *>(slot + C::kRows * D)[row] = make_float2(top, sum);
-            __threadfence();
-            tc::named_bar_sync(kBar, kAll);
+            tc::named_bar_sync(kBar, kAll);  // before the release below: it covers every thread's stores
             if (tid == 0) {
-                const bool done = atomicAdd(counters + first_cta, 1u) == (uint32_t)(last_cta - first_cta);
+                uint32_t seen;
+                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(seen) : "l"(counters + first_cta) : "memory");
+                const bool done = seen == (uint32_t)(last_cta - first_cta);
                 if (done)
                     counters[first_cta] = 0;
                 sh->last = done;
-                __threadfence();
             }
             tc::named_bar_sync(kBar, kAll);
             if (sh->last) {

@@ -170,40 +170,79 @@ NVFP4_DEVINL uint32_t chunk_at(int r, int c)
     return line * 128 + ((id & 7) ^ flip) * 16;
 }
 
-// A warp's copy of 16 keys into a stage of its ring.  `valid`: rows that hold
-// keys; the others become zeros, so that nothing an unwritten slot holds can
-// reach the second product.  (An exponent byte of 0, which no written row has,
-// masks the key: so do keys whose page is not there.)
+// What a lane copies of every step: its chunks of codes (of K, and the same of
+// V), and for the first lanes a chunk of scales or exponents.
+struct LaneCopy {
+    uint32_t code_at;  // of the first chunk in a stage; the others lie 512 bytes on (odd ones with bit 6 flipped, CPR = 8)
+    uint32_t aux_at;   // in a stage; all ones: no scales or exponents for this lane
+    uint32_t aux_from, aux_row;  // bytes from K's block of a page, and per row
+};
+
 template <int FMT, int D, int NT>
-NVFP4_DEVINL void load_step(const Call &c, int page, int head, int at, int valid, uint32_t stage, int lane)
+NVFP4_DEVINL LaneCopy lane_copy(const Call &c, int lane)
 {
     using C = Cfg<FMT, D, NT>;
     using R = kv::Row<FMT, D>;
-    constexpr int kChunks = R::kCode / 16;  // of a row
+    constexpr int kChunks = R::kCode / 16, kScaleChunks = C::kScaleBytes / 16, per = kScaleChunks > 0 ? kScaleChunks : 1;
     const int shift = c.pool.page_shift;
-    const uint8_t *blk = kv::block_ptr(c.pool, page, head, 0) + (int64_t)at * R::kCode;
-#pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-#pragma unroll
-        for (int i = 0; i < kStep * kChunks / 32; ++i) {
-            const int id = i * 32 + lane, r = id / kChunks;
-            cp_async16(stage + kv * C::kCodeBytes + chunk_at<kChunks>(r, id % kChunks),
-                       blk + (int64_t)kv * c.pool.block_bytes + id * 16, r < valid ? 16 : 0);
-        }
-    }
-    // scales (16 / kScale rows a chunk) and exponents
-    constexpr int kScaleChunks = C::kScaleBytes / 16;
-    const uint8_t *base = kv::block_ptr(c.pool, page, head, 0);
+    LaneCopy m;
+    m.code_at = chunk_at<kChunks>(lane / kChunks, lane % kChunks);
     if (lane < 2 * kScaleChunks) {
-        constexpr int per = kScaleChunks > 0 ? kScaleChunks : 1;
-        const int kv = lane / per, j = lane % per;
-        cp_async16(stage + C::kScaleAt + lane * 16,
-                   base + (int64_t)kv * c.pool.block_bytes + (R::kCode << shift) + at * R::kScale + j * 16,
-                   min(16, max(0, valid * R::kScale - j * 16)));
+        m.aux_at = C::kScaleAt + lane * 16;
+        m.aux_from = lane / per * c.pool.block_bytes + (R::kCode << shift) + lane % per * 16;
+        m.aux_row = R::kScale;
     } else if (lane < 2 * kScaleChunks + 2) {
         const int kv = lane - 2 * kScaleChunks;
-        cp_async16(stage + C::kExpAt + kv * kStep,
-                   base + (int64_t)kv * c.pool.block_bytes + ((R::kCode + R::kScale) << shift) + at, valid);
+        m.aux_at = C::kExpAt + kv * kStep;
+        m.aux_from = kv * c.pool.block_bytes + ((R::kCode + R::kScale) << shift);
+        m.aux_row = 1;
+    } else {
+        m.aux_at = ~0u;
+        m.aux_from = m.aux_row = 0;
+    }
+    return m;
+}
+
+// A warp's copy of 16 keys from row `at` of a page (whose K block of the head is
+// `blk`) into a stage of its ring.  `valid`: rows that hold keys; the others
+// become zeros, so that nothing an unwritten slot holds can reach the second
+// product.  (An exponent byte of 0, which no written row has, masks the key: so
+// do keys whose page is not there.)
+template <int FMT, int D, int NT>
+NVFP4_DEVINL void load_step(const Call &c, const LaneCopy &m, const uint8_t *blk, int at, int valid, uint32_t stage,
+                            int lane)
+{
+    using C = Cfg<FMT, D, NT>;
+    using R = kv::Row<FMT, D>;
+    constexpr int kChunks = R::kCode / 16, kMine = kStep * kChunks / 32;
+    const uint8_t *const src = blk + at * R::kCode + lane * 16;
+    const uint8_t *const aux = blk + m.aux_from + at * m.aux_row;
+    const uint32_t even = stage + m.code_at, odd = stage + (kChunks == 8 ? m.code_at ^ 64 : m.code_at);
+    if (valid == kStep) {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            const uint8_t *const from = src + (kv ? c.pool.block_bytes : 0);
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((i & 1 ? odd : even) + kv * C::kCodeBytes + 512 * i),
+                             "l"(from + 512 * i)
+                             : "memory");
+        }
+        if (m.aux_at != ~0u)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(stage + m.aux_at), "l"(aux) : "memory");
+    } else {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i)
+                cp_async16((i & 1 ? odd : even) + kv * C::kCodeBytes + 512 * i,
+                           src + (kv ? c.pool.block_bytes : 0) + 512 * i, (i * 32 + lane) / kChunks < valid ? 16 : 0);
+        }
+        if (m.aux_at != ~0u) {
+            // rows of this chunk that hold keys
+            const int begin = m.aux_row == 1 ? 0 : lane % (C::kScaleBytes / 16 > 0 ? C::kScaleBytes / 16 : 1) * 16;
+            cp_async16(stage + m.aux_at, aux, min(16, max(0, valid * (int)m.aux_row - begin)));
+        }
     }
 }
 
@@ -382,43 +421,57 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
         return;
     const uint32_t ring = tc::smem_addr(smem) + warp * C::kStages * C::kStageBytes;
     const int page_mask = (1 << c.pool.page_shift) - 1;
+    const LaneCopy copy = lane_copy<FMT, D, NT>(c, lane);
     uint32_t *const counters = reinterpret_cast<uint32_t *>(workspace + kCounterOffset);
     float *const partials = reinterpret_cast<float *>(workspace + kPartialOffset);
 
     for (int64_t u = range.begin; u < range.end;) {
-        const int64_t item_end = item_begin + it.tiles;
+        const int64_t tiles_begin = item_begin + c.item_cost, item_end = item_begin + it.units;
         const int64_t seg_end = min(item_end, range.end);
-        const int key0 = (it.tile0 + (int)(u - item_begin)) * kTile;
+        if (seg_end <= tiles_begin) {  // no tile of the item is this CTA's
+            u = seg_end;
+            if (u < range.end) {
+                item_begin = item_end;
+                next_item<C::kRows, kTile>(c, &it);
+            }
+            continue;
+        }
+        u = max(u, tiles_begin);
+        const int key0 = (it.tile0 + (int)(u - tiles_begin)) * kTile;
         const int steps = (int)(seg_end - u) * (kTile / kStep);
         const int mine = (steps - warp + kWarps - 1) / kWarps;  // steps of this warp: warp, warp + kWarps, ...
         const int32_t *const table = c.table + (int64_t)it.b * c.table_width;
 
         // Copies run kStages - 1 steps ahead; page numbers one step ahead of the copies.
-        const auto page_at = [&](int i) {
-            const int key = key0 + (warp + i * kWarps) * kStep;
-            const bool used = i < mine && key < it.hi && key + kStep > it.lo;
-            return used ? table[key >> c.pool.page_shift] : -1;
+        const uint8_t *const head_blk = kv::block_ptr(c.pool, 0, it.head, 0);
+        int next_key = key0 + warp * kStep, next_left = mine;  // of the step whose page is looked up next
+        uint32_t next_stage = ring;
+        const auto page_at = [&](int key) {
+            return next_left > 0 && key < it.hi && key + kStep > it.lo ? table[key >> c.pool.page_shift] : -1;
         };
-        int page_next = page_at(0);
-        const auto issue = [&](int i) {
-            int page = page_next;
-            page_next = page_at(i + 1);
-            if (i < mine) {
-                const int key = key0 + (warp + i * kWarps) * kStep;
+        int page_next = page_at(next_key);
+        const auto issue = [&] {
+            const int page = page_next, key = next_key;
+            const bool any = next_left > 0;
+            next_key += kWarps * kStep;
+            --next_left;
+            page_next = page_at(next_key);
+            if (any) {
                 const bool used = key < it.hi && key + kStep > it.lo;
                 int valid = used ? min(kStep, it.seq.kv - key) : 0;
                 if (used && (page < 0 || page >= c.pool.n_pages)) {
                     kv::report(c.pool.status, kStatusKvAttention);
                     valid = 0;
                 }
-                load_step<FMT, D, NT>(c, valid > 0 ? page : 0, it.head, key & page_mask, valid,
-                                      ring + i % C::kStages * C::kStageBytes, lane);
+                const uint8_t *blk = head_blk + (valid > 0 ? (int64_t)((uint64_t)(uint32_t)page * (uint32_t)c.pool.page_bytes) : 0);
+                load_step<FMT, D, NT>(c, copy, blk, key & page_mask, valid, next_stage, lane);
+                next_stage = next_stage == ring + (C::kStages - 1) * C::kStageBytes ? ring : next_stage + C::kStageBytes;
             }
             cp_async_commit();
         };
 #pragma unroll
         for (int i = 0; i < C::kStages - 1; ++i)
-            issue(i);
+            issue();
 
         // Q rows to f16 fragments (scaled by a power of two), their score factors and key ranges
         for (int r = warp; r < C::kRows; r += kWarps) {
@@ -489,12 +542,18 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                 o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
         }
 
-        for (int i = 0; i < mine; ++i) {
+        float limit[NT][2], base[NT][2];  // top + kSlack, and top or 0 where there is none yet
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            limit[n][0] = limit[n][1] = -INFINITY;
+            base[n][0] = base[n][1] = 0.f;
+        }
+        int key = key0 + warp * kStep;
+        uint32_t stage = ring;
+        for (int i = 0; i < mine; ++i, key += kWarps * kStep) {
             cp_async_wait<C::kStages - 2>();
             __syncwarp();
-            issue(i + C::kStages - 1);
-            const uint32_t stage = ring + i % C::kStages * C::kStageBytes;
-            const int key = key0 + (warp + i * kWarps) * kStep;
+            issue();
 
             float s[NT][4];
 #pragma unroll
@@ -513,14 +572,17 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
             bool over = false;
             {
                 const uint32_t ea = stage + C::kExpAt + g;
-                const float fk[2] = {kv::exp2_byte(lds8(ea)), kv::exp2_byte(lds8(ea + 8))};
+                // K's mark of a row that is not a number reads infinity here, and its codes are zeros: NaN again
+                const float fk[2] = {__uint_as_float(lds8(ea) << 23), __uint_as_float(lds8(ea + 8) << 23)};
                 const uint32_t ev[2] = {lds8(ea + kStep), lds8(ea + kStep + 8)};
                 float kv[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    kv[h] = ev[h] == kv::kNanRow ? NAN : ev[h] == 0 ? -INFINITY : (float)((int)ev[h] - 127);
+                    // the byte as a float: 2^23 + ev - (2^23 + 127)
+                    kv[h] = __uint_as_float(0x4B000000u | ev[h]) - 8388735.f;
+                    kv[h] = ev[h] == kv::kNanRow ? NAN : ev[h] == 0 ? -INFINITY : kv[h];
                     // finite for a NaN row too: masked, its weight of 0 must add 0
-                    unscale[h] = ev[h] == kv::kNanRow ? 1.f : __uint_as_float((254u - ev[h]) << 23) * kSumUnit;
+                    unscale[h] = __uint_as_float((uint32_t)max(254 - (int)ev[h], 0) << 23) * kSumUnit;
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -546,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
             for (int n = 0; n < NT; ++n) {
 #pragma unroll
                 for (int h = 0; h < 4; ++h)
-                    over |= z[n][h] > top[n][h & 1] + kSlack;
+                    over |= z[n][h] > limit[n][h & 1];
             }
             if (__any_sync(0xFFFFFFFFu, over)) {
 #pragma unroll
@@ -560,6 +622,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                         const float next = fmaxf(top[n][h], m - kHeadroom);
                         const float shrink = next == -INFINITY ? 1.f : ex2(top[n][h] - next);
                         top[n][h] = next;
+                        limit[n][h] = next + kSlack;
+                        base[n][h] = next == -INFINITY ? 0.f : next;
                         sum[n][h] *= shrink;
 #pragma unroll
                         for (int k = 0; k < KS; ++k) {
@@ -575,8 +639,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                 float w[4];
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    const float m = top[n][h & 1];
-                    w[h] = ex2(z[n][h] - (m == -INFINITY ? 0.f : m));
+                    w[h] = ex2(z[n][h] - base[n][h & 1]);
                     sum[n][h & 1] = fmaf(w[h], unscale[h >> 1], sum[n][h & 1]);
                 }
 #pragma unroll
@@ -603,6 +666,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                     }
                 }
             });
+            stage = stage == ring + (C::kStages - 1) * C::kStageBytes ? ring : stage + C::kStageBytes;
         }
         cp_async_wait<0>();
         __syncthreads();  // every warp is done with its ring: the arena now holds the warps' results
@@ -630,7 +694,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
         }
         __syncthreads();
 
-        const bool whole = u == item_begin && seg_end == item_end;
+        const bool whole = u == tiles_begin && seg_end == item_end;
         // sums of the CTA: thread handles element pairs of rows; `emit` gets (row, element, values, top, sum)
         const auto merged = [&](auto &&emit) {
             for (int x = tid; x < it.rows * (D / 2); x += kThreads) {
@@ -668,23 +732,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
         if (whole) {
             merged([&](int r, int d, float2 acc, float, float l) { store(r, d, acc, l); });
         } else {
-            const int first = range_owner(range.total, range.ctas, item_begin);
+            const int first = range_owner(range.total, range.ctas, tiles_begin);
             const int last = range_owner(range.total, range.ctas, item_end - 1);
-            float *slot = partials + ((int64_t)blockIdx.x * 2 + (item_begin < range.begin ? 0 : 1)) * C::kSlotFloats;
+            float *slot = partials + ((int64_t)blockIdx.x * 2 + ((int)blockIdx.x == first ? 1 : 0)) * C::kSlotFloats;
             merged([&](int r, int d, float2 acc, float m, float l) {
                 *reinterpret_cast<float2 *>(slot + r * D + d) = acc;
                 if (d == 0)
                     *reinterpret_cast<float2 *>(slot + C::kRows * D + r * 2) = make_float2(m, l);
             });
-            __threadfence();
-            __syncthreads();
+            __syncthreads();  // before the release below: it covers every thread's stores
             if (tid == 0) {
-                const uint32_t seen = atomicAdd(counters + first, 1u);
+                uint32_t seen;
+                asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(seen) : "l"(counters + first) : "memory");
                 const bool done = seen == (uint32_t)(last - first);
                 if (done)
                     counters[first] = 0;
                 scratch[0] = done;
-                __threadfence();
             }
             __syncthreads();
             if (scratch[0]) {
@@ -713,19 +776,22 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                     }
                 }
                 __syncthreads();
-                for (int x = tid; x < it.rows * (D / 2); x += kThreads) {
-                    const int r = x / (D / 2), d = x % (D / 2) * 2;
-                    float2 acc = make_float2(0.f, 0.f);
+                for (int x = tid; x < it.rows * (D / 4); x += kThreads) {
+                    const int r = x / (D / 4), d = x % (D / 4) * 4;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
                     float l = 0.f;
 #pragma unroll 8
                     for (int i = 0; i < n; ++i) {
-                        const float2 v = __ldcg(reinterpret_cast<const float2 *>(slot_of(i) + r * D + d));
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(slot_of(i) + r * D + d));
                         const float f = weight[i * C::kRows + r];
                         acc.x = fmaf(f, v.x, acc.x);
                         acc.y = fmaf(f, v.y, acc.y);
+                        acc.z = fmaf(f, v.z, acc.z);
+                        acc.w = fmaf(f, v.w, acc.w);
                         l = fmaf(f, weight[(n + i) * C::kRows + r], l);
                     }
-                    store(r, d, acc, l);
+                    store(r, d, make_float2(acc.x, acc.y), l);
+                    store(r, d + 2, make_float2(acc.z, acc.w), l);
                 }
             }
         }
@@ -745,6 +811,9 @@ cudaError_t launch(const Call &c, uint8_t *workspace, int num_sms, cudaStream_t 
     static std::once_flag once[kMaxDevices];
     static cudaError_t results[kMaxDevices];
     const auto kernel = decode_kernel<FMT, D, NT, WIDE>;
+    Call call = c;
+    // An item costs a CTA about as much as four of its tiles.  (With few items that does not matter.)
+    call.item_cost = (int64_t)c.n_seqs * c.pool.heads >= 128 ? 4 : 0;
     const cudaError_t e = once_per_device(once, results, [kernel] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
@@ -752,7 +821,7 @@ cudaError_t launch(const Call &c, uint8_t *workspace, int num_sms, cudaStream_t 
         return e;
     constexpr int most = decode_max_ctas(C::kRows);
     const int grid = num_sms * C::kCtasPerSm;
-    kernel<<<grid < most ? grid : most, kThreads, C::kSmem, stream>>>(c, workspace);
+    kernel<<<grid < most ? grid : most, kThreads, C::kSmem, stream>>>(call, workspace);
     return cudaGetLastError();
 }
 

@@ -8,7 +8,9 @@
 // P equal ranges of it, whatever the lengths: long sequences are split over
 // many CTAs, short ones share one, and every CTA has the same number of tiles
 // to within one.  The lengths are on the device, so each CTA finds its range
-// itself.
+// itself.  What an item costs beyond its tiles (its queries, joining the warps,
+// a partial result) can be counted as tiles too: c.item_cost places without
+// work stand before each item's tiles in the list.
 //
 // A CTA that holds a whole item writes its output rows.  Otherwise it leaves
 // its partial result (accumulators, maximum and sum) in one of its two slots
@@ -40,6 +42,7 @@ struct Item {
     int row0, rows;     // rows of the block
     int lo, hi;         // keys that some row of the block may see
     int tile0, tiles;   // first tile (in units of TK keys from key 0) and their number
+    int units;          // places in the list: the tiles, behind `c.item_cost` places without any
 };
 
 // Rows and key range of row block rb of an item's sequence.
@@ -54,6 +57,7 @@ NVFP4_DEVINL void set_block(const Call &c, Item &it)
     it.tile0 = it.lo / TK;
     // an item without keys still has its zeros to write
     it.tiles = max(1, (it.hi + TK - 1) / TK - it.tile0);
+    it.units = it.tiles + c.item_cost;
 }
 
 template <int RB>
@@ -65,16 +69,23 @@ struct Range {
     int ctas;            // that have a range
 };
 
-NVFP4_DEVINL int64_t range_start(int64_t total, int ctas, int cta) { return total * cta / ctas; }
+// (Lists of up to 2^22 tiles divide in 32 bits, which is several times faster.)
+NVFP4_DEVINL int64_t range_start(int64_t total, int ctas, int cta)
+{
+    return total < (1 << 22) ? (int64_t)((uint32_t)total * (uint32_t)cta / (uint32_t)ctas) : total * cta / ctas;
+}
 // The CTA whose range holds tile u.
 NVFP4_DEVINL int range_owner(int64_t total, int ctas, int64_t u)
 {
+    if (total < (1 << 22))
+        return (int)((((uint32_t)u + 1) * (uint32_t)ctas + (uint32_t)total - 1) / (uint32_t)total) - 1;
     return (int)(((u + 1) * ctas + total - 1) / total) - 1;
 }
+static_assert(kMaxCtas < 1 << 9, "32-bit products of tiles and CTAs");
 
 // Every thread of the CTA calls this: this CTA's range, its first item, and
-// the list position of that item's first tile.  `scratch`: shared memory,
-// THREADS / 32 + 4 words of 64 bits.  Returns false if the CTA has no work.
+// the list position of that item's first place.  `scratch`: shared memory,
+// THREADS / 32 + 5 words of 64 bits.  Returns false if the CTA has no work.
 //
 // Row blocks are numbered as if every sequence had as many as the longest can
 // have; thread t sums the t-th run of consecutive numbers (one long sequence
@@ -86,20 +97,20 @@ __device__ bool find_range(const Call &c, int64_t *scratch, Range *range, Item *
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
     const int most = (int)(((int64_t)c.max_q_len * c.group + RB - 1) / RB);  // row blocks of a sequence
     const int64_t numbers = (int64_t)c.n_seqs * most;
-    const int64_t per = (numbers + THREADS - 1) / THREADS;
+    const int64_t per = numbers <= THREADS ? 1 : (numbers + THREADS - 1) / THREADS;
     const int64_t n0 = min(tid * per, numbers), n1 = min(n0 + per, numbers);
     // f(sequence and row block of each number of the run that is there, its tiles over all heads) until it returns true
     const auto each = [&](auto &&f) {
         if (n0 >= n1)
             return;
         Item it;
-        it.b = (int)(n0 / most);
+        it.b = most == 1 ? (int)n0 : (int)(n0 / most);
         it.rb = (int)(n0 - (int64_t)it.b * most);
         it.seq = load_seq(c, it.b);
         for (int64_t i = n0; i < n1; ++i) {
             if (it.rb < row_blocks<RB>(c, it.seq)) {
                 set_block<RB, TK>(c, it);
-                if (f(it, (int64_t)it.tiles * c.pool.heads))
+                if (f(it, (int64_t)it.units * c.pool.heads))
                     return;
             }
             if (++it.rb == most && i + 1 < n1) {
@@ -143,11 +154,13 @@ __device__ bool find_range(const Call &c, int64_t *scratch, Range *range, Item *
                 at += n;
                 return false;
             }
-            const int head = (int)((range->begin - at) / it.tiles);
+            const int head = (int)((range->begin - at) / it.units);
             int64_t *out = scratch + THREADS / 32;
             out[0] = (int64_t)it.b << 32 | it.rb;
             out[1] = head;
-            out[2] = at + (int64_t)head * it.tiles;
+            out[2] = at + (int64_t)head * it.units;
+            out[3] = (int64_t)it.seq.q_begin << 32 | (uint32_t)it.seq.n;
+            out[4] = (int64_t)it.seq.kv << 32 | (uint32_t)it.seq.past;
             return true;
         });
     }
@@ -157,7 +170,7 @@ __device__ bool find_range(const Call &c, int64_t *scratch, Range *range, Item *
     item->rb = (int)(out[0] & 0x7FFFFFFF);
     item->head = (int)out[1];
     *item_begin = out[2];
-    item->seq = load_seq(c, item->b);
+    item->seq = {(int)(out[3] >> 32), (int)out[3], (int)(out[4] >> 32), (int)out[4]};
     set_block<RB, TK>(c, *item);
     return true;
 }
