@@ -8,6 +8,7 @@ missing or fails to load, every call raises: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -82,6 +83,8 @@ def library_path() -> str:
 def load_library():
     """Load libnvfp4.so (built by gemm_nvfp4_gb300.build / __graft_entry__.build())."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -530,8 +533,21 @@ def nvfp4_stream_run(plan: StreamPlan, stream=None) -> None:
 # Quantised paged KV cache and attention over it
 # ---------------------------------------------------------------------------
 
+@functools.lru_cache(maxsize=None)
 def nvfp4_kv_page_bytes(page_size: int, n_kv_heads: int, head_dim: int, format: int) -> int:
-    return load_library().nvfp4_kv_page_bytes(int(page_size), int(n_kv_heads), int(head_dim), int(format))
+    return load_library().nvfp4_kv_page_bytes(page_size, n_kv_heads, head_dim, format)
+
+
+# Handle of the current stream without a Stream object around it: these calls
+# take a few microseconds, and making that object is one or two of them.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(t: torch.Tensor, stream) -> int:
+    """Stream handle: `stream`, or the current one of the device that holds t."""
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(t.get_device()) if _raw_stream else torch.cuda.current_stream(t.device).cuda_stream
 
 
 @dataclass
@@ -562,7 +578,7 @@ class KVCache:
 
     def c(self) -> KVCacheC:
         pool = self.pool
-        n_pages, heads = pool.shape[:2]
+        n_pages, heads = pool.shape[0], pool.shape[1]
         if pool.dtype != torch.uint8 or not pool.is_contiguous() or pool.numel() != n_pages * nvfp4_kv_page_bytes(
                 self.page_size, heads, self.head_dim, self.format):
             raise ValueError("pool is not a contiguous uint8 [n_pages, n_kv_heads, 2, block] of this cache's format")
@@ -576,13 +592,13 @@ def _buffer(t):
 
 def _head_rows(t, heads, head_dim, dtypes, what):
     """Token stride (elements) of [tokens, heads, head_dim] rows whose heads lie side by side."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or t.dtype not in dtypes:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != head_dim or t.dtype not in dtypes:
         raise ValueError(f"{what} must be {' or '.join(str(d) for d in dtypes)} [tokens, {heads}, {head_dim}], "
-                         f"got {t.dtype} {list(t.shape)}")
-    tokens, by_head, by_elem = t.stride()
-    if by_elem != 1 or (heads > 1 and by_head != head_dim):
-        raise ValueError(f"{what}: the heads of a token must lie side by side (strides {t.stride()})")
-    return tokens if t.shape[0] > 1 else max(tokens, heads * head_dim)
+                         f"got {t.dtype} {list(shape)}")
+    if stride[2] != 1 or (heads > 1 and stride[1] != head_dim):
+        raise ValueError(f"{what}: the heads of a token must lie side by side (strides {stride})")
+    return stride[0] if shape[0] > 1 else max(stride[0], heads * head_dim)
 
 
 _BF16 = (torch.bfloat16,)
@@ -606,8 +622,9 @@ def nvfp4_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: tor
     _check_slots(slots, k.shape[0])
     ws, ws_bytes = _buffer(workspace)
     st = load_library().nvfp4_kv_append(ctypes.byref(c), k.data_ptr(), k_ld, v.data_ptr(), v_ld, slots.data_ptr(),
-                                        k.shape[0], ws, ws_bytes, _stream(stream))
-    _check(st, "nvfp4_kv_append")
+                                        k.shape[0], ws, ws_bytes, _stream_of(slots, stream))
+    if st:
+        _check(st, "nvfp4_kv_append")
 
 
 def nvfp4_kv_read(cache: KVCache, slots: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None,
@@ -625,8 +642,9 @@ def nvfp4_kv_read(cache: KVCache, slots: torch.Tensor, out: tuple[torch.Tensor, 
     _check_slots(slots, v.shape[0])
     ws, ws_bytes = _buffer(workspace)
     st = load_library().nvfp4_kv_read(ctypes.byref(c), k.data_ptr(), k_ld, v.data_ptr(), v_ld, slots.data_ptr(),
-                                      k.shape[0], ws, ws_bytes, _stream(stream))
-    _check(st, "nvfp4_kv_read")
+                                      k.shape[0], ws, ws_bytes, _stream_of(slots, stream))
+    if st:
+        _check(st, "nvfp4_kv_read")
     return out
 
 
@@ -638,7 +656,7 @@ def nvfp4_paged_attention_workspace_bytes(cache: KVCache, q: torch.Tensor, n_seq
 
 
 def _device_ints(t, dtype, shape, what):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dtype} {list(shape)}, got {t.dtype} {list(t.shape)}")
     return t.data_ptr()
 
@@ -689,7 +707,8 @@ def nvfp4_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Te
         # zero-filled: the call keeps arrival counters in it
         workspace = torch.zeros(lib.nvfp4_paged_attention_workspace_bytes(ctypes.byref(a)), dtype=torch.uint8,
                                 device=q.device)
-    st = lib.nvfp4_paged_attention(ctypes.byref(a), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                   _stream(stream))
-    _check(st, "nvfp4_paged_attention")
+    ws, ws_bytes = _buffer(workspace)
+    st = lib.nvfp4_paged_attention(ctypes.byref(a), ws, ws_bytes, _stream_of(q, stream))
+    if st:
+        _check(st, "nvfp4_paged_attention")
     return out

@@ -67,140 +67,200 @@ NVFP4_DEVINL int row_exponent(float amax)
 
 NVFP4_DEVINL float pow2f(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
 
-// Shared by both kernels: which row a group of lanes works on.  Rows are
-// ordered (token, K or V, head), so a token's K rows are neighbours, as in k.
-struct RowId {
+// Rows of one pass of a group of lanes: their loads are all on their way before
+// the first is used.
+constexpr int kRowsAtOnce = 4;
+
+// A group of lanes has one token and walks over its rows (K's heads, then V's),
+// so that the slot is looked up once.  The groups of a CTA have consecutive
+// tokens, which mostly lie in one page: together they touch whole runs of
+// its codes, scales and exponents.  (With a token's heads side by side in a
+// CTA instead, every 8 bytes of scales and byte of exponent cost a sector of
+// their own, and reading 65536 NVFP4 tokens of 8 heads back took 98 us.)
+// Few tokens are shared out by rows as well, `rows` of a token to a CTA.
+struct RowWalk {
     uint32_t token;
-    int is_v, head;
+    int begin, end;
 };
 
-NVFP4_DEVINL RowId row_id(uint32_t r, uint32_t heads)
+template <int L>
+NVFP4_DEVINL RowWalk row_walk(int heads, int rows)
 {
-    RowId id;
-    id.token = r / (2 * heads);
-    const uint32_t rest = r - id.token * 2 * heads;
-    id.is_v = rest >= heads;
-    id.head = (int)(rest - (id.is_v ? heads : 0));
-    return id;
+    RowWalk w;
+    w.token = blockIdx.x * (kThreads / L) + threadIdx.x / L;
+    w.begin = (int)blockIdx.y * rows;
+    w.end = min(w.begin + rows, 2 * heads);
+    return w;
+}
+
+// A row's place in the pool; slot < 0 for a row that is left out.
+struct Place {
+    int64_t page;
+    int at;
+    bool there;
+};
+
+NVFP4_DEVINL Place place_of(const Pool &pool, int64_t slot, bool report_it, uint32_t code)
+{
+    Place p;
+    p.page = slot >> pool.page_shift;
+    p.at = (int)(slot & ((1 << pool.page_shift) - 1));
+    p.there = slot >= 0 && p.page < pool.n_pages;
+    if (slot >= 0 && !p.there && report_it)
+        report(pool.status, code);
+    return p;
+}
+
+// y / s rounded to E2M1 (nearest, ties to even), for two elements of a lane:
+// lo in bits 0..3.  y is a bf16 value times a power of two (8 significant
+// bits), s an E4M3 value (4 bits), r = 1 / s to within an ulp.  A quotient that is
+// not a tie between two codes (3 bits times s: at most 7) is off it by more than
+// 2^-9 of itself, and y * r is off the quotient by less than 2^-21: rounding y * r
+// to 12 bits makes every tie exact and moves no other quotient across one.
+NVFP4_DEVINL uint32_t e2m1_codes(float y0, float y1, float r)
+{
+    const float q0 = __uint_as_float((__float_as_uint(y0 * r) + 0x800u) & ~0xFFFu);
+    const float q1 = __uint_as_float((__float_as_uint(y1 * r) + 0x800u) & ~0xFFFu);
+    return f32x2_to_e2m1x2(q0, q1);
 }
 
 template <int FMT, int D>
 __global__ void __launch_bounds__(kThreads) append_kernel(Pool pool, const uint16_t *__restrict__ k, int64_t k_ld,
                                                           const uint16_t *__restrict__ v, int64_t v_ld,
-                                                          const int64_t *__restrict__ slots, uint32_t n_rows)
+                                                          const int64_t *__restrict__ slots, uint32_t n_tokens,
+                                                          int rows)
 {
-    constexpr int L = D / 8;  // lanes of a row
+    constexpr int L = D / 8, U = kRowsAtOnce;  // lanes of a row
     using R = Row<FMT, D>;
     const int lane = threadIdx.x % L;
-    const uint32_t per_grid = gridDim.x * (kThreads / L);
-    const uint32_t rounds = (n_rows + per_grid - 1) / per_grid;
-    uint32_t r = blockIdx.x * (kThreads / L) + threadIdx.x / L;
-    for (uint32_t it = 0; it < rounds; ++it, r += per_grid) {
-        // every lane stays for the shuffles; rows beyond the end store nothing
-        const bool live = r < n_rows;
-        const RowId id = row_id(live ? r : 0, pool.heads);
-        const int64_t slot = live ? slots[id.token] : -1;
-        const uint16_t *src = id.is_v ? v + (int64_t)id.token * v_ld : k + (int64_t)id.token * k_ld;
-        const uint4 x = ldg_v4(src + (int64_t)id.head * D + lane * 8);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        // maximum of the magnitudes as integers: NaN and infinity come out on top
-        uint32_t m2 = 0;
+    const uint32_t group_lanes = ((1u << L) - 1) << (threadIdx.x % 32 / L * L);
+    const RowWalk w = row_walk<L>(pool.heads, rows);
+    if (w.token >= n_tokens)
+        return;
+    const Place p = place_of(pool, slots[w.token], lane == 0, kStatusKvAppendSlot);
+    if (!p.there)
+        return;
+    uint8_t *const page = block_ptr(pool, p.page, 0, 0);
+    const uint16_t *const k_row = k + w.token * k_ld + lane * 8, *const v_row = v + w.token * v_ld + lane * 8;
+    for (int j = w.begin; j < w.end; j += U) {
+        uint4 x[U];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            m2 = __vmaxu2(m2, w[i] & 0x7FFF7FFFu);
-        uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        const uint32_t block_max = m;  // of this lane pair's 16 elements
-#pragma unroll
-        for (int o = 2; o < L; o *= 2)
-            m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        if (!live || slot < 0)
-            continue;
-        const int64_t page = slot >> pool.page_shift;
-        if (page >= pool.n_pages) {
-            if (lane == 0)
-                report(pool.status, kStatusKvAppendSlot);
-            continue;
+        for (int u = 0; u < U; ++u) {
+            const int head = j + u < pool.heads ? j + u : j + u - pool.heads;
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (j + u < w.end)
+                x[u] = ldg_v4((j + u < pool.heads ? k_row : v_row) + head * D);
         }
-        const int at = (int)(slot & ((1 << pool.page_shift) - 1));
-        int ke = row_exponent<FMT>(__uint_as_float(m << 16));
-        const bool bad = m >= 0x7F80u || ke > kExpMax;
-        const float unit = pow2f(bad ? 0 : -ke);
-        float y[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            y[2 * i] = bad ? 0.f : __uint_as_float(w[i] << 16) * unit;
-            y[2 * i + 1] = bad ? 0.f : __uint_as_float(w[i] & 0xFFFF0000u) * unit;
-        }
-        uint8_t *blk = block_ptr(pool, page, id.head, id.is_v);
-        if constexpr (FMT == NVFP4_KV_E4M3) {
-            uint2 c;
-            c.x = f32x2_to_e4m3x2(y[0], y[1]) | f32x2_to_e4m3x2(y[2], y[3]) << 16;
-            c.y = f32x2_to_e4m3x2(y[4], y[5]) | f32x2_to_e4m3x2(y[6], y[7]) << 16;
-            *reinterpret_cast<uint2 *>(blk + at * R::kCode + lane * 8) = c;
-        } else {
-            const uint32_t sb = bad ? 0u
-                                    : f32_to_e4m3_satfinite(__fdiv_rn(__uint_as_float(block_max << 16), 6.f) * unit);
-            const float s = e4m3_to_f32(sb);
-            uint32_t c = 0;
-            if (sb != 0) {
+        for (int u = 0; u < U; ++u) {
+            if (j + u >= w.end)
+                break;
+            const int is_v = j + u >= pool.heads, head = j + u - (is_v ? pool.heads : 0);
+            const uint32_t e[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            // maximum of the magnitudes as integers: NaN and infinity come out on top
+            uint32_t m2 = __vmaxu2(__vmaxu2(e[0] & 0x7FFF7FFFu, e[1] & 0x7FFF7FFFu),
+                                   __vmaxu2(e[2] & 0x7FFF7FFFu, e[3] & 0x7FFF7FFFu));
+            uint32_t m = max(m2 & 0xFFFFu, m2 >> 16);
+            m = max(m, __shfl_xor_sync(group_lanes, m, 1));
+            const uint32_t block_max = m;  // of this lane pair's 16 elements
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    c |= f32x2_to_e2m1x2(__fdiv_rn(y[2 * i], s), __fdiv_rn(y[2 * i + 1], s)) << (8 * i);
+            for (int o = 2; o < L; o *= 2)
+                m = max(m, __shfl_xor_sync(group_lanes, m, o));
+            int ke = row_exponent<FMT>(__uint_as_float(m << 16));
+            const bool bad = m >= 0x7F80u || ke > kExpMax;
+            const float unit = pow2f(bad ? 0 : -ke);
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[2 * i] = bad ? 0.f : __uint_as_float(e[i] << 16) * unit;
+                y[2 * i + 1] = bad ? 0.f : __uint_as_float(e[i] & 0xFFFF0000u) * unit;
             }
-            *reinterpret_cast<uint32_t *>(blk + at * R::kCode + lane * 4) = c;
-            if (lane % 2 == 0)
-                blk[(R::kCode << pool.page_shift) + at * R::kScale + lane / 2] = (uint8_t)sb;
+            uint8_t *blk = page + (int64_t)(head * 2 + is_v) * pool.block_bytes;
+            if constexpr (FMT == NVFP4_KV_E4M3) {
+                uint2 c;
+                c.x = f32x2_to_e4m3x2(y[0], y[1]) | f32x2_to_e4m3x2(y[2], y[3]) << 16;
+                c.y = f32x2_to_e4m3x2(y[4], y[5]) | f32x2_to_e4m3x2(y[6], y[7]) << 16;
+                *reinterpret_cast<uint2 *>(blk + p.at * R::kCode + lane * 8) = c;
+            } else {
+                const uint32_t sb =
+                    bad ? 0u : f32_to_e4m3_satfinite(__fdiv_rn(__uint_as_float(block_max << 16), 6.f) * unit);
+                uint32_t c = 0;
+                if (sb != 0) {
+                    const float r = 1.f / e4m3_to_f32(sb);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        c |= e2m1_codes(y[2 * i], y[2 * i + 1], r) << (8 * i);
+                }
+                *reinterpret_cast<uint32_t *>(blk + p.at * R::kCode + lane * 4) = c;
+                if (lane % 2 == 0)
+                    blk[(R::kCode << pool.page_shift) + p.at * R::kScale + lane / 2] = (uint8_t)sb;
+            }
+            if (lane == 0)
+                blk[((R::kCode + R::kScale) << pool.page_shift) + p.at] =
+                    (uint8_t)(bad ? kNanRow : (uint32_t)(ke + 127));
         }
-        if (lane == 0)
-            blk[((R::kCode + R::kScale) << pool.page_shift) + at] = (uint8_t)(bad ? kNanRow : (uint32_t)(ke + 127));
     }
 }
 
 template <int FMT, int D>
 __global__ void __launch_bounds__(kThreads) read_kernel(Pool pool, uint16_t *__restrict__ k, int64_t k_ld,
                                                         uint16_t *__restrict__ v, int64_t v_ld,
-                                                        const int64_t *__restrict__ slots, uint32_t n_rows)
+                                                        const int64_t *__restrict__ slots, uint32_t n_tokens, int rows)
 {
-    constexpr int L = D / 8;
+    constexpr int L = D / 8, U = kRowsAtOnce;
     using R = Row<FMT, D>;
     const int lane = threadIdx.x % L;
-    const uint32_t per_grid = gridDim.x * (kThreads / L);
-    for (uint32_t r = blockIdx.x * (kThreads / L) + threadIdx.x / L; r < n_rows;
-         r = r + per_grid < r ? n_rows : r + per_grid) {
-        const RowId id = row_id(r, pool.heads);
-        const int64_t slot = slots[id.token];
-        const int64_t page = slot >> pool.page_shift;
-        uint4 out = make_uint4(0, 0, 0, 0);
-        if (page >= pool.n_pages) {
-            if (lane == 0)
-                report(pool.status, kStatusKvReadSlot);
-        } else if (slot >= 0) {
-            const int at = (int)(slot & ((1 << pool.page_shift) - 1));
-            const uint8_t *blk = block_ptr(pool, page, id.head, id.is_v);
-            const float unit = exp2_byte(blk[((R::kCode + R::kScale) << pool.page_shift) + at]);
+    const RowWalk w = row_walk<L>(pool.heads, rows);
+    if (w.token >= n_tokens)
+        return;
+    const Place p = place_of(pool, slots[w.token], lane == 0, kStatusKvReadSlot);
+    const uint8_t *const page = block_ptr(pool, p.there ? p.page : 0, 0, 0);
+    uint16_t *const k_row = k + w.token * k_ld + lane * 8, *const v_row = v + w.token * v_ld + lane * 8;
+    for (int j = w.begin; j < w.end; j += U) {
+        uint2 code[U];
+        uint32_t exps[U], scale[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            code[u] = make_uint2(0, 0);
+            exps[u] = 127;
+            scale[u] = 0;
+            if (p.there && j + u < w.end) {
+                const int is_v = j + u >= pool.heads, head = j + u - (is_v ? pool.heads : 0);
+                const uint8_t *blk = page + (int64_t)(head * 2 + is_v) * pool.block_bytes;
+                exps[u] = blk[((R::kCode + R::kScale) << pool.page_shift) + p.at];
+                if constexpr (FMT == NVFP4_KV_E4M3) {
+                    code[u] = *reinterpret_cast<const uint2 *>(blk + p.at * R::kCode + lane * 8);
+                } else {
+                    code[u].x = *reinterpret_cast<const uint32_t *>(blk + p.at * R::kCode + lane * 4);
+                    scale[u] = blk[(R::kCode << pool.page_shift) + p.at * R::kScale + lane / 2];
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (j + u >= w.end)
+                break;
             uint32_t o[4];
+            const float unit = exp2_byte(exps[u]);
             if constexpr (FMT == NVFP4_KV_E4M3) {
-                const uint2 c = *reinterpret_cast<const uint2 *>(blk + at * R::kCode + lane * 8);
-                const uint32_t two[4] = {c.x & 0xFFFFu, c.x >> 16, c.y & 0xFFFFu, c.y >> 16};
+                const uint32_t two[4] = {code[u].x & 0xFFFFu, code[u].x >> 16, code[u].y & 0xFFFFu, code[u].y >> 16};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 f = f16x2_to_f32(e4m3x2_to_f16x2((uint16_t)two[i]));
                     o[i] = f32x2_to_bf16x2(f.x * unit, f.y * unit);
                 }
             } else {
-                const uint32_t c = *reinterpret_cast<const uint32_t *>(blk + at * R::kCode + lane * 4);
-                const float s = e4m3_to_f32(blk[(R::kCode << pool.page_shift) + at * R::kScale + lane / 2]) * unit;
+                const float s = e4m3_to_f32(scale[u]) * unit;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float2 f = f16x2_to_f32(e2m1x2_to_f16x2(c >> (8 * i) & 0xFFu));
+                    const float2 f = f16x2_to_f32(e2m1x2_to_f16x2(code[u].x >> (8 * i) & 0xFFu));
                     o[i] = f32x2_to_bf16x2(f.x * s, f.y * s);
                 }
             }
-            out = make_uint4(o[0], o[1], o[2], o[3]);
+            const int is_v = j + u >= pool.heads;
+            *reinterpret_cast<uint4 *>((is_v ? v_row : k_row) + (j + u - (is_v ? pool.heads : 0)) * D) =
+                make_uint4(o[0], o[1], o[2], o[3]);
         }
-        uint16_t *dst = id.is_v ? v + (int64_t)id.token * v_ld : k + (int64_t)id.token * k_ld;
-        *reinterpret_cast<uint4 *>(dst + (int64_t)id.head * D + lane * 8) = out;
     }
 }
 
@@ -235,12 +295,15 @@ int check_rows(const nvfp4_kv_cache *c, const void *k, int64_t k_ld, const void 
     return NVFP4_OK;
 }
 
-// One round of resident CTAs at most; each group of lanes strides over rows.
-uint32_t row_grid(uint32_t n_rows, int head_dim)
+// Grid for n_tokens, and the rows of a token that a CTA walks over: all, unless
+// that leaves most of the SMs without a CTA.
+dim3 row_grid(uint32_t n_tokens, const nvfp4_kv_cache *c, int *rows)
 {
-    const uint32_t per_cta = kThreads / (head_dim / 8);
-    const uint32_t need = (n_rows + per_cta - 1) / per_cta;
-    return need < 152 * 8 ? need : 152 * 8;
+    const uint32_t per_cta = kThreads / (c->head_dim / 8), all = 2 * c->n_kv_heads;
+    const uint32_t ctas = (n_tokens + per_cta - 1) / per_cta;
+    const uint32_t parts = ctas >= 152 * 4 ? 1 : 152 * 4 / ctas;
+    *rows = (int)(parts >= all ? 1 : (all + parts - 1) / parts);
+    return dim3(ctas, (all + *rows - 1) / *rows);
 }
 
 }  // namespace
@@ -298,11 +361,11 @@ int nvfp4_kv_append(const nvfp4_kv_cache *cache, const uint16_t *k, int64_t k_ld
         rc = kv::check_rows(cache, k, k_ld, v, v_ld, slots, n_tokens);
     if (rc != NVFP4_OK || n_tokens == 0)
         return rc;
-    const uint32_t rows = (uint32_t)(n_tokens * 2 * cache->n_kv_heads);
-    const uint32_t grid = kv::row_grid(rows, cache->head_dim);
+    int rows = 0;
+    const dim3 grid = kv::row_grid((uint32_t)n_tokens, cache, &rows);
     kv::by_format(cache, [&](auto fmt, auto d) {
         kv::append_kernel<fmt.value, d.value>
-            <<<grid, kv::kThreads, 0, (cudaStream_t)stream>>>(pool, k, k_ld, v, v_ld, slots, rows);
+            <<<grid, kv::kThreads, 0, (cudaStream_t)stream>>>(pool, k, k_ld, v, v_ld, slots, (uint32_t)n_tokens, rows);
     });
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
@@ -317,11 +380,11 @@ int nvfp4_kv_read(const nvfp4_kv_cache *cache, uint16_t *k, int64_t k_ld, uint16
         rc = kv::check_rows(cache, k, k_ld, v, v_ld, slots, n_tokens);
     if (rc != NVFP4_OK || n_tokens == 0)
         return rc;
-    const uint32_t rows = (uint32_t)(n_tokens * 2 * cache->n_kv_heads);
-    const uint32_t grid = kv::row_grid(rows, cache->head_dim);
+    int rows = 0;
+    const dim3 grid = kv::row_grid((uint32_t)n_tokens, cache, &rows);
     kv::by_format(cache, [&](auto fmt, auto d) {
         kv::read_kernel<fmt.value, d.value>
-            <<<grid, kv::kThreads, 0, (cudaStream_t)stream>>>(pool, k, k_ld, v, v_ld, slots, rows);
+            <<<grid, kv::kThreads, 0, (cudaStream_t)stream>>>(pool, k, k_ld, v, v_ld, slots, (uint32_t)n_tokens, rows);
     });
     return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
