@@ -981,6 +981,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
     static_assert(sizeof(Shared) <= C::kSmem - C::kBarAt, "barriers");
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid / 32, 0);
 
+    tc::griddep_launch_dependents();
+    tc::griddep_wait();
     Range range;
     Item item;
     int64_t item_begin;
@@ -1070,8 +1072,8 @@ cudaError_t launch(const Call &c, uint8_t *workspace, int num_sms, cudaStream_t 
     });
     if (e != cudaSuccess)
         return e;
-    kernel<<<num_sms < kMaxChunkCtas ? num_sms : kMaxChunkCtas, kThreads, C::kSmem, stream>>>(c, workspace);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3(num_sms < kMaxChunkCtas ? num_sms : kMaxChunkCtas), kThreads, C::kSmem, stream, c,
+                            workspace);
 }
 
 template <int FMT>

@@ -414,6 +414,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
     int64_t *const scratch = reinterpret_cast<int64_t *>(q_tree + C::kRows);
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32, g = lane / 4, t = lane % 4;
 
+    tc::griddep_launch_dependents();
+    tc::griddep_wait();
     Range range;
     Item it;
     int64_t item_begin;
@@ -821,8 +823,7 @@ cudaError_t launch(const Call &c, uint8_t *workspace, int num_sms, cudaStream_t 
         return e;
     constexpr int most = decode_max_ctas(C::kRows);
     const int grid = num_sms * C::kCtasPerSm;
-    kernel<<<grid < most ? grid : most, kThreads, C::kSmem, stream>>>(call, workspace);
-    return cudaGetLastError();
+    return launch_dependent(kernel, dim3(grid < most ? grid : most), kThreads, C::kSmem, stream, call, workspace);
 }
 
 template <int FMT, int D, bool WIDE>

@@ -135,4 +135,23 @@ constexpr size_t kKvWorkspaceBytes = 256;     // append and read: the status wor
 // Streaming multiprocessors of the current device, cached per device; an nvfp4_status.
 int current_num_sms(int *out);
 
+// Launch as a programmatic dependent of the kernel before it on the stream: the
+// launch and the kernel's set-up overlap that kernel's end.  The kernel waits
+// (griddepcontrol.wait) before its first access to global memory.
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args)
+{
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 }  // namespace nvfp4

@@ -10,6 +10,7 @@
 
 #include "kernels.h"
 #include "kv_layout.cuh"
+#include "tcgen05.cuh"
 
 namespace nvfp4 {
 namespace kv {
@@ -135,6 +136,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(Pool pool, const uint1
     const int lane = threadIdx.x % L;
     const uint32_t group_lanes = ((1u << L) - 1) << (threadIdx.x % 32 / L * L);
     const RowWalk w = row_walk<L>(pool.heads, rows);
+    tc::griddep_launch_dependents();
+    tc::griddep_wait();
     if (w.token >= n_tokens)
         return;
     const Place p = place_of(pool, slots[w.token], lane == 0, kStatusKvAppendSlot);
@@ -211,6 +214,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(Pool pool, uint16_t *__r
     using R = Row<FMT, D>;
     const int lane = threadIdx.x % L;
     const RowWalk w = row_walk<L>(pool.heads, rows);
+    tc::griddep_launch_dependents();
+    tc::griddep_wait();
     if (w.token >= n_tokens)
         return;
     const Place p = place_of(pool, slots[w.token], lane == 0, kStatusKvReadSlot);
@@ -363,11 +368,12 @@ int nvfp4_kv_append(const nvfp4_kv_cache *cache, const uint16_t *k, int64_t k_ld
         return rc;
     int rows = 0;
     const dim3 grid = kv::row_grid((uint32_t)n_tokens, cache, &rows);
+    cudaError_t e = cudaSuccess;
     kv::by_format(cache, [&](auto fmt, auto d) {
-        kv::append_kernel<fmt.value, d.value>
-            <<<grid, kv::kThreads, 0, (cudaStream_t)stream>>>(pool, k, k_ld, v, v_ld, slots, (uint32_t)n_tokens, rows);
+        e = launch_dependent(kv::append_kernel<fmt.value, d.value>, grid, kv::kThreads, 0, (cudaStream_t)stream, pool, k,
+                             k_ld, v, v_ld, slots, (uint32_t)n_tokens, rows);
     });
-    return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+    return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
 int nvfp4_kv_read(const nvfp4_kv_cache *cache, uint16_t *k, int64_t k_ld, uint16_t *v, int64_t v_ld,
@@ -382,11 +388,12 @@ int nvfp4_kv_read(const nvfp4_kv_cache *cache, uint16_t *k, int64_t k_ld, uint16
         return rc;
     int rows = 0;
     const dim3 grid = kv::row_grid((uint32_t)n_tokens, cache, &rows);
+    cudaError_t e = cudaSuccess;
     kv::by_format(cache, [&](auto fmt, auto d) {
-        kv::read_kernel<fmt.value, d.value>
-            <<<grid, kv::kThreads, 0, (cudaStream_t)stream>>>(pool, k, k_ld, v, v_ld, slots, (uint32_t)n_tokens, rows);
+        e = launch_dependent(kv::read_kernel<fmt.value, d.value>, grid, kv::kThreads, 0, (cudaStream_t)stream, pool, k, k_ld,
+                             v, v_ld, slots, (uint32_t)n_tokens, rows);
     });
-    return cudaGetLastError() == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+    return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
 }  // extern "C"
