@@ -12,7 +12,7 @@
 //                   the f16 A operand of the second product, over the scores.
 //   warp 18         bulk copies of a tile's codes, scales and exponents from the
 //                   pages to shared memory, ahead of their conversion.
-//   warps 8-15      codes to f16, from there to the layout of the MMA's B operands
+//   warps 8-11, 12-15  codes of K, and of V, to f16, from there to the layout of the MMA's B operands
 //                   (K with the head dimension contiguous; V likewise, read
 //                   transposed).
 //   warps 16, 17    MMA issue for row tile 0 and 1: S = Q K^T, O += P V.
@@ -45,10 +45,10 @@ namespace chunk {
 constexpr int kTile = 128;                      // keys of a tile
 constexpr int kRowTile = 128;                   // rows of a row tile
 constexpr int kSoftmaxWarps = 8, kConvertWarps = 8;
-constexpr int kConvertThreads = 32 * kConvertWarps;
+constexpr int kConvertThreads = 32 * kConvertWarps / 2;  // of K, and as many of V
 constexpr int kThreads = 32 * (kSoftmaxWarps + kConvertWarps + 4);  // whole warpgroups; warp 19 idles
 // Registers of a thread by role: what the launch gives every thread, shared out anew.
-constexpr int kSoftmaxRegs = 136, kConvertRegs = 64, kMmaRegs = 72, kLaunchRegs = 96;
+constexpr int kSoftmaxRegs = 128, kConvertRegs = 72, kMmaRegs = 72, kLaunchRegs = 96;
 static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kConvertWarps * kConvertRegs + 4 * kMmaRegs) <= kThreads * kLaunchRegs,
               "setmaxnreg would wait for registers that nobody gives back");
 constexpr int kStages = 2;
@@ -66,11 +66,11 @@ struct Cfg {
     static constexpr int kRows = SPLIT ? kRowTile : 2 * kRowTile;
     static constexpr int kOperand = 128 * D * 2;  // Q, K or V tile in f16
     static constexpr int kQAt = 0, kKAt = (SPLIT ? 1 : 2) * kOperand, kVAt = kKAt + kStages * kOperand;
-    // a tile's bytes as they lie in the pages: K's codes, scales, exponents and V's exponents; V's codes and scales
+    // a tile's bytes as they lie in the pages: K's codes, scales, exponents and V's exponents; the same of V without K's
     static constexpr int kRawRows = kTile * (R::kCode + R::kScale);
     static constexpr int kRawKAt = kVAt + kStages * kOperand, kRawVAt = kRawKAt + kRawRows + 2 * kTile;
-    static constexpr int kBarAt = kRawVAt + kRawRows;
-    static constexpr int kSmem = kBarAt + 2816;
+    static constexpr int kBarAt = kRawVAt + kRawRows + kTile;
+    static constexpr int kSmem = kBarAt + 2688;
     static constexpr int kSlotFloats = kRows * (D + 2);
     // tensor memory columns
     static constexpr int kScoreCols = 0, kOutCols = 2 * kTile;
@@ -108,7 +108,7 @@ struct Shared {
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t q_ready[2], s_full[2][2], p_ready[2][2], pv_done[2][2], drain[2];  // by group, and half of the keys
     TileInfo info[kInfos];
-    RawInfo raw;
+    RawInfo raw[2];  // K's and V's
     Segment seg;
     uint32_t tmem, last;
     int64_t scratch[kThreads / 32 + 5];
@@ -318,7 +318,7 @@ NVFP4_DEVINL bool load_role(const Call &c, const Range &range, const Item &first
         if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
             break;
         if (lane == 0) {
-            sh->raw = info;
+            sh->raw[0] = info;
             tc::mbar_arrive_expect_tx(&sh->raw_k_full, copied * run * (R::kCode + R::kScale + 2));
         }
         __syncwarp();
@@ -336,8 +336,10 @@ NVFP4_DEVINL bool load_role(const Call &c, const Range &range, const Item &first
             ++tile;  // K's copies of this tile are in flight
             break;
         }
-        if (lane == 0)
-            tc::mbar_arrive_expect_tx(&sh->raw_v_full, copied * run * (R::kCode + R::kScale));
+        if (lane == 0) {
+            sh->raw[1] = info;
+            tc::mbar_arrive_expect_tx(&sh->raw_v_full, copied * run * (R::kCode + R::kScale + 1));
+        }
         __syncwarp();
         if (there) {
             const uint32_t dst = smem + C::kRawVAt;
@@ -345,6 +347,7 @@ NVFP4_DEVINL bool load_role(const Call &c, const Range &range, const Item &first
             if (R::kScale)
                 tc::bulk_load_a(dst + kTile * R::kCode + lane * run * R::kScale, v + scales + at * R::kScale,
                                 run * R::kScale, v_full);
+            tc::bulk_load_a(dst + C::kRawRows + lane * run, v + exps + at, run, v_full);
         }
     }
     // nothing is in flight when the warp leaves
@@ -446,69 +449,59 @@ NVFP4_DEVINL void convert(uint32_t raw, uint32_t operand, int tid, const uint32_
     }
 }
 
+// Four warps have K's tiles and four V's, so that one's waits and fences overlap
+// the other's arithmetic (the same eight warps doing K, then V, of each tile took
+// 2400 clocks a tile).
 template <int FMT, int D, bool SPLIT>
-NVFP4_DEVINL bool convert_role(uint32_t tiles, Shared *sh, uint32_t smem, int tid)
+NVFP4_DEVINL bool convert_role(uint32_t tiles, Shared *sh, uint32_t smem, int is_v, int tid)
 {
     using C = Cfg<FMT, D, SPLIT>;
     constexpr int per = C::kPerBlock, mine = C::kRowsMine;
     const int lane = tid % 32;
+    uint64_t *const raw_full = is_v ? &sh->raw_v_full : &sh->raw_k_full;
+    uint64_t *const raw_empty = is_v ? &sh->raw_v_empty : &sh->raw_k_empty;
+    uint64_t *const full = is_v ? sh->v_full : sh->k_full, *const empty = is_v ? sh->v_empty : sh->k_empty;
+    const uint32_t raw = smem + (is_v ? C::kRawVAt : C::kRawKAt), operand = smem + (is_v ? C::kVAt : C::kKAt);
     for (uint32_t tile = 0; tile < tiles; ++tile) {
         const uint32_t st = tile % kStages, ph = (tile / kStages) & 1;
-        bool ok = tc::mbar_wait(&sh->raw_k_full, tile & 1);
-        ok = ok && (tile < kStages || tc::mbar_wait(&sh->k_empty[st], ph ^ 1));
+        bool ok = tc::mbar_wait(raw_full, tile & 1);
+        ok = ok && (tile < kStages || tc::mbar_wait(&empty[st], ph ^ 1));
         if (!__all_sync(0xFFFFFFFFu, ok))
             return false;
         // exponents of rows 4 lane .. 4 lane + 3, a byte each; 0: no row that anyone sees
-        const RawInfo info = sh->raw;
-        uint32_t ek = tc::lds32(smem + C::kRawKAt + C::kRawRows + 4 * lane);
-        uint32_t ev = tc::lds32(smem + C::kRawKAt + C::kRawRows + kTile + 4 * lane);
+        const RawInfo info = sh->raw[is_v];
+        uint32_t own = tc::lds32(raw + C::kRawRows + 4 * lane);
+        uint32_t other = is_v ? own : tc::lds32(raw + C::kRawRows + kTile + 4 * lane);
         const int first = info.key0 + 4 * lane;
         uint32_t keep = info.present >> (lane / 4) & 1 ? 0xFFFFFFFFu : 0u;
         if (first < info.lo)
             keep = first + 4 <= info.lo ? 0u : keep << (8 * (info.lo - first));
         if (first + 4 > info.hi)
             keep &= first >= info.hi ? 0u : 0xFFFFFFFFu >> (8 * (first + 4 - info.hi));
-        ek &= keep;
-        ev &= keep;
-        const int ku = largest_exp(ek), vu = largest_exp(ev);
-        uint32_t unit[mine], v_unit[mine], rows[mine];
+        own &= keep;
+        other &= keep;
+        const int top = largest_exp(own);
+        uint32_t unit[mine], rows[mine];
 #pragma unroll
         for (int i = 0; i < mine; ++i) {
             const int row = tid / per + i * C::kRowStep, sh8 = 8 * (row & 3);
-            const uint32_t a = __shfl_sync(0xFFFFFFFFu, ek, row >> 2) >> sh8 & 0xFFu;
-            const uint32_t b = __shfl_sync(0xFFFFFFFFu, ev, row >> 2) >> sh8 & 0xFFu;
-            // a row that is not a number makes its scores NaN, whichever of K and V it is
-            unit[i] = a == kv::kNanRow || b == kv::kNanRow ? 0x7FFF7FFFu : pow2_f16x2((int)a - ku);
-            v_unit[i] = b == kv::kNanRow ? 0u : pow2_f16x2((int)b - vu);
+            const uint32_t a = __shfl_sync(0xFFFFFFFFu, own, row >> 2) >> sh8 & 0xFFu;
+            const uint32_t b = __shfl_sync(0xFFFFFFFFu, other, row >> 2) >> sh8 & 0xFFu;
+            // a row that is not a number makes its scores NaN, whichever of K and V it is, and V's are zero
+            unit[i] = a == kv::kNanRow || b == kv::kNanRow ? (is_v ? 0u : 0x7FFF7FFFu) : pow2_f16x2((int)a - top);
             rows[i] = a != 0 ? 0xFFFFFFFFu : 0u;
         }
-        // K, then V
-        uint32_t from = smem + C::kRawKAt, to = smem + C::kKAt + st * C::kOperand;
-        uint64_t *full = &sh->k_full[st], *raw_empty = &sh->raw_k_empty;
-#pragma unroll 1
-        for (int which = 0; which < 2; ++which) {
-            if (which == 1) {
-                ok = tc::mbar_wait(&sh->raw_v_full, tile & 1);
-                ok = ok && (tile < kStages || tc::mbar_wait(&sh->v_empty[st], ph ^ 1));
-                if (!__all_sync(0xFFFFFFFFu, ok))
-                    return false;
-            }
-            convert<FMT, D, SPLIT>(from, to, tid, unit, rows);
-            if (which == 0 && tid == 0)
-                sh->info[tile % kInfos] = {kv::exp2_byte(ku), (float)(vu - 127), info.present, 0};
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                tc::mbar_arrive(full);
-                tc::mbar_arrive(raw_empty);
-            }
-            from = smem + C::kRawVAt;
-            to = smem + C::kVAt + st * C::kOperand;
-            full = &sh->v_full[st];
-            raw_empty = &sh->raw_v_empty;
-#pragma unroll
-            for (int i = 0; i < mine; ++i)
-                unit[i] = v_unit[i];
+        convert<FMT, D, SPLIT>(raw, operand + st * C::kOperand, tid, unit, rows);
+        if (!is_v) {
+            const int v_top = largest_exp(other);
+            if (tid == 0)
+                sh->info[tile % kInfos] = {kv::exp2_byte(top), (float)(v_top - 127), info.present, 0};
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tc::mbar_arrive(&full[st]);
+            tc::mbar_arrive(raw_empty);
         }
     }
     return true;
@@ -900,6 +893,8 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, ui
             for (int q = 0; q < kCols / 32; ++q) {
                 float x[32];
                 result(q, x);
+                if (!live)
+                    continue;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     reinterpret_cast<float4 *>(slot)[(col0 / 4 + 8 * q + j) * C::kRows + row] =
@@ -921,34 +916,46 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, ui
                 const int count = last_cta - first_cta + 1;
                 const float *const from = partials + (int64_t)first_cta * 2 * C::kSlotFloats;
                 const auto slot_of = [&](int i) { return from + (int64_t)(i == 0 ? 1 : 2 * i) * C::kSlotFloats; };
-                float m = -INFINITY;
-                for (int i = 0; i < count; ++i)
-                    m = fmaxf(m, __ldcg(reinterpret_cast<const float2 *>(slot_of(i) + C::kRows * D) + row).x);
-                float l = 0.f;
-                for (int i = 0; i < count; ++i) {
-                    const float2 ml = __ldcg(reinterpret_cast<const float2 *>(slot_of(i) + C::kRows * D) + row);
-                    l = fmaf(ml.x == -INFINITY ? 0.f : ex2(ml.x - m), ml.y, l);
-                }
-                for (int q = 0; q < kCols / 32; ++q) {
-                    float x[32];
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        x[j] = 0.f;
-#pragma unroll 1
+                const auto stats_of = [&](int i) {
+                    return __ldcg(reinterpret_cast<const float2 *>(slot_of(i) + C::kRows * D) + row);
+                };
+                // several contributors' loads at once: one at a time, the join ran at the latency of L2
+                if (live) {
+                    float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+                    for (int i = 0; i < count; ++i)
+                        m = fmaxf(m, stats_of(i).x);
+#pragma unroll 4
                     for (int i = 0; i < count; ++i) {
-                        const float tw = __ldcg(reinterpret_cast<const float2 *>(slot_of(i) + C::kRows * D) + row).x;
-                        const float w = tw == -INFINITY ? 0.f : ex2(tw - m);
-                        const float4 *v = reinterpret_cast<const float4 *>(slot_of(i)) + (col0 / 4 + 8 * q) * C::kRows + row;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 y = __ldcg(v + j * C::kRows);
-                            x[4 * j] = fmaf(w, y.x, x[4 * j]);
-                            x[4 * j + 1] = fmaf(w, y.y, x[4 * j + 1]);
-                            x[4 * j + 2] = fmaf(w, y.z, x[4 * j + 2]);
-                            x[4 * j + 3] = fmaf(w, y.w, x[4 * j + 3]);
-                        }
+                        const float2 ml = stats_of(i);
+                        l = fmaf(ml.x == -INFINITY ? 0.f : ex2(ml.x - m), ml.y, l);
                     }
-                    store(q, x, l);
+#pragma unroll 1
+                    for (int q = 0; q < kCols / 32; ++q) {
+                        float x[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            x[j] = 0.f;
+#pragma unroll 2
+                        for (int i = 0; i < count; ++i) {
+                            const float tw = stats_of(i).x;
+                            const float w = tw == -INFINITY ? 0.f : ex2(tw - m);
+                            const float4 *v =
+                                reinterpret_cast<const float4 *>(slot_of(i)) + (col0 / 4 + 8 * q) * C::kRows + row;
+                            float4 y[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                y[j] = __ldcg(v + j * C::kRows);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                x[4 * j] = fmaf(w, y[j].x, x[4 * j]);
+                                x[4 * j + 1] = fmaf(w, y[j].y, x[4 * j + 1]);
+                                x[4 * j + 2] = fmaf(w, y[j].z, x[4 * j + 2]);
+                                x[4 * j + 3] = fmaf(w, y[j].w, x[4 * j + 3]);
+                            }
+                        }
+                        store(q, x, l);
+                    }
                 }
             }
         }
@@ -995,8 +1002,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
         sh->seg.index = 0;
         set_segment(range, &sh->seg);
         for (int i = 0; i < kStages; ++i) {
-            tc::mbar_init(&sh->k_full[i], kConvertWarps);
-            tc::mbar_init(&sh->v_full[i], kConvertWarps);
+            tc::mbar_init(&sh->k_full[i], kConvertWarps / 2);
+            tc::mbar_init(&sh->v_full[i], kConvertWarps / 2);
             tc::mbar_init(&sh->k_empty[i], SPLIT ? 1 : 2);
             tc::mbar_init(&sh->v_empty[i], SPLIT ? 1 : 2);
         }
@@ -1011,8 +1018,8 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
         }
         tc::mbar_init(&sh->raw_k_full, 1);
         tc::mbar_init(&sh->raw_v_full, 1);
-        tc::mbar_init(&sh->raw_k_empty, kConvertWarps);
-        tc::mbar_init(&sh->raw_v_empty, kConvertWarps);
+        tc::mbar_init(&sh->raw_k_empty, kConvertWarps / 2);
+        tc::mbar_init(&sh->raw_v_empty, kConvertWarps / 2);
         tc::fence_mbar_init();
     }
     if (warp == kSoftmaxWarps + kConvertWarps + 2)
@@ -1030,7 +1037,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
         code = kTimeoutSoftmax;
     } else if (warp < kSoftmaxWarps + kConvertWarps) {
         give_regs<kConvertRegs>();
-        ok = convert_role<FMT, D, SPLIT>((uint32_t)(range.end - range.begin), sh, smem, tid - 32 * kSoftmaxWarps);
+        const int ct = tid - 32 * kSoftmaxWarps;
+        ok = convert_role<FMT, D, SPLIT>((uint32_t)(range.end - range.begin), sh, smem, ct / kConvertThreads,
+                                         ct % kConvertThreads);
         code = kTimeoutConvert;
     } else {
         give_regs<kMmaRegs>();
