@@ -53,6 +53,8 @@ static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kConvertWarps * kConvertRegs 
               "setmaxnreg would wait for registers that nobody gives back");
 constexpr int kStages = 2;
 constexpr int kInfos = 4;
+constexpr int kMostRaw = 4;         // buffers of K or V as they lie in the pages
+constexpr int kSharedBytes = 1024;  // barriers and the like (Shared)
 constexpr float kHeadroom = 7.f;
 constexpr float kMostWeight = 0x1p15f;  // of the weights of half a tile, in sum
 constexpr float kSumUnit = 0x1p-32f;
@@ -66,11 +68,21 @@ struct Cfg {
     static constexpr int kRows = SPLIT ? kRowTile : 2 * kRowTile;
     static constexpr int kOperand = 128 * D * 2;  // Q, K or V tile in f16
     static constexpr int kQAt = 0, kKAt = (SPLIT ? 1 : 2) * kOperand, kVAt = kKAt + kStages * kOperand;
-    // a tile's bytes as they lie in the pages: K's codes, scales, exponents and V's exponents; the same of V without K's
-    static constexpr int kRawRows = kTile * (R::kCode + R::kScale);
-    static constexpr int kRawKAt = kVAt + kStages * kOperand, kRawVAt = kRawKAt + kRawRows + 2 * kTile;
-    static constexpr int kBarAt = kRawVAt + kRawRows + kTile;
-    static constexpr int kSmem = kBarAt + 2688;
+    // a tile's bytes as they lie in the pages, run by run (codes, scales, exponents); K's with V's exponents behind.
+    // One tile's loads take as long as its conversion, so there are as many buffers as fit, for K first.
+    static constexpr int kRawRows = kTile * R::kBytes;
+    static constexpr int kRawKBytes = kRawRows + kTile, kRawVBytes = kRawRows;
+    static constexpr int kStatsBytes = SPLIT ? 2 * kRowTile * 8 : 0;
+    static constexpr int kRawAt = kVAt + kStages * kOperand;
+    static constexpr int kRoom = 227 * 1024 - kRawAt - kStatsBytes - kSharedBytes;
+    static constexpr int kRawPairs = kRoom / (kRawKBytes + kRawVBytes);
+    static constexpr int kRawVs = kRawPairs < kMostRaw ? kRawPairs : kMostRaw;
+    static constexpr int kRawKs = kRawVs < kMostRaw && kRoom - kRawVs * (kRawKBytes + kRawVBytes) >= kRawKBytes ? kRawVs + 1 : kRawVs;
+    static constexpr int kRawKAt = kRawAt, kRawVAt = kRawKAt + kRawKs * kRawKBytes;
+    static constexpr int kStatsAt = kRawVAt + kRawVs * kRawVBytes;
+    static constexpr int kBarAt = kStatsAt + kStatsBytes;
+    static constexpr int kSmem = kBarAt + kSharedBytes;
+    static_assert(kRawVs >= 1, "shared memory");
     static constexpr int kSlotFloats = kRows * (D + 2);
     // tensor memory columns
     static constexpr int kScoreCols = 0, kOutCols = 2 * kTile;
@@ -104,16 +116,16 @@ struct Segment {
 };
 
 struct Shared {
-    uint64_t raw_k_full, raw_k_empty, raw_v_full, raw_v_empty;
+    uint64_t raw_full[2][kMostRaw], raw_empty[2][kMostRaw];  // K's, V's
     uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
     uint64_t q_ready[2], s_full[2][2], p_ready[2][2], pv_done[2][2], drain[2];  // by group, and half of the keys
     TileInfo info[kInfos];
-    RawInfo raw[2];  // K's and V's
+    RawInfo raw[2][kMostRaw];
     Segment seg;
     uint32_t tmem, last;
     int64_t scratch[kThreads / 32 + 5];
-    float2 stats[2][kRowTile];  // largest and sum of a row, by softmax group
 };
+static_assert(sizeof(Shared) <= kSharedBytes, "barriers");
 
 // One lane of a converged warp; unlike a test of the lane number this tells the
 // compiler that a single thread follows, and MMA operands can go to uniform
@@ -276,7 +288,7 @@ struct TileCursor {
 // ---------------------------------------------------------------------------
 
 // A tile is cut into runs that lie in one page each (16 keys at least); lane i
-// copies run i.  Runs that no row sees, and pages that are not there, are not
+// copies run i, a whole page in one piece.  Runs that no row sees, and pages that are not there, are not
 // copied.
 template <int FMT, int D, bool SPLIT>
 NVFP4_DEVINL bool load_role(const Call &c, const Range &range, const Item &first, int64_t item_begin, Shared *sh,
@@ -287,17 +299,32 @@ NVFP4_DEVINL bool load_role(const Call &c, const Range &range, const Item &first
     const int shift = c.pool.page_shift, run = min(1 << shift, kTile), runs = kTile / run;
     TileCursor<C::kRows> cur{first, item_begin, range.begin, range.end};
     const uint32_t tiles = (uint32_t)(range.end - range.begin);
-    const auto sees = [&](int key) { return lane < runs && key < cur.it.hi && key + run > cur.it.lo; };
-    const auto look_up = [&](int key) {
-        return sees(key) ? c.table[(int64_t)cur.it.b * c.table_width + (key >> shift)] : -1;
+    // Page numbers of 32 runs of the item at a time, and of the 32 behind them:
+    // a table read per tile took longer than everything else the warp does.
+    const auto look_up = [&](uint32_t key) {  // (unsigned: 63 runs beyond a tile may pass 2^31)
+        const bool sees = key < (uint32_t)cur.it.hi && (int)key + run > cur.it.lo;
+        return sees ? c.table[(int64_t)cur.it.b * c.table_width + (key >> shift)] : -1;
     };
-    int page = look_up(cur.key0() + lane * run);
-    const uint32_t k_full = tc::smem_addr(&sh->raw_k_full), v_full = tc::smem_addr(&sh->raw_v_full);
+    int pages = 0, pages_behind = 0, used = 32;  // runs of `pages` that are behind us
+    int64_t item_of_pages = -1;
     bool ok = true;
-    uint32_t tile = 0;
-    for (; tile < tiles; ++tile) {
+    uint32_t issued[2] = {0, 0};  // tiles of K and of V
+    for (uint32_t tile = 0; tile < tiles && ok; ++tile) {
         const int key0 = cur.key0(), key = key0 + lane * run, head = cur.it.head;
-        const bool want = sees(key), there = want && page >= 0 && page < c.pool.n_pages;
+        if (item_of_pages != cur.item_begin) {
+            item_of_pages = cur.item_begin;
+            pages = look_up(key0 + lane * run);
+            pages_behind = look_up((uint32_t)key0 + (32 + lane) * run);
+            used = 0;
+        } else if (used == 32) {
+            pages = pages_behind;
+            pages_behind = look_up((uint32_t)key0 + (32 + lane) * run);
+            used = 0;
+        }
+        const int page = __shfl_sync(0xFFFFFFFFu, pages, (used + lane) & 31);
+        used += runs;
+        const bool want = lane < runs && key < cur.it.hi && key + run > cur.it.lo;
+        const bool there = want && page >= 0 && page < c.pool.n_pages;
         if (want && !there)
             kv::report(c.pool.status, kStatusKvAttention);
         const uint32_t missing = __ballot_sync(0xFFFFFFFFu, want && !there);
@@ -309,54 +336,44 @@ NVFP4_DEVINL bool load_role(const Call &c, const Range &range, const Item &first
         const uint8_t *const k = kv::block_ptr(c.pool, there ? page : 0, head, 0);
         const uint8_t *const v = k + c.pool.block_bytes;
         const int at = key & ((1 << shift) - 1);
-        const int64_t scales = (int64_t)R::kCode << shift, exps = (int64_t)(R::kCode + R::kScale) << shift;
+        const uint32_t scales = R::kCode << shift, exps = (R::kCode + R::kScale) << shift;
         cur.step(c);
-        if (!cur.at_end())
-            page = look_up(cur.key0() + lane * run);
-
-        ok = tile == 0 || tc::mbar_wait(&sh->raw_k_empty, (tile - 1) & 1);
-        if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
-            break;
-        if (lane == 0) {
-            sh->raw[0] = info;
-            tc::mbar_arrive_expect_tx(&sh->raw_k_full, copied * run * (R::kCode + R::kScale + 2));
-        }
-        __syncwarp();
-        if (there) {
-            const uint32_t dst = smem + C::kRawKAt;
-            tc::bulk_load_a(dst + lane * run * R::kCode, k + at * R::kCode, run * R::kCode, k_full);
-            if (R::kScale)
-                tc::bulk_load_a(dst + kTile * R::kCode + lane * run * R::kScale, k + scales + at * R::kScale,
-                                run * R::kScale, k_full);
-            tc::bulk_load_a(dst + C::kRawRows + lane * run, k + exps + at, run, k_full);
-            tc::bulk_load_a(dst + C::kRawRows + kTile + lane * run, v + exps + at, run, k_full);
-        }
-        ok = tile == 0 || tc::mbar_wait(&sh->raw_v_empty, (tile - 1) & 1);
-        if (!(ok = __all_sync(0xFFFFFFFFu, ok))) {
-            ++tile;  // K's copies of this tile are in flight
-            break;
-        }
-        if (lane == 0) {
-            sh->raw[1] = info;
-            tc::mbar_arrive_expect_tx(&sh->raw_v_full, copied * run * (R::kCode + R::kScale + 1));
-        }
-        __syncwarp();
-        if (there) {
-            const uint32_t dst = smem + C::kRawVAt;
-            tc::bulk_load_a(dst + lane * run * R::kCode, v + at * R::kCode, run * R::kCode, v_full);
-            if (R::kScale)
-                tc::bulk_load_a(dst + kTile * R::kCode + lane * run * R::kScale, v + scales + at * R::kScale,
-                                run * R::kScale, v_full);
-            tc::bulk_load_a(dst + C::kRawRows + lane * run, v + exps + at, run, v_full);
+#pragma unroll 1
+        for (int is_v = 0; is_v < 2; ++is_v) {
+            const uint32_t n = is_v ? C::kRawVs : C::kRawKs, slot = tile % n, round = tile / n;
+            ok = round == 0 || tc::mbar_wait(&sh->raw_empty[is_v][slot], (round - 1) & 1);
+            if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
+                break;
+            if (lane == 0) {
+                sh->raw[is_v][slot] = info;
+                tc::mbar_arrive_expect_tx(&sh->raw_full[is_v][slot], copied * run * (R::kBytes + (is_v ? 0 : 1)));
+            }
+            __syncwarp();
+            ++issued[is_v];
+            if (there) {
+                const uint8_t *const from = is_v ? v : k;
+                const uint32_t full = tc::smem_addr(&sh->raw_full[is_v][slot]);
+                const uint32_t dst = smem + (is_v ? C::kRawVAt + slot * C::kRawVBytes : C::kRawKAt + slot * C::kRawKBytes);
+                const uint32_t to = dst + lane * run * R::kBytes;
+                if (run == 1 << shift) {  // a whole page: its codes, scales and exponents are one piece
+                    tc::bulk_load_a(to, from, run * R::kBytes, full);
+                } else {
+                    tc::bulk_load_a(to, from + at * R::kCode, run * R::kCode, full);
+                    if (R::kScale)
+                        tc::bulk_load_a(to + run * R::kCode, from + scales + at * R::kScale, run * R::kScale, full);
+                    tc::bulk_load_a(to + run * (R::kCode + R::kScale), from + exps + at, run, full);
+                }
+                if (!is_v)
+                    tc::bulk_load_a(dst + C::kRawRows + lane * run, v + exps + at, run, full);
+            }
         }
     }
     // nothing is in flight when the warp leaves
-    if (tile > 0)
-        ok = tc::mbar_wait(&sh->raw_k_full, (tile - 1) & 1) && ok;
-    if (tile > 0 && ok)
-        ok = tc::mbar_wait(&sh->raw_v_full, (tile - 1) & 1);
-    else if (tile > 1)
-        tc::mbar_wait(&sh->raw_v_full, (tile - 2) & 1);
+    for (int is_v = 0; is_v < 2; ++is_v) {
+        const uint32_t n = is_v ? C::kRawVs : C::kRawKs;
+        for (uint32_t t = issued[is_v] > n ? issued[is_v] - n : 0; t < issued[is_v]; ++t)
+            ok = tc::mbar_wait(&sh->raw_full[is_v][t % n], (t / n) & 1) && ok;
+    }
     return ok;
 }
 
@@ -391,7 +408,7 @@ NVFP4_DEVINL int largest_exp(uint32_t four)
 // banks.  unit[i]: f16x2 factor of row i; keep[i]: all ones, or zero for a row
 // that is written as zeros whatever lies in the buffer.
 template <int FMT, int D, bool SPLIT>
-NVFP4_DEVINL void convert(uint32_t raw, uint32_t operand, int tid, const uint32_t (&unit)[Cfg<FMT, D, SPLIT>::kRowsMine],
+NVFP4_DEVINL void convert(uint32_t raw, int run, uint32_t operand, int tid, const uint32_t (&unit)[Cfg<FMT, D, SPLIT>::kRowsMine],
                           const uint32_t (&keep)[Cfg<FMT, D, SPLIT>::kRowsMine])
 {
     using C = Cfg<FMT, D, SPLIT>;
@@ -406,15 +423,15 @@ NVFP4_DEVINL void convert(uint32_t raw, uint32_t operand, int tid, const uint32_
 #pragma unroll 1
     for (int b = 0; b < D / 64; ++b) {
         const int block = b ^ flip;
-        const uint32_t from = raw + row0 * R::kCode + (block * per + place) * 16;
         uint4 code[rows];
         uint32_t two[rows];
 #pragma unroll
         for (int i = 0; i < rows; ++i) {
-            code[i] = tc::lds128(from + i * C::kRowStep * R::kCode);
+            const int row = row0 + i * C::kRowStep, in_run = row & (run - 1);
+            const uint32_t from = raw + (row - in_run) * R::kBytes;  // the row's run
+            code[i] = tc::lds128(from + in_run * R::kCode + (block * per + place) * 16);
             if constexpr (FMT == NVFP4_KV_NVFP4)
-                two[i] = tc::lds16(raw + kTile * R::kCode + (row0 + i * C::kRowStep) * R::kScale +
-                                   (block * per + place) * 2);
+                two[i] = tc::lds16(from + run * R::kCode + in_run * R::kScale + (block * per + place) * 2);
         }
 #pragma unroll
         for (int i = 0; i < rows; ++i) {
@@ -453,25 +470,27 @@ NVFP4_DEVINL void convert(uint32_t raw, uint32_t operand, int tid, const uint32_
 // the other's arithmetic (the same eight warps doing K, then V, of each tile took
 // 2400 clocks a tile).
 template <int FMT, int D, bool SPLIT>
-NVFP4_DEVINL bool convert_role(uint32_t tiles, Shared *sh, uint32_t smem, int is_v, int tid)
+NVFP4_DEVINL bool convert_role(uint32_t tiles, int run, Shared *sh, uint32_t smem, int is_v, int tid)
 {
     using C = Cfg<FMT, D, SPLIT>;
+    using R = kv::Row<FMT, D>;
     constexpr int per = C::kPerBlock, mine = C::kRowsMine;
     const int lane = tid % 32;
-    uint64_t *const raw_full = is_v ? &sh->raw_v_full : &sh->raw_k_full;
-    uint64_t *const raw_empty = is_v ? &sh->raw_v_empty : &sh->raw_k_empty;
+    const uint32_t slots = is_v ? C::kRawVs : C::kRawKs;
     uint64_t *const full = is_v ? sh->v_full : sh->k_full, *const empty = is_v ? sh->v_empty : sh->k_empty;
-    const uint32_t raw = smem + (is_v ? C::kRawVAt : C::kRawKAt), operand = smem + (is_v ? C::kVAt : C::kKAt);
+    const uint32_t operand = smem + (is_v ? C::kVAt : C::kKAt);
     for (uint32_t tile = 0; tile < tiles; ++tile) {
-        const uint32_t st = tile % kStages, ph = (tile / kStages) & 1;
-        bool ok = tc::mbar_wait(raw_full, tile & 1);
+        const uint32_t st = tile % kStages, ph = (tile / kStages) & 1, slot = tile % slots;
+        const uint32_t raw = smem + (is_v ? C::kRawVAt + slot * C::kRawVBytes : C::kRawKAt + slot * C::kRawKBytes);
+        bool ok = tc::mbar_wait(&sh->raw_full[is_v][slot], (tile / slots) & 1);
         ok = ok && (tile < kStages || tc::mbar_wait(&empty[st], ph ^ 1));
         if (!__all_sync(0xFFFFFFFFu, ok))
             return false;
         // exponents of rows 4 lane .. 4 lane + 3, a byte each; 0: no row that anyone sees
-        const RawInfo info = sh->raw[is_v];
-        uint32_t own = tc::lds32(raw + C::kRawRows + 4 * lane);
-        uint32_t other = is_v ? own : tc::lds32(raw + C::kRawRows + kTile + 4 * lane);
+        const RawInfo info = sh->raw[is_v][slot];
+        const int in_run = 4 * lane & (run - 1);
+        uint32_t own = tc::lds32(raw + (4 * lane - in_run) * R::kBytes + run * (R::kCode + R::kScale) + in_run);
+        uint32_t other = is_v ? own : tc::lds32(raw + C::kRawRows + 4 * lane);
         const int first = info.key0 + 4 * lane;
         uint32_t keep = info.present >> (lane / 4) & 1 ? 0xFFFFFFFFu : 0u;
         if (first < info.lo)
@@ -491,7 +510,7 @@ NVFP4_DEVINL bool convert_role(uint32_t tiles, Shared *sh, uint32_t smem, int is
             unit[i] = a == kv::kNanRow || b == kv::kNanRow ? (is_v ? 0u : 0x7FFF7FFFu) : pow2_f16x2((int)a - top);
             rows[i] = a != 0 ? 0xFFFFFFFFu : 0u;
         }
-        convert<FMT, D, SPLIT>(raw, operand + st * C::kOperand, tid, unit, rows);
+        convert<FMT, D, SPLIT>(raw, run, operand + st * C::kOperand, tid, unit, rows);
         if (!is_v) {
             const int v_top = largest_exp(other);
             if (tid == 0)
@@ -501,7 +520,7 @@ NVFP4_DEVINL bool convert_role(uint32_t tiles, Shared *sh, uint32_t smem, int is
         __syncwarp();
         if (lane == 0) {
             tc::mbar_arrive(&full[st]);
-            tc::mbar_arrive(raw_empty);
+            tc::mbar_arrive(&sh->raw_empty[is_v][slot]);
         }
     }
     return true;
@@ -639,6 +658,7 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, ui
     const uint32_t scores = tmem + C::kScoreCols + group * kTile + lanes;
     const uint32_t out = tmem + C::kOutCols + group * D + lanes;
     const Segment &g = sh->seg;
+    float2 (*const stats)[kRowTile] = reinterpret_cast<float2 (*)[kRowTile]>(reinterpret_cast<uint8_t *>(sh) - C::kStatsBytes);  // SPLIT: of a row, by group
     bool ok = true;
     uint32_t mine = 0;
 
@@ -690,7 +710,7 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, ui
             }
             factor = fabsf(c.scale_log2) * __uint_as_float((uint32_t)(e - 14) << 23);
             if (SPLIT)
-                sh->stats[0][r].x = factor;
+                stats[0][r].x = factor;
             tc::fence_proxy_async_smem();
             // a group waits once for each segment in which it has a tile
             for (int i = SPLIT ? 0 : group; i <= (SPLIT ? 1 : group); ++i) {
@@ -700,7 +720,7 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, ui
         }
         if (SPLIT) {
             tc::named_bar_sync(kBar, kAll);
-            factor = sh->stats[0][r].x;
+            factor = stats[0][r].x;
         }
 
         float sum = 0.f;
@@ -829,9 +849,9 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, ui
         const int col0 = SPLIT ? group * kCols : 0;
         float w_other = 0.f, w_mine = 1.f;
         if (SPLIT) {
-            sh->stats[group][r] = make_float2(begun ? top : -INFINITY, begun ? sum : 0.f);
+            stats[group][r] = make_float2(begun ? top : -INFINITY, begun ? sum : 0.f);
             tc::named_bar_sync(kBar, kAll);
-            const float2 a = sh->stats[0][r], b = sh->stats[1][r];
+            const float2 a = stats[0][r], b = stats[1][r];
             top = fmaxf(a.x, b.x);
             // groups without a tile have nothing in tensor memory; 0 * NaN stays NaN in the others
             const float wa = a.x == -INFINITY ? 0.f : ex2(a.x - top), wb = b.x == -INFINITY ? 0.f : ex2(b.x - top);
@@ -985,7 +1005,6 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
     using C = Cfg<FMT, D, SPLIT>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     Shared *const sh = reinterpret_cast<Shared *>(smem_raw + C::kBarAt);
-    static_assert(sizeof(Shared) <= C::kSmem - C::kBarAt, "barriers");
     const int tid = threadIdx.x, warp = __shfl_sync(0xFFFFFFFFu, tid / 32, 0);
 
     tc::griddep_launch_dependents();
@@ -1016,10 +1035,10 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
             }
             tc::mbar_init(&sh->drain[g], 1);
         }
-        tc::mbar_init(&sh->raw_k_full, 1);
-        tc::mbar_init(&sh->raw_v_full, 1);
-        tc::mbar_init(&sh->raw_k_empty, kConvertWarps / 2);
-        tc::mbar_init(&sh->raw_v_empty, kConvertWarps / 2);
+        for (int i = 0; i < 2 * kMostRaw; ++i) {
+            tc::mbar_init(&sh->raw_full[0][0] + i, 1);
+            tc::mbar_init(&sh->raw_empty[0][0] + i, kConvertWarps / 2);
+        }
         tc::fence_mbar_init();
     }
     if (warp == kSoftmaxWarps + kConvertWarps + 2)
@@ -1038,7 +1057,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
     } else if (warp < kSoftmaxWarps + kConvertWarps) {
         give_regs<kConvertRegs>();
         const int ct = tid - 32 * kSoftmaxWarps;
-        ok = convert_role<FMT, D, SPLIT>((uint32_t)(range.end - range.begin), sh, smem, ct / kConvertThreads,
+        ok = convert_role<FMT, D, SPLIT>((uint32_t)(range.end - range.begin), min(1 << c.pool.page_shift, kTile), sh, smem, ct / kConvertThreads,
                                          ct % kConvertThreads);
         code = kTimeoutConvert;
     } else {
