@@ -10,8 +10,8 @@
 //   warps 0-3, 4-7  softmax of row tile 0 and 1: a thread has one row.  Scores
 //                   come from tensor memory and the weights P go back there as
 //                   the f16 A operand of the second product, over the scores.
-//   warp 18         bulk copies of a tile's codes, scales and exponents from the
-//                   pages to shared memory, ahead of their conversion.
+//   warps 18, 19    bulk copies of K's, and V's, codes, scales and exponents from
+//                   the pages to shared memory, ahead of their conversion.
 //   warps 8-11, 12-15  codes of K, and of V, to f16, from there to the layout of the MMA's B operands
 //                   (K with the head dimension contiguous; V likewise, read
 //                   transposed).
@@ -46,7 +46,7 @@ constexpr int kTile = 128;                      // keys of a tile
 constexpr int kRowTile = 128;                   // rows of a row tile
 constexpr int kSoftmaxWarps = 8, kConvertWarps = 8;
 constexpr int kConvertThreads = 32 * kConvertWarps / 2;  // of K, and as many of V
-constexpr int kThreads = 32 * (kSoftmaxWarps + kConvertWarps + 4);  // whole warpgroups; warp 19 idles
+constexpr int kThreads = 32 * (kSoftmaxWarps + kConvertWarps + 4);  
 // Registers of a thread by role: what the launch gives every thread, shared out anew.
 constexpr int kSoftmaxRegs = 128, kConvertRegs = 72, kMmaRegs = 72, kLaunchRegs = 96;
 static_assert(32 * (kSoftmaxWarps * kSoftmaxRegs + kConvertWarps * kConvertRegs + 4 * kMmaRegs) <= kThreads * kLaunchRegs,
@@ -292,10 +292,11 @@ struct TileCursor {
 // copied.
 template <int FMT, int D, bool SPLIT>
 NVFP4_DEVINL bool load_role(const Call &c, const Range &range, const Item &first, int64_t item_begin, Shared *sh,
-                            uint32_t smem, int lane)
+                            uint32_t smem, int is_v, int lane)
 {
     using C = Cfg<FMT, D, SPLIT>;
     using R = kv::Row<FMT, D>;
+    const uint32_t n = is_v ? C::kRawVs : C::kRawKs;  // buffers
     const int shift = c.pool.page_shift, run = min(1 << shift, kTile), runs = kTile / run;
     TileCursor<C::kRows> cur{first, item_begin, range.begin, range.end};
     const uint32_t tiles = (uint32_t)(range.end - range.begin);
@@ -308,8 +309,8 @@ NVFP4_DEVINL bool load_role(const Call &c, const Range &range, const Item &first
     int pages = 0, pages_behind = 0, used = 32;  // runs of `pages` that are behind us
     int64_t item_of_pages = -1;
     bool ok = true;
-    uint32_t issued[2] = {0, 0};  // tiles of K and of V
-    for (uint32_t tile = 0; tile < tiles && ok; ++tile) {
+    uint32_t tile = 0;
+    for (; tile < tiles; ++tile) {
         const int key0 = cur.key0(), key = key0 + lane * run, head = cur.it.head;
         if (item_of_pages != cur.item_begin) {
             item_of_pages = cur.item_begin;
@@ -338,42 +339,35 @@ NVFP4_DEVINL bool load_role(const Call &c, const Range &range, const Item &first
         const int at = key & ((1 << shift) - 1);
         const uint32_t scales = R::kCode << shift, exps = (R::kCode + R::kScale) << shift;
         cur.step(c);
-#pragma unroll 1
-        for (int is_v = 0; is_v < 2; ++is_v) {
-            const uint32_t n = is_v ? C::kRawVs : C::kRawKs, slot = tile % n, round = tile / n;
-            ok = round == 0 || tc::mbar_wait(&sh->raw_empty[is_v][slot], (round - 1) & 1);
-            if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
-                break;
-            if (lane == 0) {
-                sh->raw[is_v][slot] = info;
-                tc::mbar_arrive_expect_tx(&sh->raw_full[is_v][slot], copied * run * (R::kBytes + (is_v ? 0 : 1)));
+        const uint32_t slot = tile % n, round = tile / n;
+        ok = round == 0 || tc::mbar_wait(&sh->raw_empty[is_v][slot], (round - 1) & 1);
+        if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
+            break;
+        if (lane == 0) {
+            sh->raw[is_v][slot] = info;
+            tc::mbar_arrive_expect_tx(&sh->raw_full[is_v][slot], copied * run * (R::kBytes + (is_v ? 0 : 1)));
+        }
+        __syncwarp();
+        if (there) {
+            const uint8_t *const from = is_v ? v : k;
+            const uint32_t full = tc::smem_addr(&sh->raw_full[is_v][slot]);
+            const uint32_t dst = smem + (is_v ? C::kRawVAt + slot * C::kRawVBytes : C::kRawKAt + slot * C::kRawKBytes);
+            const uint32_t to = dst + lane * run * R::kBytes;
+            if (run == 1 << shift) {  // a whole page: its codes, scales and exponents are one piece
+                tc::bulk_load_a(to, from, run * R::kBytes, full);
+            } else {
+                tc::bulk_load_a(to, from + at * R::kCode, run * R::kCode, full);
+                if (R::kScale)
+                    tc::bulk_load_a(to + run * R::kCode, from + scales + at * R::kScale, run * R::kScale, full);
+                tc::bulk_load_a(to + run * (R::kCode + R::kScale), from + exps + at, run, full);
             }
-            __syncwarp();
-            ++issued[is_v];
-            if (there) {
-                const uint8_t *const from = is_v ? v : k;
-                const uint32_t full = tc::smem_addr(&sh->raw_full[is_v][slot]);
-                const uint32_t dst = smem + (is_v ? C::kRawVAt + slot * C::kRawVBytes : C::kRawKAt + slot * C::kRawKBytes);
-                const uint32_t to = dst + lane * run * R::kBytes;
-                if (run == 1 << shift) {  // a whole page: its codes, scales and exponents are one piece
-                    tc::bulk_load_a(to, from, run * R::kBytes, full);
-                } else {
-                    tc::bulk_load_a(to, from + at * R::kCode, run * R::kCode, full);
-                    if (R::kScale)
-                        tc::bulk_load_a(to + run * R::kCode, from + scales + at * R::kScale, run * R::kScale, full);
-                    tc::bulk_load_a(to + run * (R::kCode + R::kScale), from + exps + at, run, full);
-                }
-                if (!is_v)
-                    tc::bulk_load_a(dst + C::kRawRows + lane * run, v + exps + at, run, full);
-            }
+            if (!is_v)
+                tc::bulk_load_a(dst + C::kRawRows + lane * run, v + exps + at, run, full);
         }
     }
     // nothing is in flight when the warp leaves
-    for (int is_v = 0; is_v < 2; ++is_v) {
-        const uint32_t n = is_v ? C::kRawVs : C::kRawKs;
-        for (uint32_t t = issued[is_v] > n ? issued[is_v] - n : 0; t < issued[is_v]; ++t)
-            ok = tc::mbar_wait(&sh->raw_full[is_v][t % n], (t / n) & 1) && ok;
-    }
+    for (uint32_t t = tile > n ? tile - n : 0; t < tile; ++t)
+        ok = tc::mbar_wait(&sh->raw_full[is_v][t % n], (t / n) & 1) && ok;
     return ok;
 }
 
@@ -1069,8 +1063,9 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
                 code = kTimeoutMma;
             }
             __syncwarp();
-        } else if (warp == kSoftmaxWarps + kConvertWarps + 2) {
-            ok = load_role<FMT, D, SPLIT>(c, range, item, item_begin, sh, smem, tid % 32);
+        } else {
+            ok = load_role<FMT, D, SPLIT>(c, range, item, item_begin, sh, smem, warp - (kSoftmaxWarps + kConvertWarps + 2),
+                                          tid % 32);
             code = kTimeoutLoad;
         }
     }
