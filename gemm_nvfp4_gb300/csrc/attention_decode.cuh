@@ -63,7 +63,7 @@ struct Cfg {
     // stage: K codes, V codes, K scales, V scales, K exponents, V exponents
     static constexpr int kScaleAt = 2 * kCodeBytes, kExpAt = kScaleAt + 2 * kScaleBytes;
     static constexpr int kStageBytes = kExpAt + 2 * kStep;
-    static constexpr int kCtasPerSm = NT <= 2 ? 2 : 1;
+    static constexpr int kCtasPerSm = NT == 1 ? 2 : 1;
     // the ring takes what shared memory is left beside Q and the tables
     static constexpr int kQBytes = kRows * D * 2;
     static constexpr int kRowBytes = kRows * (4 + 4 + 4 + 8);  // score factor, key range, tree word
@@ -834,7 +834,8 @@ cudaError_t launch_rows(const Call &c, uint8_t *workspace, int num_sms, cudaStre
     const int block = decode_block(rows);
     return block == 8    ? launch<FMT, D, 1, WIDE>(c, workspace, num_sms, stream)
            : block == 16 ? launch<FMT, D, 2, WIDE>(c, workspace, num_sms, stream)
-                        : launch<FMT, D, 4, WIDE>(c, workspace, num_sms, stream);
+           : block == 24 ? launch<FMT, D, 3, WIDE>(c, workspace, num_sms, stream)
+                         : launch<FMT, D, 4, WIDE>(c, workspace, num_sms, stream);
 }
 
 template <int FMT>
