@@ -459,7 +459,10 @@ int nvfp4_kv_read(const nvfp4_kv_cache *cache, uint16_t *k, int64_t k_ld, uint16
  * query of a call sees (beyond kv_len, or before the window) are not looked at.
  * workspace  nvfp4_paged_attention_workspace_bytes(args) bytes, zero-filled
  *            before its first use; each call leaves its counters zero, so one
- *            buffer serves calls of any shapes, ordered on one stream.
+ *            buffer serves attention calls of any shapes, ordered on one
+ *            stream.  Not shared with product calls (their counters lie where
+ *            this call has partial results); zero it again after a call that
+ *            timed out.  The append and read calls may use its status word.
  * Determinism: a token's result depends on the shapes and lengths of the call,
  * never on timing. */
 typedef struct {

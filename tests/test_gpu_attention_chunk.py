@@ -158,3 +158,28 @@ def test_pages_out_of_bounds_are_left_out_and_reported(q_len):
     assert (np.abs(ref.to_np(got[:q_len]) - out) <= ref.tolerance(out, weight, s, torch.bfloat16)).all()
     check(b, b.run(workspace=ws))
     assert g.nvfp4_device_status(ws) == (g.NVFP4_OK, 0)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_long_context(fmt):
+    """Chunks over a context that many CTAs share, with page offsets beyond 2^31 bytes, on both row-tile forms."""
+    kv, hk, d, ps = 40003, 2, 128, 32
+    pages = (1 << 31) // g.nvfp4_kv_page_bytes(ps, hk, d, fmt) + kv // ps + 64
+    cache = g.KVCache.empty(pages, ps, hk, d, fmt, device=DEV)
+    need = -(-kv // ps)
+    table = (pages - 1 - torch.arange(need, dtype=torch.int32)).to(DEV)[None].contiguous()
+    gen = torch.Generator(DEV).manual_seed(1)
+    k, v = (torch.randn(kv, hk, d, device=DEV, generator=gen).to(torch.bfloat16) for _ in range(2))
+    at = torch.arange(kv, device=DEV)
+    slots = table[0].long()[at // ps] * ps + at % ps
+    g.nvfp4_kv_append(cache, k, v, slots)
+    ck, cv = (ref.to_np(x) for x in g.nvfp4_kv_read(cache, slots))
+    lens = torch.tensor([kv], dtype=torch.int32, device=DEV)
+    for q_len in (20, 131):
+        q = torch.randn(q_len, 8, d, device=DEV, generator=gen).to(torch.bfloat16)
+        got = g.nvfp4_paged_attention(q, cache, table, lens)
+        rows = sorted({0, q_len // 2, q_len - 1})
+        see = ref.visible(q_len, kv)[rows]
+        out, weight, s = ref.attention(ref.to_np(q)[rows], ck, cv, see, d ** -0.5)
+        tol = ref.tolerance(out, weight, s, got.dtype) + kv * 2.0 ** -28 * np.abs(cv).max()
+        assert (np.abs(ref.to_np(got)[rows] - out) <= tol).all()
