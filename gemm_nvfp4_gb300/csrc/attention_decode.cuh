@@ -814,8 +814,13 @@ cudaError_t launch(const Call &c, uint8_t *workspace, int num_sms, cudaStream_t 
     static cudaError_t results[kMaxDevices];
     const auto kernel = decode_kernel<FMT, D, NT, WIDE>;
     Call call = c;
-    // An item costs a CTA about as much as four of its tiles.  (With few items that does not matter.)
-    call.item_cost = (int64_t)c.n_seqs * c.pool.heads >= 128 ? 4 : 0;
+    // An item costs a CTA about as much as four to six of its tiles.  E4M3, 8 KV heads: 64 sequences of 258 to 8192
+    // keys 61.9 us at 3, 59.7 at 4, 58.9 to 59.7 at 6, 59.6 at 9; 32 x 2000 with 24 rows 56.6 at 4, 55.9 at 6.
+    // Sequences x cached tokens, at 0 and 4: 4 x 4000 with 4 rows 15.8 and 13.3 us, 8 x 4000 20.5 and 18.9,
+    // 8 x 300 with 24 rows 23.5 and 14.6; slower is 12 x 1000 with 24 rows, 24.7 and 26.9.  With 8 items it
+    // takes CTAs from the tiles: 1 x 1000 with 24 rows 14.0 and 17.8.
+    const int64_t items = (int64_t)c.n_seqs * c.pool.heads;
+    call.item_cost = items >= 128 ? 6 : items >= 32 ? 4 : 0;
     const cudaError_t e = once_per_device(once, results, [kernel] {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     });
