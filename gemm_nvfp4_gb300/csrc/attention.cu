@@ -14,9 +14,9 @@ namespace {
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Which kernel: by the rows that share a KV head's keys.  At 32 rows the chunk
-// kernel took 35.5 us where the decode kernel took 42.4 (8 sequences of 4000 E4M3
-// keys, 32 and 8 heads), and 39.2 where it took 37.2 (one of 30000); at 24 rows
-// 35.6 against 39.5, and 39.1 against 34.4.  fp32 outputs keep the decode kernel's
+// kernel took 33.6 us where the decode kernel took 40.6 (8 sequences of 4000 E4M3
+// keys, 32 and 8 heads), and 40.1 where it took 37.2 (one of 30000); at 24 rows
+// 33.4 against 32.5, and 39.8 against 29.4.  fp32 outputs keep the decode kernel's
 // wide weights.
 bool use_chunk(int64_t rows, int out_dtype) { return rows > 24 && out_dtype == NVFP4_OUT_BF16; }
 

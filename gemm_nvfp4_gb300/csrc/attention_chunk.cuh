@@ -40,9 +40,10 @@
 // no pass for the maximum.
 //
 // Measured on one GB300: 2048 tokens behind 14336 cached ones (E4M3, 40 and 8 heads
-// of 128, 644 GFLOP) 507 us, 1.27 PFLOP/s, 0.65 of the measured bf16 rate;
-// 2 x 512 tokens in a window of 4096 98 us; 8 trees of 16 tokens over 2016 to
-// 6017 NVFP4 keys 37.5 us.  A tile of 256 rows and 128 keys takes 3900 clocks,
+// of 128, 644 GFLOP) 506 us, 1.27 PFLOP/s, 0.65 of the measured bf16 rate;
+// 2 x 512 tokens in a window of 4096 97 us; 8 trees of 16 tokens over 2016 to
+// 6017 NVFP4 keys 35.4 us; four ragged prefills of up to 1500 tokens (heads of 64,
+// NVFP4) 41 us.  A tile of 256 rows and 128 keys takes 3900 clocks,
 // 3300 of them the softmax warps' own chain; the MMAs alone would take 2600.
 #pragma once
 
