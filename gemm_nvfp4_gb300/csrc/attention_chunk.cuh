@@ -120,7 +120,11 @@ struct TileInfo {
 // Where the tile in the raw buffers lies.
 struct RawInfo {
     int key0, lo, hi;
+    int all_lo, all_hi;  // keys that every row of the item sees
     uint32_t present;
+
+    // whether some row does not see some key of the tile that another one may see
+    NVFP4_DEVINL bool mixed() const { return max(key0, lo) < all_lo || min(key0 + kTile, hi) > all_hi; }
 };
 
 // The part of an item that a CTA works on: the softmax warps' place in the CTA's range.
@@ -231,12 +235,6 @@ NVFP4_DEVINL void settle(uint32_t (&r)[32])
                    "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
 }
 
-NVFP4_DEVINL void sts128(uint32_t addr, uint4 v)
-{
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                 : "memory");
-}
-
 // Address of 16-byte chunk `oc` (8 elements) of row `r` of a 128-row f16
 // operand: 64-element column blocks of 128 rows x 128 bytes, chunks of a row
 // permuted by the 128-byte swizzle.
@@ -343,12 +341,14 @@ NVFP4_DEVINL bool load_role(const Call &c, const Range &range, const Item &first
     };
     int pages = 0, pages_behind = 0, used = 32;  // runs of `pages` that are behind us
     int64_t item_of_pages = -1;
+    int all_lo = 0, all_hi = 0;
     bool ok = true;
     uint32_t tile = 0;
     for (; tile < tiles; ++tile) {
         const int key0 = cur.key0(c), key = key0 + lane * run, head = cur.it.head;
         if (item_of_pages != cur.item_begin) {
             item_of_pages = cur.item_begin;
+            common_keys(c, cur.it, &all_lo, &all_hi);
             pages = look_up(key0 + lane * run);
             pages_behind = look_up((uint32_t)key0 + (32 + lane) * run);
             used = 0;
@@ -365,7 +365,7 @@ NVFP4_DEVINL bool load_role(const Call &c, const Range &range, const Item &first
             kv::report(c.pool.status, kStatusKvAttention);
         const uint32_t missing = __ballot_sync(0xFFFFFFFFu, want && !there);
         const uint32_t copied = __popc(__ballot_sync(0xFFFFFFFFu, there));
-        RawInfo info{key0, cur.it.lo, cur.it.hi, 0};
+        RawInfo info{key0, cur.it.lo, cur.it.hi, all_lo, all_hi, 0};
 #pragma unroll
         for (int g = 0; g < kTile / 16; ++g)
             info.present |= (missing >> (g * 16 / run) & 1 ? 0u : 1u) << g;
@@ -475,11 +475,11 @@ NVFP4_DEVINL void convert(uint32_t raw, int run, uint32_t operand, int tid, cons
                         asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
                             : "=r"(o[2 * j]), "=r"(o[2 * j + 1])
                             : "r"(w[2 * h + j]));
-                    sts128(swizzled[h] + to, make_uint4(sk::f16x2_mul(o[0], unit[i]), sk::f16x2_mul(o[1], unit[i]),
+                    tc::sts128(swizzled[h] + to, make_uint4(sk::f16x2_mul(o[0], unit[i]), sk::f16x2_mul(o[1], unit[i]),
                                                         sk::f16x2_mul(o[2], unit[i]), sk::f16x2_mul(o[3], unit[i])));
                 }
             } else {
-                const uint32_t sc = two[i] & keep[i];
+                const uint32_t sc = kv::without_nan(two[i] & keep[i]);
                 const uint32_t s[2] = {sk::f16x2_mul(e4m3x2_to_f16x2((uint16_t)((sc & 0xFFu) * 0x101u)), unit[i]),
                                        sk::f16x2_mul(e4m3x2_to_f16x2((uint16_t)((sc >> 8) * 0x101u)), unit[i])};
 #pragma unroll
@@ -487,10 +487,30 @@ NVFP4_DEVINL void convert(uint32_t raw, int run, uint32_t operand, int tid, cons
                     uint32_t o[4];
                     sk::e2m1x8_to_f16x2(w[h], o);
                     const uint32_t m = s[h / 2];
-                    sts128(swizzled[h] + to, make_uint4(sk::f16x2_mul(o[0], m), sk::f16x2_mul(o[1], m),
+                    tc::sts128(swizzled[h] + to, make_uint4(sk::f16x2_mul(o[0], m), sk::f16x2_mul(o[1], m),
                                                         sk::f16x2_mul(o[2], m), sk::f16x2_mul(o[3], m)));
                 }
             }
+        }
+    }
+}
+
+// Takes the codes that are not a number out of what the thread converts of a
+// tile of V (see clear_nan_codes in attention_decode.cuh; block scales: convert).
+template <int FMT, int D, bool SPLIT>
+NVFP4_DEVINL void clear_nan_codes(uint32_t raw, int run, int tid)
+{
+    using C = Cfg<FMT, D, SPLIT>;
+    using R = kv::Row<FMT, D>;
+    constexpr int per = C::kPerBlock;
+#pragma unroll 1
+    for (int i = 0; i < C::kRowsMine; ++i) {
+        const int row = tid / per + i * C::kRowStep, in_run = row & (run - 1);
+#pragma unroll
+        for (int b = 0; b < D / 64; ++b) {
+            const uint32_t at = raw + (row - in_run) * R::kBytes + in_run * R::kCode + (b * per + tid % per) * 16;
+            const uint4 w = tc::lds128(at);
+            tc::sts128(at, make_uint4(kv::without_nan(w.x), kv::without_nan(w.y), kv::without_nan(w.z), kv::without_nan(w.w)));
         }
     }
 }
@@ -539,6 +559,8 @@ NVFP4_DEVINL bool convert_role(uint32_t tiles, int run, Shared *sh, uint32_t sme
             unit[i] = a == kv::kNanRow || b == kv::kNanRow ? (is_v ? 0u : 0x7FFF7FFFu) : pow2_f16x2((int)a - top);
             rows[i] = a != 0 ? 0xFFFFFFFFu : 0u;
         }
+        if (FMT == NVFP4_KV_E4M3 && is_v && info.mixed())
+            clear_nan_codes<FMT, D, SPLIT>(raw, run, tid);
         convert<FMT, D, SPLIT>(raw, run, operand + st * C::kOperand, tid, unit, rows);
         if (!is_v) {
             const int v_top = largest_exp(other);
@@ -742,7 +764,7 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, ui
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     h[j] = f32x2_to_f16x2(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xFFFF0000u) * up);
-                sts128(operand_chunk(q_at, r, i), make_uint4(h[0], h[1], h[2], h[3]));
+                tc::sts128(operand_chunk(q_at, r, i), make_uint4(h[0], h[1], h[2], h[3]));
             }
             factor = fabsf(c.scale_log2) * __uint_as_float((uint32_t)(e - 14) << 23);
             if (SPLIT)

@@ -321,6 +321,28 @@ NVFP4_DEVINL uint32_t e2m1x2_to_bf16x2(uint32_t x, uint32_t mult)
     return bf16x2_mul((mag & 0x01C001C0u) | (sign & 0x80008000u), mult);
 }
 
+// Takes the bytes that are not a number (no append writes them, but a slot that
+// none has written may hold them) out of a step's V codes or block scales: a weight
+// of zero does not keep such a key away from the rows that do not see it.  Steps
+// whose keys every row sees need none of this.
+template <int FMT, int D, int NT>
+NVFP4_DEVINL void clear_nan_codes(uint32_t stage, int lane)
+{
+    using C = Cfg<FMT, D, NT>;
+    if constexpr (FMT == NVFP4_KV_E4M3) {
+#pragma unroll 1
+        for (int i = 0; i < C::kCodeBytes / 512; ++i) {
+            const uint32_t at = stage + C::kCodeBytes + i * 512 + lane * 16;
+            const uint4 w = tc::lds128(at);
+            tc::sts128(at, make_uint4(kv::without_nan(w.x), kv::without_nan(w.y), kv::without_nan(w.z), kv::without_nan(w.w)));
+        }
+    } else if (lane < C::kScaleBytes / 4) {
+        const uint32_t at = stage + C::kScaleAt + C::kScaleBytes + lane * 4;
+        tc::sts32(at, kv::without_nan(tc::lds32(at)));
+    }
+    __syncwarp();
+}
+
 template <int FMT, int D, int NT, bool WIDE, class F>
 NVFP4_DEVINL void for_v_fragments(uint32_t stage, int g, int t, F &&f)
 {
@@ -520,14 +542,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                 qf[i] = tc::lds64(q_addr + i * 256);
         }
         float factor[NT][2];
-        int lo_last = 0, hi_first = it.seq.kv;  // keys from lo_last to hi_first are seen by every row
-        {
-            int unused;
-            key_range(c, it.seq, it.row0 / c.group, &unused, &hi_first);
-            key_range(c, it.seq, (it.row0 + it.rows - 1) / c.group, &lo_last, &unused);
-            if (c.tree)
-                hi_first = min(hi_first, max(it.seq.past, 0));
-        }
+        int lo_last, hi_first;  // keys from lo_last to hi_first are seen by every row
+        common_keys(c, it, &lo_last, &hi_first);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             factor[n][0] = q_factor[n * 8 + 2 * t];
@@ -594,6 +610,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                 }
             }
             if (key < lo_last || key + kStep > hi_first) {
+                if (key < lo_last || min(key + kStep, it.seq.kv) > hi_first)
+                    clear_nan_codes<FMT, D, NT>(stage, lane);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
 #pragma unroll

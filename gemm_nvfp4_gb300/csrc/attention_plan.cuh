@@ -62,6 +62,16 @@ NVFP4_DEVINL void set_block(const Call &c, Item &it)
     it.units = it.tiles + c.item_cost;
 }
 
+// Keys [lo, hi) that every row of an item sees.
+NVFP4_DEVINL void common_keys(const Call &c, const Item &it, int *lo, int *hi)
+{
+    int unused;
+    key_range(c, it.seq, it.row0 / c.group, &unused, hi);
+    key_range(c, it.seq, (it.row0 + it.rows - 1) / c.group, lo, &unused);
+    if (c.tree)
+        *hi = min(*hi, max(it.seq.past, 0));
+}
+
 template <int RB>
 NVFP4_DEVINL int row_blocks(const Call &c, const Seq &s) { return (s.n * c.group + RB - 1) / RB; }
 

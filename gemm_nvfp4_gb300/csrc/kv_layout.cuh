@@ -45,6 +45,14 @@ NVFP4_DEVINL void report(uint32_t *status, uint32_t code)
 // 2^(e - 127) as a float; NaN for the mark of a row that is not a number.
 NVFP4_DEVINL float exp2_byte(uint32_t e) { return __uint_as_float(e == kNanRow ? 0x7FC00000u : e << 23); }
 
+// Four E4M3 bytes with those that are not a number (0x7F, 0xFF; the append
+// writes none) replaced by zeros.
+NVFP4_DEVINL uint32_t without_nan(uint32_t w)
+{
+    const uint32_t t = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+    return w & ~((t >> 7) * 0xFFu);
+}
+
 // Host: checks of a cache's description, and its Pool.  0, or an nvfp4_status.
 int make_pool(const nvfp4_kv_cache *c, void *workspace, size_t workspace_bytes, Pool *out);
 

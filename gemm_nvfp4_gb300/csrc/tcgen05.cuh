@@ -169,6 +169,14 @@ NVFP4_DEVINL uint32_t lds16(uint32_t addr)
     return v;
 }
 
+NVFP4_DEVINL void sts128(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+NVFP4_DEVINL void sts32(uint32_t addr, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory"); }
+
 NVFP4_DEVINL uint32_t lds32(uint32_t addr)
 {
     uint32_t v;

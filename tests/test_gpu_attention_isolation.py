@@ -1,0 +1,94 @@
+"""What nvfp4_paged_attention keeps away from a token: keys that it does not
+see, whatever their slots hold, and keys of very different magnitudes beside
+the ones it does see.  The bound is the one of include/nvfp4.h with nothing in
+it but the keys that a token sees."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import gemm_nvfp4_gb300 as g
+import kv_reference as ref
+from helpers import DEV
+from test_gpu_attention import FORMATS, Batch
+
+pytestmark = pytest.mark.gpu
+
+# (new tokens, query heads) over 2 KV heads: 8, 16, 24 rows (few-row kernel), 64 and 240 (both row-tile forms of the
+# many-row kernel); fp32 outputs take the few-row kernel whatever the rows
+SHAPES = [(2, 8), (4, 8), (6, 8), (16, 8), (60, 8)]
+
+
+def run_and_check(b: Batch, skip=None, scale=None, **kw):
+    """Every row, in both output types, against the definition.  `skip`: keys of each sequence; tokens that see one are
+    left out."""
+    group, scale = b.hq // b.hk, b.d ** -0.5 if scale is None else scale
+    pool, tree, at, checked = b.cache.pool.cpu().numpy(), kw.get("tree"), 0, 0
+    outs = [b.run(out_dtype=t, **kw) for t in (torch.bfloat16, torch.float32)]
+    for i, (n, kv) in enumerate(zip(b.q_lens, b.kv_lens)):
+        rows = slice(at, at + n)
+        at += n
+        k, v = ref.cache_rows(pool, b.slots(i, kv).numpy(), b.cache.page_size, b.d, b.cache.format)
+        see = ref.visible(n, kv, kw.get("causal", True), kw.get("window", 0), None if tree is None else tree[rows].cpu().numpy())
+        live = ~see[:, skip[i] if skip else []].any(1)
+        see = see[live]
+        out, weight, s = ref.attention(ref.to_np(b.q[rows])[live], k, v, see, scale)
+        for got in outs:
+            tol = ref.tolerance(out, weight, s, got.dtype)
+            if got.dtype == torch.bfloat16:  # f16 weights lose n * 2^-28 * max |V| over the n keys seen
+                for j in np.flatnonzero(see.any(1)):
+                    tol[j] += see[j].sum() * 2.0 ** -28 * np.repeat(np.abs(v[see[j]]).max((0, 2)), group)[:, None]
+            have = ref.to_np(got[rows])[live]
+            assert not np.isnan(have).any(), f"{got.dtype}: {np.isnan(have).sum()} NaN of {have.size}"
+            err = np.abs(have - out)
+            assert (err <= tol).all(), (f"{got.dtype}: {(err > tol).sum()} of {err.size} out of bounds, "
+                                        f"worst {(err / tol).max():.3g} of the bound")
+        checked += live.sum()
+    assert checked
+
+
+def batch(fmt, q_len, hq, d, seed=0, kv_lens=(200, 77)):
+    return Batch(fmt, [q_len] * len(kv_lens), [max(q_len + 1, n) for n in kv_lens], hq, 2, d, 16, seed=seed)
+
+
+def idle_tree(q_len, idle, seqs):
+    """Tree words in which a token descends from every live one before it, and none holds an idle place."""
+    words, above = [], 0
+    for i in range(q_len):
+        if i not in idle:
+            above |= 1 << i
+        words.append(above - (1 << 64) if above >> 63 else above)
+    return torch.tensor(words * seqs, device=DEV)
+
+
+def fill_slots(b: Batch, seq, keys, what):
+    """Puts bytes that no append writes into the slots of some keys."""
+    ps, d, fmt = b.cache.page_size, b.d, b.cache.format
+    cb, sb = (d, 0) if fmt == ref.E4M3 else (d // 2, d // 16)
+    rng = np.random.default_rng(5)
+    pool = b.cache.pool.cpu().numpy()
+    for s in b.slots(seq, b.kv_lens[seq]).numpy()[list(keys)]:
+        page, at = divmod(int(s), ps)
+        for first, n, is_e in ((at * cb, cb, False), (ps * cb + at * sb, sb, False), (ps * (cb + sb) + at, 1, True)):
+            value = {"NaN codes": 127 if is_e else 0xFF, "bytes of 255": 255, "largest codes": 254 if is_e else 0x7E,
+                     "random": rng.integers(0, 256, (b.hk, 2, n))}[what]
+            pool[page, :, :, first:first + n] = value
+    b.cache.pool.copy_(torch.from_numpy(pool))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("q_len,hq", SHAPES)
+@pytest.mark.parametrize("what", ["NaN codes", "bytes of 255"])
+@pytest.mark.parametrize("mode", ["tree", "causal", "window"])
+def test_slots_never_written(fmt, q_len, hq, what, mode):
+    """Idle draft places below kv_len (no slot, no tree bit), the slot of a token that others do not see, a slot that
+    has left every window."""
+    d = 128 if what != "bytes of 255" else 64
+    b = batch(fmt, q_len, hq, d, seed=q_len, kv_lens=(200, 150))
+    idle = sorted({1, q_len // 2, q_len - 1} - {0})
+    keys = {"tree": [[kv - q_len + i for i in idle] for kv in b.kv_lens], "causal": [[kv - 1] for kv in b.kv_lens],
+            "window": [[kv - q_len - 32, kv - 1] for kv in b.kv_lens]}[mode]
+    for seq, bad in enumerate(keys):
+        fill_slots(b, seq, bad, what)
+    run_and_check(b, skip=keys, **{"tree": dict(tree=idle_tree(q_len, idle, 2)), "causal": {}, "window": dict(window=30)}[mode])
