@@ -126,10 +126,16 @@ int nvfp4_paged_attention(const nvfp4_paged_attention_args *args, void *workspac
     if (rc != NVFP4_OK)
         return rc;
     const bool e4m3 = args->cache.format == NVFP4_KV_E4M3;
-    const auto launch = attn::use_chunk((int64_t)c.max_q_len * c.group, args->out_dtype)
-                            ? (e4m3 ? attn::launch_chunk_e4m3 : attn::launch_chunk_nvfp4)
-                            : (e4m3 ? attn::launch_decode_e4m3 : attn::launch_decode_nvfp4);
-    const cudaError_t e = launch(c, args->cache.head_dim, workspace, sms, (cudaStream_t)stream);
+    const auto decode = e4m3 ? attn::launch_decode_e4m3 : attn::launch_decode_nvfp4;
+    const auto chunk = e4m3 ? attn::launch_chunk_e4m3 : attn::launch_chunk_nvfp4;
+    c.redo = nullptr;
+    cudaError_t e = cudaSuccess;
+    if (attn::use_chunk((int64_t)c.max_q_len * c.group, args->out_dtype)) {
+        c.redo = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + attn::kRedoOffset);
+        e = chunk(c, args->cache.head_dim, workspace, sms, (cudaStream_t)stream);
+    }
+    if (e == cudaSuccess)
+        e = decode(c, args->cache.head_dim, workspace, sms, (cudaStream_t)stream);
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 

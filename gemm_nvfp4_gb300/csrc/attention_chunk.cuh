@@ -26,12 +26,20 @@
 // row tile, one the even and the other the odd key tiles, and their results
 // are joined at the end; otherwise half the pipeline would idle.
 //
-// f16 holds codes exactly.  A row's power of two is applied relative to the
-// largest in its tile of 128 keys, whose exponent goes to the softmax as one
-// factor (K) and one addend (V; see attention_decode.cuh): exact as long as the
-// rows of a tile lie within 2^14 of each other; smaller rows are rounded to a
-// multiple of 2^-24 of the tile's unit (its largest value is between 224 and
-// 2688 units), below what bf16 outputs show.  Outputs are bf16 only.
+// f16 holds codes exactly.  A row's power of two is applied relative to a unit of
+// its tile of 128 keys, that of the largest row, whose exponent goes to the softmax
+// as one factor (K) and one addend (V; see attention_decode.cuh).  That is exact
+// while no row lies more than 2^14 (kBelow) below the unit.  V's unit also sets
+// what the f16 weights of other tiles lose (for a row of Q, relative to the largest
+// unit beside its largest weight), so a key that a row does not see must not raise
+// it: in tiles whose keys some rows see and others do not, the unit is that of the
+// largest row that all see, as far as f16 holds the others' codes times up to
+// kAbove; 2^2 (kUnseen) more than that is within the bound.  A call with a tile that
+// breaks these rules is done again by the decode kernel, launched behind this one,
+// which keeps every key's exponent by itself; ordinarily that launch ends at
+// once.  (Handling such tiles here, in a loop of their own with each key's exponent
+// in the softmax, took 5 to 25 % of a long chunk's time even where no tile was one:
+// the roles' loops fill the instruction cache.)  Outputs are bf16 only.
 //
 // A tile's scores are made in two halves of 64 keys, each in columns of its own,
 // which its weights then take: the next half's scores are made while the
@@ -72,6 +80,7 @@ constexpr int kSharedBytes = 1024;  // barriers and the like (Shared)
 // What an item costs a CTA beside its tiles, in tiles.  (Ragged prefill of four sequences: 61.1 us at 0, 40.8 at 2,
 // 41.2 at 3, 43.7 at 8; 8 trees of 16 tokens 37.8, 35.8, 35.4, 35.4.)
 constexpr int kItemCost = 3;
+constexpr int kBelow = 14, kUnseen = 2;
 constexpr float kHeadroom = 7.f;
 constexpr float kMostWeight = 0x1p15f;  // of the weights of half a tile, in sum
 constexpr float kSumUnit = 0x1p-32f;
@@ -103,6 +112,8 @@ struct Cfg {
     static constexpr int kSlotFloats = kRows * (D + 2);
     // tensor memory columns
     static constexpr int kScoreCols = 0, kOutCols = 2 * kTile;
+    // log2 of how far a row of V may exceed its tile's unit: 448 * 2^7 and 2688 * 2^4 are f16 numbers
+    static constexpr int kAbove = FMT == NVFP4_KV_E4M3 ? 7 : 4;
     // 16-byte chunks of codes of a 64-element column block of a row.  A thread's lie in kRowsMine rows, kRowStep apart.
     static constexpr int kPerBlock = FMT == NVFP4_KV_E4M3 ? 4 : 2;
     static constexpr int kRowStep = kConvertThreads / kPerBlock, kRowsMine = kTile / kRowStep;
@@ -308,11 +319,6 @@ struct TileCursor {
     // to the first tile from u on
     NVFP4_DEVINL void settle(const Call &c) { find_tile<RB>(c, end, &it, &item_begin, &u); }
     NVFP4_DEVINL int key0(const Call &c) const { return (it.tile0 + (int)(u - item_begin - c.item_cost)) * kTile; }
-    NVFP4_DEVINL void step(const Call &c)
-    {
-        ++u;
-        settle(c);
-    }
 };
 
 // ---------------------------------------------------------------------------
@@ -331,7 +337,6 @@ NVFP4_DEVINL bool load_role(const Call &c, const Range &range, const Item &first
     const uint32_t n = is_v ? C::kRawVs : C::kRawKs;  // buffers
     const int shift = c.pool.page_shift, run = min(1 << shift, kTile), runs = kTile / run;
     TileCursor<C::kRows> cur{first, item_begin, range.begin, range.end};
-    cur.settle(c);
     const uint32_t tiles = sh->tiles;
     // Page numbers of 32 runs of the item at a time, and of the 32 behind them:
     // a table read per tile took longer than everything else the warp does.
@@ -344,7 +349,9 @@ NVFP4_DEVINL bool load_role(const Call &c, const Range &range, const Item &first
     int all_lo = 0, all_hi = 0;
     bool ok = true;
     uint32_t tile = 0;
+#pragma unroll 1
     for (; tile < tiles; ++tile) {
+        cur.settle(c);
         const int key0 = cur.key0(c), key = key0 + lane * run, head = cur.it.head;
         if (item_of_pages != cur.item_begin) {
             item_of_pages = cur.item_begin;
@@ -373,7 +380,7 @@ NVFP4_DEVINL bool load_role(const Call &c, const Range &range, const Item &first
         const uint8_t *const v = k + c.pool.block_bytes;
         const int at = key & ((1 << shift) - 1);
         const uint32_t scales = R::kCode << shift, exps = (R::kCode + R::kScale) << shift;
-        cur.step(c);
+        ++cur.u;
         const uint32_t slot = tile % n, round = tile / n;
         ok = round == 0 || tc::mbar_wait(&sh->raw_empty[is_v][slot], (round - 1) & 1);
         if (!(ok = __all_sync(0xFFFFFFFFu, ok)))
@@ -417,33 +424,64 @@ NVFP4_DEVINL uint32_t pow2_f16x2(int x)
     return f32x2_to_f16x2(f, f);
 }
 
-// Largest exponent byte of the rows that hold numbers; 127 if there is none.
+// Exponent bytes, four to a lane: 0 is a row that nobody sees, 255 one that is not a number.
+//
+// The warp's largest of rows that hold numbers; 0 or less if there is none.
 NVFP4_DEVINL int largest_exp(uint32_t four)
 {
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t e = four >> (8 * j) & 0xFFu;
-        m = max(m, e == kv::kNanRow ? 0u : e);
-    }
-    m = __reduce_max_sync(0xFFFFFFFFu, m);
-    return m == 0 ? 127 : (int)m;
+    const uint32_t a = (four & 0x00FF00FFu) + 0x00010001u, b = (four >> 8 & 0x00FF00FFu) + 0x00010001u;  // e + 1 mod 256
+    const uint32_t m = __vmaxu2(a & 0x00FF00FFu, b & 0x00FF00FFu);
+    return (int)__reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16)) - 1;
+}
+NVFP4_DEVINL int unit_of(int largest) { return largest <= 0 ? 127 : largest; }
+
+// A lane's smallest of rows that hold numbers other than zero (e = 27 is the
+// smallest that the append writes: such a row counts as zero); from 255 on: there is none.
+NVFP4_DEVINL int smallest_of(uint32_t four)
+{
+    const uint32_t a = (four & 0x00FF00FFu) + 0x00E400E4u, b = (four >> 8 & 0x00FF00FFu) + 0x00E400E4u;  // e - 28 mod 256
+    const uint32_t m = __vminu2(a & 0x00FF00FFu, b & 0x00FF00FFu);
+    return (int)min(m & 0xFFFFu, m >> 16) + 28;
+}
+
+// Bytes j of a word for keys first + j that lie in [lo, hi), all ones.
+NVFP4_DEVINL uint32_t range_bytes(int first, int lo, int hi)
+{
+    uint32_t m = 0xFFFFFFFFu;
+    if (first < lo)
+        m = first + 4 <= lo ? 0u : m << (8 * (lo - first));
+    if (first + 4 > hi)
+        m &= first >= hi ? 0u : 0xFFFFFFFFu >> (8 * (first + 4 - hi));
+    return m;
+}
+
+// Exponent byte of V's unit in a tile whose rows see different keys; its largest
+// exponent is `top`.  all: bytes of the keys that every row sees.
+template <int ABOVE>
+NVFP4_DEVINL int mixed_unit(uint32_t four, uint32_t all, int top, bool *redo)
+{
+    int from = largest_exp(four & all);
+    if (from <= 27)  // a row may see any one of the others alone
+        from = min(top, (int)__reduce_min_sync(0xFFFFFFFFu, (uint32_t)smallest_of(four)));
+    const int unit = max(from, top - ABOVE);
+    *redo |= unit > from + kUnseen;
+    return unit;
 }
 
 // A thread converts, in each of its kRowsMine rows of a tile of K or V, one
-// 16-byte chunk of codes of every 64-element column block.  Neighbouring lanes take the chunks of a block, then the next row; every
+// 16-byte chunk of codes of every 64-element column block; two rows (from its
+// i0-th on) a call, which keeps the loop short.  Neighbouring lanes take the chunks of a block, then the next row; every
 // other group of rows begins with the other block, so that both the reads (rows
 // of codes) and the writes (swizzled rows of f16) of 8 lanes lie on different
 // banks.  unit[i]: f16x2 factor of row i; keep[i]: all ones, or zero for a row
 // that is written as zeros whatever lies in the buffer.
 template <int FMT, int D, bool SPLIT>
-NVFP4_DEVINL void convert(uint32_t raw, int run, uint32_t operand, int tid, const uint32_t (&unit)[Cfg<FMT, D, SPLIT>::kRowsMine],
-                          const uint32_t (&keep)[Cfg<FMT, D, SPLIT>::kRowsMine])
+NVFP4_DEVINL void convert(uint32_t raw, int run, uint32_t operand, int tid, int i0, const uint32_t (&unit)[2], const uint32_t (&keep)[2])
 {
     using C = Cfg<FMT, D, SPLIT>;
     using R = kv::Row<FMT, D>;
-    constexpr int per = C::kPerBlock, rows = C::kRowsMine, kOut = 8 / per;  // 16-byte chunks of f16 from one of codes
-    const int row0 = tid / per, place = tid % per;
+    constexpr int per = C::kPerBlock, rows = 2, kOut = 8 / per;  // 16-byte chunks of f16 from one of codes
+    const int row0 = tid / per + i0 * C::kRowStep, place = tid % per;
     const int flip = D == 64 ? 0 : per == 4 ? row0 & 1 : row0 >> 1 & 1;
     uint32_t swizzled[kOut];
 #pragma unroll
@@ -503,10 +541,11 @@ NVFP4_DEVINL void clear_nan_codes(uint32_t raw, int run, int tid)
     using C = Cfg<FMT, D, SPLIT>;
     using R = kv::Row<FMT, D>;
     constexpr int per = C::kPerBlock;
+    asm volatile("" : "+r"(tid), "+r"(run), "+r"(raw));  // nothing of this is kept ready in the loop over the tiles
 #pragma unroll 1
     for (int i = 0; i < C::kRowsMine; ++i) {
         const int row = tid / per + i * C::kRowStep, in_run = row & (run - 1);
-#pragma unroll
+#pragma unroll 1
         for (int b = 0; b < D / 64; ++b) {
             const uint32_t at = raw + (row - in_run) * R::kBytes + in_run * R::kCode + (b * per + tid % per) * 16;
             const uint4 w = tc::lds128(at);
@@ -519,12 +558,13 @@ NVFP4_DEVINL void clear_nan_codes(uint32_t raw, int run, int tid)
 // the other's arithmetic (the same eight warps doing K, then V, of each tile took
 // 2400 clocks a tile).
 template <int FMT, int D, bool SPLIT>
-NVFP4_DEVINL bool convert_role(uint32_t tiles, int run, Shared *sh, uint32_t smem, int is_v, int tid)
+NVFP4_DEVINL bool convert_role(uint32_t tiles, int run, uint32_t *redo, Shared *sh, uint32_t smem, int is_v, int tid)
 {
     using C = Cfg<FMT, D, SPLIT>;
     using R = kv::Row<FMT, D>;
     constexpr int per = C::kPerBlock, mine = C::kRowsMine;
     const int lane = tid % 32;
+    bool redo_it = false;  // a row of the lane's lies too far from its tile's unit
     const uint32_t slots = is_v ? C::kRawVs : C::kRawKs;
     uint64_t *const full = is_v ? sh->v_full : sh->k_full, *const empty = is_v ? sh->v_empty : sh->k_empty;
     const uint32_t operand = smem + (is_v ? C::kVAt : C::kKAt);
@@ -541,32 +581,34 @@ NVFP4_DEVINL bool convert_role(uint32_t tiles, int run, Shared *sh, uint32_t sme
         uint32_t own = tc::lds32(raw + (4 * lane - in_run) * R::kBytes + run * (R::kCode + R::kScale) + in_run);
         uint32_t other = is_v ? own : tc::lds32(raw + C::kRawRows + 4 * lane);
         const int first = info.key0 + 4 * lane;
-        uint32_t keep = info.present >> (lane / 4) & 1 ? 0xFFFFFFFFu : 0u;
-        if (first < info.lo)
-            keep = first + 4 <= info.lo ? 0u : keep << (8 * (info.lo - first));
-        if (first + 4 > info.hi)
-            keep &= first >= info.hi ? 0u : 0xFFFFFFFFu >> (8 * (first + 4 - info.hi));
+        const uint32_t keep = info.present >> (lane / 4) & 1 ? range_bytes(first, info.lo, info.hi) : 0u;
         own &= keep;
         other &= keep;
-        const int top = largest_exp(own);
-        uint32_t unit[mine], rows[mine];
+        const bool mixed = info.mixed();
+        int v_unit = unit_of(largest_exp(other));
+        if (mixed) {
+            if (FMT == NVFP4_KV_E4M3 && is_v)
+                clear_nan_codes<FMT, D, SPLIT>(raw, run, tid);
+            v_unit = mixed_unit<C::kAbove>(other, range_bytes(first, info.all_lo, info.all_hi), v_unit, &redo_it);
+        }
+        const int top = is_v ? v_unit : unit_of(largest_exp(own));
+        redo_it |= smallest_of(own) < top - kBelow;
+#pragma unroll 1
+        for (int i0 = 0; i0 < mine; i0 += 2) {
+            uint32_t unit[2], rows[2];
 #pragma unroll
-        for (int i = 0; i < mine; ++i) {
-            const int row = tid / per + i * C::kRowStep, sh8 = 8 * (row & 3);
-            const uint32_t a = __shfl_sync(0xFFFFFFFFu, own, row >> 2) >> sh8 & 0xFFu;
-            const uint32_t b = __shfl_sync(0xFFFFFFFFu, other, row >> 2) >> sh8 & 0xFFu;
-            // a row that is not a number makes its scores NaN, whichever of K and V it is, and V's are zero
-            unit[i] = a == kv::kNanRow || b == kv::kNanRow ? (is_v ? 0u : 0x7FFF7FFFu) : pow2_f16x2((int)a - top);
-            rows[i] = a != 0 ? 0xFFFFFFFFu : 0u;
+            for (int i = 0; i < 2; ++i) {
+                const int row = tid / per + (i0 + i) * C::kRowStep, sh8 = 8 * (row & 3);
+                const uint32_t a = __shfl_sync(0xFFFFFFFFu, own, row >> 2) >> sh8 & 0xFFu;
+                const uint32_t b = __shfl_sync(0xFFFFFFFFu, other, row >> 2) >> sh8 & 0xFFu;
+                // a row that is not a number makes its scores NaN, whichever of K and V it is, and V's are zero
+                unit[i] = a == kv::kNanRow || b == kv::kNanRow ? (is_v ? 0u : 0x7FFF7FFFu) : pow2_f16x2((int)a - top);
+                rows[i] = a != 0 ? 0xFFFFFFFFu : 0u;
+            }
+            convert<FMT, D, SPLIT>(raw, run, operand + st * C::kOperand, tid, i0, unit, rows);
         }
-        if (FMT == NVFP4_KV_E4M3 && is_v && info.mixed())
-            clear_nan_codes<FMT, D, SPLIT>(raw, run, tid);
-        convert<FMT, D, SPLIT>(raw, run, operand + st * C::kOperand, tid, unit, rows);
-        if (!is_v) {
-            const int v_top = largest_exp(other);
-            if (tid == 0)
-                sh->info[tile % kInfos] = {kv::exp2_byte(top), (float)(v_top - 127), info.present, 0};
-        }
+        if (!is_v && tid == 0)
+            sh->info[tile % kInfos] = {kv::exp2_byte(top), (float)(v_unit - 127), info.present, 0};
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -574,6 +616,8 @@ NVFP4_DEVINL bool convert_role(uint32_t tiles, int run, Shared *sh, uint32_t sme
             tc::mbar_arrive(&sh->raw_empty[is_v][slot]);
         }
     }
+    if (redo_it)
+        *redo = 1;
     return true;
 }
 
@@ -1119,7 +1163,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
     } else if (warp < kSoftmaxWarps + kConvertWarps) {
         give_regs<kConvertRegs>();
         const int ct = tid - 32 * kSoftmaxWarps;
-        ok = convert_role<FMT, D, SPLIT>(tiles, min(1 << c.pool.page_shift, kTile), sh, smem, ct / kConvertThreads,
+        ok = convert_role<FMT, D, SPLIT>(tiles, min(1 << c.pool.page_shift, kTile), c.redo, sh, smem, ct / kConvertThreads,
                                          ct % kConvertThreads);
         code = kTimeoutConvert;
     } else {

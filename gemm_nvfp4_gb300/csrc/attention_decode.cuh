@@ -419,6 +419,14 @@ NVFP4_DEVINL void for_v_fragments(uint32_t stage, int g, int t, F &&f)
     }
 }
 
+// The end of a CTA.  In a call that is done again, the last one to come here clears
+// the request (every CTA has read it by then).
+NVFP4_DEVINL void leave(const Call &c)
+{
+    if (c.redo && threadIdx.x == 0 && atomicAdd(c.redo + 1, 1u) == gridDim.x - 1)
+        c.redo[0] = c.redo[1] = 0;
+}
+
 template <int FMT, int D, int NT, bool WIDE>
 __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_kernel(Call c, uint8_t *workspace)
 {
@@ -438,11 +446,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
 
     tc::griddep_launch_dependents();
     tc::griddep_wait();
+    if (c.redo && *c.redo == 0)
+        return;
     Range range;
     Item it;
     int64_t item_begin;
-    if (!find_range<C::kRows, kTile, kThreads>(c, scratch, &range, &it, &item_begin))
+    if (!find_range<C::kRows, kTile, kThreads>(c, scratch, &range, &it, &item_begin)) {
+        leave(c);
         return;
+    }
     const uint32_t ring = tc::smem_addr(smem) + warp * C::kStages * C::kStageBytes;
     const int page_mask = (1 << c.pool.page_shift) - 1;
     const LaneCopy copy = lane_copy<FMT, D, NT>(c, lane);
@@ -822,6 +834,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
             __syncthreads();  // the arena and the row tables are free again
         }
     }
+    leave(c);
 }
 
 template <int FMT, int D, int NT, bool WIDE>

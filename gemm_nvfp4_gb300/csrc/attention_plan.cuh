@@ -24,9 +24,10 @@
 namespace nvfp4 {
 namespace attn {
 
-// Workspace: the status word (in the first 256 bytes), an arrival counter per
+// Workspace: the status word and Call::redo (in the first 256 bytes), an arrival counter per
 // CTA at byte 256, then two partial slots per CTA.
 constexpr int kMaxCtas = 320;
+constexpr size_t kRedoOffset = kStatusWordOffset + 8;
 constexpr size_t kCounterOffset = 256;
 constexpr size_t kPartialOffset = kCounterOffset + kMaxCtas * sizeof(uint32_t);
 

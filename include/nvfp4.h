@@ -444,8 +444,13 @@ int nvfp4_kv_read(const nvfp4_kv_cache *cache, uint16_t *k, int64_t k_ld, uint16
  * |out - exact| <= (2^-10 + 2^-15 * S) * sum_j softmax_j |v_j|, plus the rounding
  * of out, with S = max_j |scale| * sum_d |q_d k_jd| (the fp32 sums of scores).
  * For bf16 outputs f16 loses what is below 2^-32 of a row's largest weight:
- * n * 2^-28 * max |V| over the n keys comes on top.  For fp32 outputs the weights
- * keep fp32's range (as two bf16 numbers each).
+ * n * 2^-28 * max |V| over the n keys that the token sees (of its KV head) comes
+ * on top.  For fp32 outputs the weights keep fp32's range (as two bf16 numbers
+ * each).  bf16 calls with more than 24 rows (new tokens times query heads of one KV head)
+ * are made for K and V rows whose largest magnitudes lie within about 2^14 of each
+ * other among the 128 keys around; where they do not, the call is made again by the
+ * kernel for few rows, within the same bound but in several times the time.  (Rows
+ * below 2^-91 count as zero beside larger ones there.)
  *
  * Requirements: q, out 16-byte aligned; q_ld and out_ld multiples of 8, at
  * least n_q_heads * head_dim; n_q_heads a multiple of n_kv_heads; tree only

@@ -79,7 +79,7 @@ def fill_slots(b: Batch, seq, keys, what):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("q_len,hq", SHAPES)
-@pytest.mark.parametrize("what", ["NaN codes", "bytes of 255"])
+@pytest.mark.parametrize("what", ["NaN codes", "bytes of 255", "largest codes", "random"])
 @pytest.mark.parametrize("mode", ["tree", "causal", "window"])
 def test_slots_never_written(fmt, q_len, hq, what, mode):
     """Idle draft places below kv_len (no slot, no tree bit), the slot of a token that others do not see, a slot that
@@ -92,3 +92,60 @@ def test_slots_never_written(fmt, q_len, hq, what, mode):
     for seq, bad in enumerate(keys):
         fill_slots(b, seq, bad, what)
     run_and_check(b, skip=keys, **{"tree": dict(tree=idle_tree(q_len, idle, 2)), "causal": {}, "window": dict(window=30)}[mode])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("q_len,hq", SHAPES)
+@pytest.mark.parametrize("which", ["k", "v", "both"])
+@pytest.mark.parametrize("r", [24, 40, 80])
+def test_loud_keys_that_are_not_seen(fmt, q_len, hq, which, r):
+    """A few rows 2^r larger than the others, in their tile of keys, reach the tokens that see them alone."""
+    d = 64 if r == 40 else 128
+    idle = [1, q_len - 1]
+    mode = {24: "tree", 40: "causal", 80: "window"}[r] if which != "both" else {24: "causal", 40: "window", 80: "tree"}[r]
+    b = batch(fmt, q_len, hq, d, seed=r)
+    gen = torch.Generator(DEV).manual_seed(r)
+    for seq, kv in enumerate(b.kv_lens):
+        k, v = (torch.randn(kv, 2, d, device=DEV, generator=gen) for _ in range(2))
+        loud = {"tree": [kv - q_len + i for i in idle], "causal": [kv - 1], "window": [max(0, kv - q_len - 25)]}[mode]
+        for x, name in ((k, "k"), (v, "v")):
+            if which in (name, "both"):
+                x[loud] *= 2.0 ** r
+        b.put(seq, k.to(torch.bfloat16), v.to(torch.bfloat16))
+    run_and_check(b, **{"tree": dict(tree=idle_tree(q_len, idle, 2)), "causal": {}, "window": dict(window=24)}[mode])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("q_len,hq", SHAPES)
+@pytest.mark.parametrize("r", [13, 15, 25, 60])
+@pytest.mark.parametrize("small_k", [False, True])
+def test_keys_far_apart_that_are_seen(fmt, q_len, hq, r, small_k):
+    """Few keys, every third with a V 2^r smaller than its neighbours' and, with small_k, a K as much smaller."""
+    d, kv = 128, q_len + 12
+    b = batch(fmt, q_len, hq, d, seed=r, kv_lens=(kv, kv + 130))
+    gen = torch.Generator(DEV).manual_seed(r)
+    for seq, n in enumerate(b.kv_lens):
+        k, v = (torch.randn(n, 2, d, device=DEV, generator=gen) for _ in range(2))
+        small = torch.arange(n, device=DEV) % 3 == 0
+        v[~small] *= 2.0 ** r
+        if small_k:
+            k[small] *= 2.0 ** -r
+        b.put(seq, k.to(torch.bfloat16), v.to(torch.bfloat16))
+    run_and_check(b, **(dict(causal=False) if r == 15 else dict(window=9) if r == 60 else {}))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("q_len,hq", [(16, 8), (60, 8)])
+def test_calls_that_are_made_again_leave_a_clean_workspace(fmt, q_len, hq):
+    """One workspace for calls whose rows lie far apart and for ordinary ones, in turn: the same results each time."""
+    loud, calm = batch(fmt, q_len, hq, 128, seed=1), batch(fmt, q_len, hq, 128, seed=2)
+    k, v = (torch.randn(200, 2, 128, device=DEV, generator=torch.Generator(DEV).manual_seed(s)) for s in (3, 4))
+    v[-1] *= 2.0 ** 40
+    loud.put(0, k.to(torch.bfloat16), v.to(torch.bfloat16))
+    ws = torch.zeros(g.nvfp4_paged_attention_workspace_bytes(loud.cache, loud.q, 2, q_len), dtype=torch.uint8, device=DEV)
+    first = [b.run(workspace=ws) for b in (loud, calm)]
+    for _ in range(3):
+        for b, want in zip((loud, calm), first):
+            assert torch.equal(b.run(workspace=ws), want)
+            assert (ws[:256] == 0).all()
+    assert torch.equal(calm.run(), first[1])
