@@ -81,6 +81,7 @@ constexpr int kSharedBytes = 1024;  // barriers and the like (Shared)
 // 41.2 at 3, 43.7 at 8; 8 trees of 16 tokens 37.8, 35.8, 35.4, 35.4.)
 constexpr int kItemCost = 3;
 constexpr int kBelow = 14, kUnseen = 2;
+constexpr int kNear = 48;  // of V's units, for the softmax sums (attention_decode.cuh)
 constexpr float kHeadroom = 7.f;
 constexpr float kMostWeight = 0x1p15f;  // of the weights of half a tile, in sum
 constexpr float kSumUnit = 0x1p-32f;
@@ -433,7 +434,7 @@ NVFP4_DEVINL int largest_exp(uint32_t four)
     const uint32_t m = __vmaxu2(a & 0x00FF00FFu, b & 0x00FF00FFu);
     return (int)__reduce_max_sync(0xFFFFFFFFu, max(m & 0xFFFFu, m >> 16)) - 1;
 }
-NVFP4_DEVINL int unit_of(int largest) { return largest <= 0 ? 127 : largest; }
+NVFP4_DEVINL int unit_of(int largest) { return largest <= 27 ? 127 : largest; }  // (27: all zero)
 
 // A lane's smallest of rows that hold numbers other than zero (e = 27 is the
 // smallest that the append writes: such a row counts as zero); from 255 on: there is none.
@@ -592,7 +593,7 @@ NVFP4_DEVINL bool convert_role(uint32_t tiles, int run, uint32_t *redo, Shared *
             v_unit = mixed_unit<C::kAbove>(other, range_bytes(first, info.all_lo, info.all_hi), v_unit, &redo_it);
         }
         const int top = is_v ? v_unit : unit_of(largest_exp(own));
-        redo_it |= smallest_of(own) < top - kBelow;
+        redo_it |= smallest_of(own) < top - kBelow || (uint32_t)(v_unit - 127 + kNear) > 2u * kNear;
 #pragma unroll 1
         for (int i0 = 0; i0 < mine; i0 += 2) {
             uint32_t unit[2], rows[2];

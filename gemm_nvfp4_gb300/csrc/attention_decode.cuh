@@ -28,7 +28,10 @@
 // added to the score's logarithm: with z = score + kv (in powers of two) the
 // weight P = 2^(z - M) already carries V's magnitude, its largest values are near
 // 2^7 whatever V's scale is, and f16 holds it to 2^-11; the softmax sum takes
-// P * 2^-kv.  M trails the running maximum: it moves, and the accumulators are
+// P * 2^-kv.  (Where V's exponents leave [-kNear, kNear], a key with most of the
+// softmax and a tiny V could have a P of 0 beside a huge V of little weight: such
+// a warp adds 2^(score - M) to its sum instead, and sums move to another M in two
+// steps, since the factor alone may be 0.)  M trails the running maximum: it moves, and the accumulators are
 // rescaled, only when some z exceeds it by 15 (P then stays below 2^15).
 //
 // f16 loses weights below 2^-32 of a row's largest.  That is far below what a bf16
@@ -53,7 +56,8 @@ constexpr int kStep = 16;      // keys of a warp step
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kHeadroom = 7.f, kSlack = 15.f;  // log2 of the largest P after and before a rescale
-constexpr float kSumUnit = 0x1p-32f;             // the sum is kept in units of 2^32: P * 2^-kv reaches 2^115
+constexpr float kNear = 48.f;                    // P is far from 0 for what matters to the sum: 2 * 48 + 30 < 126
+constexpr float kSumUnit = 0x1p-16f, kSumUnitLog2 = -16.f;  // the sum is kept in units of 2^16: P * 2^-kv reaches 2^115
 
 template <int FMT, int D, int NT>
 struct Cfg {
@@ -126,6 +130,22 @@ NVFP4_DEVINL float ex2(float x)
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+// 2^x, down to fp32's smallest numbers.
+NVFP4_DEVINL float ex2_subnormal(float x)
+{
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// s * 2^d for d <= 0 where 2^d may be too small for a float, but s * 2^d is not.
+constexpr float kTwoSteps = -100.f;
+NVFP4_DEVINL float times_pow2(float s, float d)
+{
+    const float half = ex2(0.5f * d);
+    return s * half * half;
 }
 
 // Four E4M3 bytes to two f16x2.
@@ -580,6 +600,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
         }
         int key = key0 + warp * kStep;
         uint32_t stage = ring;
+        bool far = false;  // the warp has met a V exponent beyond kNear
         for (int i = 0; i < mine; ++i, key += kWarps * kStep) {
             cp_async_wait<C::kStages - 2>();
             __syncwarp();
@@ -600,6 +621,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
             // exponents of keys g and g + 8
             float z[NT][4], unscale[2];
             bool over = false;
+            uint32_t v_exp[2];
             {
                 const uint32_t ea = stage + C::kExpAt + g;
                 // K's mark of a row that is not a number reads infinity here, and its codes are zeros: NaN again
@@ -611,6 +633,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                     // the byte as a float: 2^23 + ev - (2^23 + 127)
                     kv[h] = __uint_as_float(0x4B000000u | ev[h]) - 8388735.f;
                     kv[h] = ev[h] == kv::kNanRow ? NAN : ev[h] == 0 ? -INFINITY : kv[h];
+                    v_exp[h] = ev[h];
+                    over |= fabsf(kv[h]) > kNear && ev[h] != 0;
                     // finite for a NaN row too: masked, its weight of 0 must add 0
                     unscale[h] = __uint_as_float((uint32_t)max(254 - (int)ev[h], 0) << 23) * kSumUnit;
                 }
@@ -643,6 +667,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                     over |= z[n][h] > limit[n][h & 1];
             }
             if (__any_sync(0xFFFFFFFFu, over)) {
+                far |= __any_sync(0xFFFFFFFFu, v_exp[0] - 1 < 126 - (uint32_t)kNear || v_exp[0] > 127 + (uint32_t)kNear ||
+                                                   v_exp[1] - 1 < 126 - (uint32_t)kNear || v_exp[1] > 127 + (uint32_t)kNear);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -653,10 +679,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                         m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
                         const float next = fmaxf(top[n][h], m - kHeadroom);
                         const float shrink = next == -INFINITY ? 1.f : ex2(top[n][h] - next);
-                        top[n][h] = next;
                         limit[n][h] = next + kSlack;
                         base[n][h] = next == -INFINITY ? 0.f : next;
-                        sum[n][h] *= shrink;
+                        sum[n][h] = far && next != -INFINITY ? times_pow2(sum[n][h], top[n][h] - next) : sum[n][h] * shrink;
+                        top[n][h] = next;
 #pragma unroll
                         for (int k = 0; k < KS; ++k) {
                             o[n][k][h] *= shrink;
@@ -672,7 +698,15 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     w[h] = ex2(z[n][h] - base[n][h & 1]);
-                    sum[n][h & 1] = fmaf(w[h], unscale[h >> 1], sum[n][h & 1]);
+                    if (!far)
+                        sum[n][h & 1] = fmaf(w[h], unscale[h >> 1], sum[n][h & 1]);
+                }
+                if (far) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        const float kv = __uint_as_float(0x4B000000u | v_exp[h >> 1]) - 8388735.f;  // finite, whatever the row
+                        sum[n][h & 1] += ex2_subnormal(z[n][h] - (base[n][h & 1] + kv - kSumUnitLog2));
+                    }
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -744,7 +778,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                     const float2 v = *reinterpret_cast<const float2 *>(merge + (w * C::kRows + r) * C::kOutStride + d);
                     acc.x = fmaf(f, v.x, acc.x);
                     acc.y = fmaf(f, v.y, acc.y);
-                    l = fmaf(f, stats[(kWarps + w) * C::kRows + r], l);
+                    const float s = stats[(kWarps + w) * C::kRows + r];
+                    l = tw - m < kTwoSteps ? l + times_pow2(s, tw - m) : fmaf(f, s, l);
                 }
                 emit(r, d, acc, m, l);
             }
@@ -805,6 +840,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                     for (int i = lane; i < n; i += 32) {
                         const float tw = weight[i * C::kRows + r];
                         weight[i * C::kRows + r] = tw == -INFINITY ? 0.f : ex2(tw - m);
+                        // a sum (none is negative) that has been brought to m already: with its sign turned
+                        if (tw - m < kTwoSteps)
+                            weight[(n + i) * C::kRows + r] = -times_pow2(weight[(n + i) * C::kRows + r], tw - m);
                     }
                 }
                 __syncthreads();
@@ -820,7 +858,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                         acc.y = fmaf(f, v.y, acc.y);
                         acc.z = fmaf(f, v.z, acc.z);
                         acc.w = fmaf(f, v.w, acc.w);
-                        l = fmaf(f, weight[(n + i) * C::kRows + r], l);
+                        const float s = weight[(n + i) * C::kRows + r];
+                        l = s < 0.f ? l - s : fmaf(f, s, l);
                     }
                     store(r, d, make_float2(acc.x, acc.y), l);
                     store(r, d + 2, make_float2(acc.z, acc.w), l);

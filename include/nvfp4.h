@@ -448,9 +448,10 @@ int nvfp4_kv_read(const nvfp4_kv_cache *cache, uint16_t *k, int64_t k_ld, uint16
  * on top.  For fp32 outputs the weights keep fp32's range (as two bf16 numbers
  * each).  bf16 calls with more than 24 rows (new tokens times query heads of one KV head)
  * are made for K and V rows whose largest magnitudes lie within about 2^14 of each
- * other among the 128 keys around; where they do not, the call is made again by the
- * kernel for few rows, within the same bound but in several times the time.  (Rows
- * below 2^-91 count as zero beside larger ones there.)
+ * other among the 128 keys around, and V's between 2^-40 and 2^56; where they do
+ * not, the call is made again by the kernel for few rows, within the same bound but
+ * in several times the time.  (Rows below 2^-88 count as zero beside larger ones
+ * there.)
  *
  * Requirements: q, out 16-byte aligned; q_ld and out_ld multiples of 8, at
  * least n_q_heads * head_dim; n_q_heads a multiple of n_kv_heads; tree only

@@ -149,3 +149,27 @@ def test_calls_that_are_made_again_leave_a_clean_workspace(fmt, q_len, hq):
             assert torch.equal(b.run(workspace=ws), want)
             assert (ws[:256] == 0).all()
     assert torch.equal(calm.run(), first[1])
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("q_len,hq", SHAPES)
+@pytest.mark.parametrize("apart", ["interleaved", "blocks"])
+@pytest.mark.parametrize("low,high,weak", [(-90, 97, 40), (-60, 60, 20), (0, 97, 30)])
+def test_sums_over_values_far_apart(fmt, q_len, hq, apart, low, high, weak):
+    """Keys with nearly all of the softmax and a tiny V beside keys of 2^-weak of it and a huge V: the sum of the
+    weights is that of the former, whatever the V rows' magnitudes."""
+    d = 128
+    b = batch(fmt, q_len, hq, d, seed=1, kv_lens=(700, 300))
+    gen = torch.Generator(DEV).manual_seed(2)
+    # one channel of q and K decides: q . k * scale * log2(e) is 0 for the strong keys, -weak for the others
+    b.q.copy_(0.01 * torch.randn(b.q.shape, device=DEV, generator=gen))
+    b.q[:, :, 0] = 8.0
+    for seq, n in enumerate(b.kv_lens):
+        k, v = (torch.randn(n, 2, d, device=DEV, generator=gen) for _ in range(2))
+        k *= 0.01
+        at = torch.arange(n, device=DEV)
+        strong = at % 5 != 2 if apart == "interleaved" else at < n - q_len - 140
+        k[:, :, 0] = torch.where(strong, 0.0, -weak / 1.4427 / 8.0 / d ** -0.5)[:, None]
+        v *= torch.where(strong, 2.0 ** low, 2.0 ** high)[:, None, None]
+        b.put(seq, k.to(torch.bfloat16), v.to(torch.bfloat16))
+    run_and_check(b)
