@@ -209,14 +209,33 @@ def _check(status: int, where: str):
         raise NVFP4Error(status, where)
 
 
-def _workspace(op, N, M, K, device, workspace):
+def _new(stream, *shape, dtype, device):
+    """An output of a call on `stream` (None: the current one): memory of that stream, since nothing orders it behind
+    the current one's work, and not given to others before the current one's work so far is done with it."""
+    if stream is None:
+        return torch.empty(*shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(*shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _zeroed(stream, nbytes, device):
+    """A workspace of a call on `stream`, zero-filled there: only that stream's work sees it."""
+    if stream is None:
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.zeros(nbytes, dtype=torch.uint8, device=device)
+
+
+def _workspace(op, N, M, K, device, workspace, stream):
     need = nvfp4_workspace_bytes(op, N, M, K)
     if workspace is not None:
         return workspace, workspace.numel() * workspace.element_size()
     if need == 0:
         return None, 0
     # zero-filled: the skinny calls keep split-K counters in it
-    return torch.zeros(need, dtype=torch.uint8, device=device), need
+    return _zeroed(stream, need, device), need
 
 
 def _out_code(dtype) -> int:
@@ -232,10 +251,10 @@ def nvfp4_quantize(w: torch.Tensor, workspace: torch.Tensor | None = None,
     """fp32 [M, K] CUDA tensor -> NVFP4Weight (codes, scales, tensor scale)."""
     M, K = w.shape
     if out is None:
-        out = NVFP4Weight(torch.empty(M, K // 2, dtype=torch.uint8, device=w.device),
-                          torch.empty(M, K // 16, dtype=torch.uint8, device=w.device),
-                          torch.empty(1, dtype=torch.float32, device=w.device))
-    ws, ws_bytes = _workspace(NVFP4_OP_QUANTIZE, 0, M, K, w.device, workspace)
+        out = NVFP4Weight(_new(stream, M, K // 2, dtype=torch.uint8, device=w.device),
+                          _new(stream, M, K // 16, dtype=torch.uint8, device=w.device),
+                          _new(stream, 1, dtype=torch.float32, device=w.device))
+    ws, ws_bytes = _workspace(NVFP4_OP_QUANTIZE, 0, M, K, w.device, workspace, stream)
     st = load_library().nvfp4_quantize(_ptr(w), M, K, _ptr(out.codes), _ptr(out.scales),
                                        _ptr(out.tensor_scale), _ptr(ws), ws_bytes, _stream(stream))
     _check(st, "nvfp4_quantize")
@@ -249,10 +268,10 @@ def nvfp4_quantize_bf16(w: torch.Tensor, workspace: torch.Tensor | None = None,
         raise ValueError(f"nvfp4_quantize_bf16 takes bf16 weights, got {w.dtype}")
     M, K = w.shape
     if out is None:
-        out = NVFP4Weight(torch.empty(M, K // 2, dtype=torch.uint8, device=w.device),
-                          torch.empty(M, K // 16, dtype=torch.uint8, device=w.device),
-                          torch.empty(1, dtype=torch.float32, device=w.device))
-    ws, ws_bytes = _workspace(NVFP4_OP_QUANTIZE, 0, M, K, w.device, workspace)
+        out = NVFP4Weight(_new(stream, M, K // 2, dtype=torch.uint8, device=w.device),
+                          _new(stream, M, K // 16, dtype=torch.uint8, device=w.device),
+                          _new(stream, 1, dtype=torch.float32, device=w.device))
+    ws, ws_bytes = _workspace(NVFP4_OP_QUANTIZE, 0, M, K, w.device, workspace, stream)
     st = load_library().nvfp4_quantize_bf16(_ptr(w), M, K, _ptr(out.codes), _ptr(out.scales),
                                             _ptr(out.tensor_scale), _ptr(ws), ws_bytes, _stream(stream))
     _check(st, "nvfp4_quantize_bf16")
@@ -271,14 +290,14 @@ def nvfp4_import_blocked_scales(blocked: torch.Tensor, M: int, K: int,
     if blocked.numel() < nvfp4_blocked_scale_bytes(M, K):
         raise ValueError("blocked scale buffer smaller than nvfp4_blocked_scale_bytes(M, K)")
     if out is None:
-        out = torch.empty(M, K // 16, dtype=torch.uint8, device=blocked.device)
+        out = _new(stream, M, K // 16, dtype=torch.uint8, device=blocked.device)
     st = load_library().nvfp4_import_blocked_scales(_ptr(blocked), M, K, _ptr(out), _stream(stream))
     _check(st, "nvfp4_import_blocked_scales")
     return out
 
 
-def _new_out(N, M, dtype, device, out):
-    return out if out is not None else torch.empty(N, M, dtype=dtype, device=device)
+def _new_out(N, M, dtype, device, out, stream):
+    return out if out is not None else _new(stream, N, M, dtype=dtype, device=device)
 
 
 def nvfp4_gemv_skinny(x: torch.Tensor, W: NVFP4Weight, out_dtype=torch.float32,
@@ -286,8 +305,8 @@ def nvfp4_gemv_skinny(x: torch.Tensor, W: NVFP4Weight, out_dtype=torch.float32,
                       stream=None) -> torch.Tensor:
     """y[N, M] = x[N, K] (bf16) . dequant(W)^T for N = 1..16."""
     N, K = x.shape
-    y = _new_out(N, W.M, out_dtype, x.device, out)
-    ws, ws_bytes = _workspace(NVFP4_OP_GEMV_SKINNY, N, W.M, K, x.device, workspace)
+    y = _new_out(N, W.M, out_dtype, x.device, out, stream)
+    ws, ws_bytes = _workspace(NVFP4_OP_GEMV_SKINNY, N, W.M, K, x.device, workspace, stream)
     st = load_library().nvfp4_gemv_skinny(_ptr(x), N, _ptr(W.codes), _ptr(W.scales), _ptr(W.tensor_scale),
                                           W.M, K, _ptr(y), _out_code(y.dtype), _ptr(ws), ws_bytes,
                                           _stream(stream))
@@ -300,8 +319,8 @@ def nvfp4_gateup_swiglu(x: torch.Tensor, Wg: NVFP4Weight, Wu: NVFP4Weight, out_d
                         stream=None) -> torch.Tensor:
     """h[N, M] = silu(x . Wg^T) * (x . Wu^T), any N >= 1."""
     N, K = x.shape
-    h = _new_out(N, Wg.M, out_dtype, x.device, out)
-    ws, ws_bytes = _workspace(NVFP4_OP_GATEUP_SWIGLU, N, Wg.M, K, x.device, workspace)
+    h = _new_out(N, Wg.M, out_dtype, x.device, out, stream)
+    ws, ws_bytes = _workspace(NVFP4_OP_GATEUP_SWIGLU, N, Wg.M, K, x.device, workspace, stream)
     st = load_library().nvfp4_gateup_swiglu(_ptr(x), N, _ptr(Wg.codes), _ptr(Wg.scales),
                                             _ptr(Wg.tensor_scale), _ptr(Wu.codes), _ptr(Wu.scales),
                                             _ptr(Wu.tensor_scale), Wg.M, K, _ptr(h), _out_code(h.dtype),
@@ -315,8 +334,8 @@ def nvfp4_gemm_prefill(x: torch.Tensor, W: NVFP4Weight, out_dtype=torch.float32,
                        stream=None) -> torch.Tensor:
     """y[N, M] = x[N, K] (bf16) . dequant(W)^T, any N >= 1 (tensor cores for N > 16)."""
     N, K = x.shape
-    y = _new_out(N, W.M, out_dtype, x.device, out)
-    ws, ws_bytes = _workspace(NVFP4_OP_GEMM_PREFILL, N, W.M, K, x.device, workspace)
+    y = _new_out(N, W.M, out_dtype, x.device, out, stream)
+    ws, ws_bytes = _workspace(NVFP4_OP_GEMM_PREFILL, N, W.M, K, x.device, workspace, stream)
     st = load_library().nvfp4_gemm_prefill(_ptr(x), N, _ptr(W.codes), _ptr(W.scales), _ptr(W.tensor_scale),
                                            W.M, K, _ptr(y), _out_code(y.dtype), _ptr(ws), ws_bytes,
                                            _stream(stream))
@@ -364,11 +383,11 @@ class FP6Weight:
         return self.codes.numel() + self.scales.numel()
 
 
-def _fp6_out(M, K, device, out):
+def _fp6_out(M, K, device, out, stream):
     if out is not None:
         return out
-    return FP6Weight(torch.empty(M, K // 8 * 6, dtype=torch.uint8, device=device),
-                     torch.empty(M, K // 128, dtype=torch.uint8, device=device))
+    return FP6Weight(_new(stream, M, K // 8 * 6, dtype=torch.uint8, device=device),
+                     _new(stream, M, K // 128, dtype=torch.uint8, device=device))
 
 
 def nvfp4_fp6_quantize(w: torch.Tensor, out: FP6Weight | None = None, stream=None) -> FP6Weight:
@@ -376,7 +395,7 @@ def nvfp4_fp6_quantize(w: torch.Tensor, out: FP6Weight | None = None, stream=Non
     if w.dtype != torch.float32:
         raise ValueError(f"nvfp4_fp6_quantize takes fp32 weights, got {w.dtype}")
     M, K = w.shape
-    out = _fp6_out(M, K, w.device, out)
+    out = _fp6_out(M, K, w.device, out, stream)
     st = load_library().nvfp4_fp6_quantize(_ptr(w), M, K, _ptr(out.codes), _ptr(out.scales), _stream(stream))
     _check(st, "nvfp4_fp6_quantize")
     return out
@@ -387,7 +406,7 @@ def nvfp4_fp6_quantize_bf16(w: torch.Tensor, out: FP6Weight | None = None, strea
     if w.dtype != torch.bfloat16:
         raise ValueError(f"nvfp4_fp6_quantize_bf16 takes bf16 weights, got {w.dtype}")
     M, K = w.shape
-    out = _fp6_out(M, K, w.device, out)
+    out = _fp6_out(M, K, w.device, out, stream)
     st = load_library().nvfp4_fp6_quantize_bf16(_ptr(w), M, K, _ptr(out.codes), _ptr(out.scales),
                                                 _stream(stream))
     _check(st, "nvfp4_fp6_quantize_bf16")
@@ -398,8 +417,8 @@ def nvfp4_fp6_gemm(x: torch.Tensor, W: FP6Weight, out_dtype=torch.float32, out: 
                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y[N, M] = x[N, K] (bf16) . dequant(W)^T for FP6 weights, any N >= 1."""
     N, K = x.shape
-    y = _new_out(N, W.M, out_dtype, x.device, out)
-    ws, ws_bytes = _workspace(NVFP4_OP_FP6_GEMM, N, W.M, K, x.device, workspace)
+    y = _new_out(N, W.M, out_dtype, x.device, out, stream)
+    ws, ws_bytes = _workspace(NVFP4_OP_FP6_GEMM, N, W.M, K, x.device, workspace, stream)
     st = load_library().nvfp4_fp6_gemm(_ptr(x), N, _ptr(W.codes), _ptr(W.scales), W.M, K, _ptr(y),
                                        _out_code(y.dtype), _ptr(ws), ws_bytes, _stream(stream))
     _check(st, "nvfp4_fp6_gemm")
@@ -411,8 +430,8 @@ def nvfp4_fp6_gateup_swiglu(x: torch.Tensor, Wg: FP6Weight, Wu: FP6Weight, out_d
                             stream=None) -> torch.Tensor:
     """h[N, M] = silu(x . Wg^T) * (x . Wu^T) for FP6 weights, any N >= 1."""
     N, K = x.shape
-    h = _new_out(N, Wg.M, out_dtype, x.device, out)
-    ws, ws_bytes = _workspace(NVFP4_OP_FP6_GATEUP_SWIGLU, N, Wg.M, K, x.device, workspace)
+    h = _new_out(N, Wg.M, out_dtype, x.device, out, stream)
+    ws, ws_bytes = _workspace(NVFP4_OP_FP6_GATEUP_SWIGLU, N, Wg.M, K, x.device, workspace, stream)
     st = load_library().nvfp4_fp6_gateup_swiglu(_ptr(x), N, _ptr(Wg.codes), _ptr(Wg.scales), _ptr(Wu.codes),
                                                 _ptr(Wu.scales), Wg.M, K, _ptr(h), _out_code(h.dtype),
                                                 _ptr(ws), ws_bytes, _stream(stream))
@@ -426,7 +445,7 @@ def nvfp4_gemv_skinny_noalloc(x: torch.Tensor, W: NVFP4Weight, out_dtype=torch.f
     callers that cannot allocate device memory; see include/nvfp4.h).  The
     output tensor is the only buffer created here, and only when `out` is None."""
     N, K = x.shape
-    y = _new_out(N, W.M, out_dtype, x.device, out)
+    y = _new_out(N, W.M, out_dtype, x.device, out, stream)
     st = load_library().nvfp4_gemv_skinny_noalloc(_ptr(x), N, _ptr(W.codes), _ptr(W.scales),
                                                   _ptr(W.tensor_scale), W.M, K, _ptr(y),
                                                   _out_code(y.dtype), _stream(stream))
@@ -516,7 +535,7 @@ def nvfp4_stream_plan(jobs, N: int, device=None, stream=None) -> StreamPlan:
     if need == 0:
         raise NVFP4Error(NVFP4_ERR_INVALID_ARG, "nvfp4_stream_plan_bytes")
     dev = device or jobs[0].y.device
-    buf = torch.empty(need, dtype=torch.uint8, device=dev)
+    buf = _new(stream, need, dtype=torch.uint8, device=dev)
     st = lib.nvfp4_stream_plan(arr, len(jobs), int(N), _ptr(buf), need, _stream(stream))
     _check(st, "nvfp4_stream_plan")
     return StreamPlan(buf, jobs, int(N))
@@ -633,7 +652,7 @@ def nvfp4_kv_read(cache: KVCache, slots: torch.Tensor, out: tuple[torch.Tensor, 
     of negative slots are zero."""
     c = cache.c()
     if out is None:
-        out = tuple(torch.empty(slots.numel(), c.n_kv_heads, c.head_dim, dtype=torch.bfloat16, device=slots.device)
+        out = tuple(_new(stream, slots.numel(), c.n_kv_heads, c.head_dim, dtype=torch.bfloat16, device=slots.device)
                     for _ in range(2))
     k, v = out
     k_ld = _head_rows(k, c.n_kv_heads, c.head_dim, _BF16, "k")
@@ -690,7 +709,7 @@ def nvfp4_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Te
             raise ValueError(f"{total_q} tokens are not the same number for each of {n_seqs} sequences: give q_offsets")
         max_q_len = total_q // n_seqs
     if out is None:
-        out = torch.empty(total_q, heads, head_dim, dtype=out_dtype, device=q.device)
+        out = _new(stream, total_q, heads, head_dim, dtype=out_dtype, device=q.device)
     out_ld = _head_rows(out, heads, c.head_dim, (torch.bfloat16, torch.float32), "out")
     if out.shape[0] != total_q:
         raise ValueError(f"q has {total_q} tokens, out {out.shape[0]}")
@@ -705,8 +724,7 @@ def nvfp4_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Te
     lib = load_library()
     if workspace is None:
         # zero-filled: the call keeps arrival counters in it
-        workspace = torch.zeros(lib.nvfp4_paged_attention_workspace_bytes(ctypes.byref(a)), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _zeroed(stream, lib.nvfp4_paged_attention_workspace_bytes(ctypes.byref(a)), q.device)
     ws, ws_bytes = _buffer(workspace)
     st = lib.nvfp4_paged_attention(ctypes.byref(a), ws, ws_bytes, _stream_of(q, stream))
     if st:
