@@ -560,12 +560,34 @@ def nvfp4_kv_page_bytes(page_size: int, n_kv_heads: int, head_dim: int, format: 
 # Handle of the current stream without a Stream object around it: these calls
 # take a few microseconds, and making that object is one or two of them.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _launch(call, where, tensors, *args):
+    """call(*args) with the device of the tensors (those that are not None) current; they must share one."""
+    device = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0 or (device >= 0 and d != device):
+                raise ValueError(f"{where}: all tensors must be on one CUDA device, got "
+                                 f"{', '.join(str(x.device) for x in tensors if x is not None)}")
+            device = d
+    if device == _current_device():
+        st = call(*args)
+    else:
+        with torch.cuda.device(device):
+            st = call(*args)
+    if st:
+        _check(st, where)
 
 
 def _stream_of(t: torch.Tensor, stream) -> int:
     """Stream handle: `stream`, or the current one of the device that holds t."""
     if stream is not None:
         return stream.cuda_stream
+    if t.get_device() < 0:
+        return None  # refused before anything is launched
     return _raw_stream(t.get_device()) if _raw_stream else torch.cuda.current_stream(t.device).cuda_stream
 
 
@@ -640,10 +662,8 @@ def nvfp4_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: tor
         raise ValueError(f"k has {k.shape[0]} tokens, v {v.shape[0]}")
     _check_slots(slots, k.shape[0])
     ws, ws_bytes = _buffer(workspace)
-    st = load_library().nvfp4_kv_append(ctypes.byref(c), k.data_ptr(), k_ld, v.data_ptr(), v_ld, slots.data_ptr(),
-                                        k.shape[0], ws, ws_bytes, _stream_of(slots, stream))
-    if st:
-        _check(st, "nvfp4_kv_append")
+    _launch(load_library().nvfp4_kv_append, "nvfp4_kv_append", (slots, cache.pool, k, v, workspace), ctypes.byref(c),
+            k.data_ptr(), k_ld, v.data_ptr(), v_ld, slots.data_ptr(), k.shape[0], ws, ws_bytes, _stream_of(slots, stream))
 
 
 def nvfp4_kv_read(cache: KVCache, slots: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None,
@@ -660,10 +680,8 @@ def nvfp4_kv_read(cache: KVCache, slots: torch.Tensor, out: tuple[torch.Tensor, 
     _check_slots(slots, k.shape[0])
     _check_slots(slots, v.shape[0])
     ws, ws_bytes = _buffer(workspace)
-    st = load_library().nvfp4_kv_read(ctypes.byref(c), k.data_ptr(), k_ld, v.data_ptr(), v_ld, slots.data_ptr(),
-                                      k.shape[0], ws, ws_bytes, _stream_of(slots, stream))
-    if st:
-        _check(st, "nvfp4_kv_read")
+    _launch(load_library().nvfp4_kv_read, "nvfp4_kv_read", (slots, cache.pool, k, v, workspace), ctypes.byref(c),
+            k.data_ptr(), k_ld, v.data_ptr(), v_ld, slots.data_ptr(), k.shape[0], ws, ws_bytes, _stream_of(slots, stream))
     return out
 
 
@@ -726,7 +744,7 @@ def nvfp4_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Te
         # zero-filled: the call keeps arrival counters in it
         workspace = _zeroed(stream, lib.nvfp4_paged_attention_workspace_bytes(ctypes.byref(a)), q.device)
     ws, ws_bytes = _buffer(workspace)
-    st = lib.nvfp4_paged_attention(ctypes.byref(a), ws, ws_bytes, _stream_of(q, stream))
-    if st:
-        _check(st, "nvfp4_paged_attention")
+    _launch(lib.nvfp4_paged_attention, "nvfp4_paged_attention",
+            (q, cache.pool, block_table, kv_lens, q_offsets, tree, out, workspace), ctypes.byref(a), ws, ws_bytes,
+            _stream_of(q, stream))
     return out
