@@ -65,7 +65,7 @@ NVFP4_DEVINL Seq load_seq(const Call &c, int b)
         bad = true;
     }
     if (bad)
-        kv::report(c.pool.status, kStatusKvAttention);
+        kv::report_index(c.pool.status, kStatusKvAttention);
     return s;
 }
 
@@ -87,7 +87,7 @@ NVFP4_DEVINL int page_of(const Call &c, int b, int j)
 {
     const int page = c.table[(int64_t)b * c.table_width + (j >> c.pool.page_shift)];
     if (page < 0 || page >= c.pool.n_pages) {
-        kv::report(c.pool.status, kStatusKvAttention);
+        kv::report_index(c.pool.status, kStatusKvAttention);
         return -1;
     }
     return page;

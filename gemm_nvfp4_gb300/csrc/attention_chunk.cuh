@@ -370,7 +370,7 @@ NVFP4_DEVINL bool load_role(const Call &c, const Range &range, const Item &first
         const bool want = lane < runs && key < cur.it.hi && key + run > cur.it.lo;
         const bool there = want && page >= 0 && page < c.pool.n_pages;
         if (want && !there)
-            kv::report(c.pool.status, kStatusKvAttention);
+            kv::report_index(c.pool.status, kStatusKvAttention);
         const uint32_t missing = __ballot_sync(0xFFFFFFFFu, want && !there);
         const uint32_t copied = __popc(__ballot_sync(0xFFFFFFFFu, there));
         RawInfo info{key0, cur.it.lo, cur.it.hi, all_lo, all_hi, 0};
@@ -1183,7 +1183,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
         }
     }
     if (!ok)
-        kv::report(c.pool.status, code);
+        kv::report_timeout(c.pool.status, code);
     tc::fence_before_sync();
     __syncthreads();
     if (warp == kSoftmaxWarps + kConvertWarps + 2)

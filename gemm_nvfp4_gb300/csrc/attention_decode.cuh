@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                 const bool used = key < it.hi && key + kStep > it.lo;
                 int valid = used ? min(kStep, it.seq.kv - key) : 0;
                 if (used && (page < 0 || page >= c.pool.n_pages)) {
-                    kv::report(c.pool.status, kStatusKvAttention);
+                    kv::report_index(c.pool.status, kStatusKvAttention);
                     valid = 0;
                 }
                 const uint8_t *blk = head_blk + (valid > 0 ? (int64_t)((uint64_t)(uint32_t)page * (uint32_t)c.pool.page_bytes) : 0);

@@ -111,7 +111,7 @@ NVFP4_DEVINL Place place_of(const Pool &pool, int64_t slot, bool report_it, uint
     p.at = (int)(slot & ((1 << pool.page_shift) - 1));
     p.there = slot >= 0 && p.page < pool.n_pages;
     if (slot >= 0 && !p.there && report_it)
-        report(pool.status, code);
+        report_index(pool.status, code);
     return p;
 }
 

@@ -36,7 +36,15 @@ NVFP4_DEVINL uint8_t *block_ptr(const Pool &p, int64_t page, int head, int is_v)
     return p.base + page * p.page_bytes + (int64_t)(head * 2 + is_v) * p.block_bytes;
 }
 
-NVFP4_DEVINL void report(uint32_t *status, uint32_t code)
+// Stores the code of an index outside its bounds, unless the status word holds one
+// already: a timeout's must stay, since it tells that the workspace is not clean.
+NVFP4_DEVINL void report_index(uint32_t *status, uint32_t code)
+{
+    if (status)
+        atomicCAS(status, 0u, code);
+}
+// Stores the code of a wait that ran out.
+NVFP4_DEVINL void report_timeout(uint32_t *status, uint32_t code)
 {
     if (status)
         atomicExch(status, code);

@@ -559,9 +559,10 @@ int nvfp4_noalloc_selftest_wait_timeout(nvfp4_stream_t stream);
  * whose bounded pipeline wait runs out (2 s) stores a nonzero code there and
  * returns: 1..8 from the prefill kernel, 10 from its split-mode reduction
  * (a contributor or tile outside the plan, which the host's plan rules out),
- * 11..25 from the skinny kernel, 51..54 from nvfp4_paged_attention, 127 from nvfp4_selftest_wait_timeout.  No
- * kernel clears the word, so it reports
- * any failure since it was last cleared; it starts clean when the workspace is
+ * 11..25 from the skinny kernel, 51..54 from nvfp4_paged_attention, 127 from
+ * nvfp4_selftest_wait_timeout.  No kernel clears the word, so it reports any
+ * failure since it was last cleared; the codes 41..43 of the KV-cache calls are
+ * stored only where it is zero, so that a timeout stays visible.  It starts clean when the workspace is
  * zero-filled (required for the skinny calls; do it for a prefill workspace
  * too before reading its status).  A quantise call overwrites the word. */
 #define NVFP4_STATUS_WORD_OFFSET 128
