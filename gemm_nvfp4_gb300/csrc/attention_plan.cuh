@@ -108,7 +108,8 @@ template <int RB, int TK, int THREADS>
 __device__ bool find_range(const Call &c, int64_t *scratch, Range *range, Item *item, int64_t *item_begin)
 {
     const int tid = threadIdx.x, lane = tid % 32, warp = tid / 32;
-    const int most = (int)(((int64_t)c.max_q_len * c.group + RB - 1) / RB);  // row blocks of a sequence
+    // row blocks of a sequence (one at least, so that its lengths are looked at whatever max_q_len)
+    const int most = max(1, (int)(((int64_t)c.max_q_len * c.group + RB - 1) / RB));
     const int64_t numbers = (int64_t)c.n_seqs * most;
     const int64_t per = numbers <= THREADS ? 1 : (numbers + THREADS - 1) / THREADS;
     const int64_t n0 = min(tid * per, numbers), n1 = min(n0 + per, numbers);

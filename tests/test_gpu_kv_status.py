@@ -33,3 +33,17 @@ def test_an_index_does_not_hide_a_timeout(q_len):
     b.run(workspace=ws)
     assert g.nvfp4_device_status(ws) == (g.NVFP4_ERR_DEVICE_INDEX, 43)
     assert g.nvfp4_device_status(ws) == (g.NVFP4_OK, 0)
+
+
+@pytest.mark.parametrize("hq", [8, 72])
+def test_more_tokens_than_max_q_len_zero(hq):
+    """max_q_len = 0 with offsets that hold tokens: no row is written, and code 43 says so."""
+    b = Batch(g.NVFP4_KV_NVFP4, [3, 5], [60, 90], hq, 2, 64, 16)
+    out = torch.full_like(b.q, 7.0)
+    ws = torch.zeros(g.nvfp4_paged_attention_workspace_bytes(b.cache, b.q, 2, 0), dtype=torch.uint8, device=DEV)
+    g.nvfp4_paged_attention(b.q, b.cache, b.table, b.lens, q_offsets=b.offsets, max_q_len=0, out=out, workspace=ws)
+    assert g.nvfp4_device_status(ws) == (g.NVFP4_ERR_DEVICE_INDEX, 43)
+    assert (out == 7).all()
+    b.offsets.zero_()  # no sequence has any: nothing to report
+    g.nvfp4_paged_attention(b.q, b.cache, b.table, b.lens, q_offsets=b.offsets, max_q_len=0, out=out, workspace=ws)
+    assert g.nvfp4_device_status(ws) == (g.NVFP4_OK, 0)
