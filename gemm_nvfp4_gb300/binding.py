@@ -639,7 +639,7 @@ def _head_rows(t, heads, head_dim, dtypes, what):
                          f"got {t.dtype} {list(shape)}")
     if stride[2] != 1 or (heads > 1 and stride[1] != head_dim):
         raise ValueError(f"{what}: the heads of a token must lie side by side (strides {stride})")
-    return stride[0] if shape[0] > 1 else max(stride[0], heads * head_dim)
+    return stride[0] if shape[0] > 1 else heads * head_dim  # one token's stride is never used
 
 
 _BF16 = (torch.bfloat16,)
@@ -706,7 +706,7 @@ def nvfp4_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Te
                           stream=None) -> torch.Tensor:
     """Attention of new tokens q (bf16 [total_q, n_q_heads, head_dim]) over the cache.
 
-    block_table int32 [n_seqs, width], kv_lens int32 [n_seqs] (keys in the
+    block_table int32 [n_seqs, width] (contiguous, as the other index tensors), kv_lens int32 [n_seqs] (keys in the
     cache, the new tokens' own among them when causal); q_offsets int32
     [n_seqs + 1] for sequences with different numbers of new tokens, with
     max_q_len their largest; tree int64 [total_q], bit j of a token's word:
