@@ -81,18 +81,6 @@ NVFP4_DEVINL void key_range(const Call &c, const Seq &s, int i, int *lo, int *hi
     }
 }
 
-// Page of key j of sequence b, or -1 (reported) if the table's entry is
-// outside the pool.  j is below the sequence's key count.
-NVFP4_DEVINL int page_of(const Call &c, int b, int j)
-{
-    const int page = c.table[(int64_t)b * c.table_width + (j >> c.pool.page_shift)];
-    if (page < 0 || page >= c.pool.n_pages) {
-        kv::report_index(c.pool.status, kStatusKvAttention);
-        return -1;
-    }
-    return page;
-}
-
 // Few rows per KV head (attention_decode.cuh), by cache format.
 cudaError_t launch_decode_e4m3(const Call &c, int head_dim, void *workspace, int num_sms, cudaStream_t stream);
 cudaError_t launch_decode_nvfp4(const Call &c, int head_dim, void *workspace, int num_sms, cudaStream_t stream);
