@@ -33,8 +33,10 @@
 // what the f16 weights of other tiles lose (for a row of Q, relative to the largest
 // unit beside its largest weight), so a key that a row does not see must not raise
 // it: in tiles whose keys some rows see and others do not, the unit is that of the
-// largest row that all see, as far as f16 holds the others' codes times up to
-// kAbove; 2^2 (kUnseen) more than that is within the bound.  A call with a tile that
+// largest row that all see (or of the smallest, if all see none), as far as f16 holds
+// the others' codes times up to kAbove.  2^6 (kUnseen) more than that makes the
+// weights' loss 2^-24 per key where it was 2^-28; ordinary V rows need it, where no key of
+// a tile is seen by all (one query head per KV head, NVFP4).  A call with a tile that
 // breaks these rules is done again by the decode kernel, launched behind this one,
 // which keeps every key's exponent by itself; ordinarily that launch ends at
 // once.  (Handling such tiles here, in a loop of their own with each key's exponent
@@ -80,7 +82,7 @@ constexpr int kSharedBytes = 1024;  // barriers and the like (Shared)
 // What an item costs a CTA beside its tiles, in tiles.  (Ragged prefill of four sequences: 61.1 us at 0, 40.8 at 2,
 // 41.2 at 3, 43.7 at 8; 8 trees of 16 tokens 37.8, 35.8, 35.4, 35.4.)
 constexpr int kItemCost = 3;
-constexpr int kBelow = 14, kUnseen = 2;
+constexpr int kBelow = 14, kUnseen = 6;
 constexpr int kNear = 48;  // of V's units, for the softmax sums (attention_decode.cuh)
 constexpr float kHeadroom = 7.f;
 constexpr float kMostWeight = 0x1p15f;  // of the weights of half a tile, in sum

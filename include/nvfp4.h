@@ -433,8 +433,9 @@ int nvfp4_kv_read(const nvfp4_kv_cache *cache, uint16_t *k, int64_t k_ld, uint16
  *   not causal                 every key (cross attention).
  * out = sum_j softmax_j(scale * q . k_j) v_j over the keys it sees, query head
  * h reading KV head h / (n_q_heads / n_kv_heads).  A token that sees no key
- * gets zeros; a query that holds an infinity or a NaN gets NaN; K and V of keys that a token does not see never reach its output,
- * whatever they hold.
+ * gets zeros; a query that holds an infinity or a NaN gets NaN; K and V of keys that a
+ * token does not see never reach its output, whatever they hold (but for the
+ * rounding of its weights, below).
  *
  * Numerics: q . k_j is exact in its products (q scaled by a power of two to
  * f16, K's codes in f16) with fp32 accumulation; softmax statistics are fp32
@@ -446,12 +447,15 @@ int nvfp4_kv_read(const nvfp4_kv_cache *cache, uint16_t *k, int64_t k_ld, uint16
  * For bf16 outputs f16 loses what is below 2^-32 of a row's largest weight:
  * n * 2^-28 * max |V| over the n keys that the token sees (of its KV head) comes
  * on top.  For fp32 outputs the weights keep fp32's range (as two bf16 numbers
- * each).  bf16 calls with more than 24 rows (new tokens times query heads of one KV head)
- * are made for K and V rows whose largest magnitudes lie within about 2^14 of each
- * other among the 128 keys around, and V's between 2^-40 and 2^56; where they do
- * not, the call is made again by the kernel for few rows, within the same bound but
- * in several times the time.  (Rows below 2^-88 count as zero beside larger ones
- * there.)
+ * each).  bf16 calls with more than 24 rows (new tokens times query heads of one KV
+ * head) are made for K and V rows whose largest magnitudes lie within about 2^14 of
+ * each other among the 128 keys around, and V's between 2^-40 and 2^56; where they
+ * do not, the call is made again by the kernel for few rows, within the same bound
+ * but in several times the time.  In them V rows that a token does not see can make
+ * that last term up to n * 2^-24 * max |V|, if they lie among the same 128 keys and
+ * are larger, and rows below 2^-88 count as zero beside larger ones.
+ * Exact products: elements of q within 2^31 of the query's largest (smaller ones
+ * lose bits, below 2^-38 of it all).  Scores have to stay within fp32's range.
  *
  * Requirements: q, out 16-byte aligned; q_ld and out_ld multiples of 8, at
  * least n_q_heads * head_dim; n_q_heads a multiple of n_kv_heads; tree only
@@ -469,8 +473,8 @@ int nvfp4_kv_read(const nvfp4_kv_cache *cache, uint16_t *k, int64_t k_ld, uint16
  *            stream.  Not shared with product calls (their counters lie where
  *            this call has partial results); zero it again after a call that
  *            timed out.  The append and read calls may use its status word.
- * Determinism: a token's result depends on the shapes and lengths of the call,
- * never on timing. */
+ * Determinism: a token's result depends on the shapes and lengths of the call and
+ * on what the cache holds, never on timing. */
 typedef struct {
     nvfp4_kv_cache cache;
     const uint16_t *q;          /* device bf16 bits [total_q][q_ld] */
