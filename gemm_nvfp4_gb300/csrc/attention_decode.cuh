@@ -28,7 +28,7 @@
 // added to the score's logarithm: with z = score + kv (in powers of two) the
 // weight P = 2^(z - M) already carries V's magnitude, its largest values are near
 // 2^7 whatever V's scale is, and f16 holds it to 2^-11; the softmax sum takes
-// P * 2^-kv.  (Where V's exponents leave [-kNear, kNear], a key with most of the
+// P * 2^-kv.  (Where V's exponents leave [-kNear, kNear), a key with most of the
 // softmax and a tiny V could have a P of 0 beside a huge V of little weight: such
 // a warp adds 2^(score - M) to its sum instead, and sums move to another M in two
 // steps, since the factor alone may be 0.)  M trails the running maximum: it moves, and the accumulators are
@@ -56,7 +56,7 @@ constexpr int kStep = 16;      // keys of a warp step
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr float kHeadroom = 7.f, kSlack = 15.f;  // log2 of the largest P after and before a rescale
-constexpr float kNear = 48.f;                    // P is far from 0 for what matters to the sum: 2 * 48 + 30 < 126
+constexpr uint32_t kNear = 32;                   // P is far from 0 for what matters to the sum: 2 * 32 + 30 < 126
 constexpr float kSumUnit = 0x1p-16f, kSumUnitLog2 = -16.f;  // the sum is kept in units of 2^16: P * 2^-kv reaches 2^115
 
 template <int FMT, int D, int NT>
@@ -147,6 +147,11 @@ NVFP4_DEVINL float times_pow2(float s, float d)
     const float half = ex2(0.5f * d);
     return s * half * half;
 }
+
+// An exponent byte less the first one that is near: below 2 kNear, a power of two, if
+// it is, so that one comparison tells it of the bits of two.
+NVFP4_DEVINL uint32_t from_near(uint32_t e) { return e - (127 - kNear); }
+static_assert((kNear & (kNear - 1)) == 0, "one comparison for two bytes");
 
 // Four E4M3 bytes to two f16x2.
 NVFP4_DEVINL void e4m3x4_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
@@ -620,21 +625,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
 
             // exponents of keys g and g + 8
             float z[NT][4], unscale[2];
-            bool over = false;
-            uint32_t v_exp[2];
+            bool over;
             {
                 const uint32_t ea = stage + C::kExpAt + g;
                 // K's mark of a row that is not a number reads infinity here, and its codes are zeros: NaN again
                 const float fk[2] = {__uint_as_float(lds8(ea) << 23), __uint_as_float(lds8(ea + 8) << 23)};
                 const uint32_t ev[2] = {lds8(ea + kStep), lds8(ea + kStep + 8)};
                 float kv[2];
+                over = (from_near(ev[0]) | from_near(ev[1])) >= 2 * kNear;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     // the byte as a float: 2^23 + ev - (2^23 + 127)
                     kv[h] = __uint_as_float(0x4B000000u | ev[h]) - 8388735.f;
                     kv[h] = ev[h] == kv::kNanRow ? NAN : ev[h] == 0 ? -INFINITY : kv[h];
-                    v_exp[h] = ev[h];
-                    over |= fabsf(kv[h]) > kNear && ev[h] != 0;
                     // finite for a NaN row too: masked, its weight of 0 must add 0
                     unscale[h] = __uint_as_float((uint32_t)max(254 - (int)ev[h], 0) << 23) * kSumUnit;
                 }
@@ -667,8 +670,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                     over |= z[n][h] > limit[n][h & 1];
             }
             if (__any_sync(0xFFFFFFFFu, over)) {
-                far |= __any_sync(0xFFFFFFFFu, v_exp[0] - 1 < 126 - (uint32_t)kNear || v_exp[0] > 127 + (uint32_t)kNear ||
-                                                   v_exp[1] - 1 < 126 - (uint32_t)kNear || v_exp[1] > 127 + (uint32_t)kNear);
+                const uint32_t e0 = lds8(stage + C::kExpAt + kStep + g), e1 = lds8(stage + C::kExpAt + kStep + g + 8);
+                far |= __any_sync(0xFFFFFFFFu, (from_near(e0) >= 2 * kNear && e0 != 0) || (from_near(e1) >= 2 * kNear && e1 != 0));
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -691,6 +694,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                     }
                 }
             }
+            if (far) {  // these keys' shares as they are; their weights add nothing below
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // finite, whatever the row
+                    const float kv = __uint_as_float(0x4B000000u | lds8(stage + C::kExpAt + kStep + g + 8 * h)) - 8388735.f;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        sum[n][0] += ex2_subnormal(z[n][2 * h] - (base[n][0] + kv - kSumUnitLog2));
+                        sum[n][1] += ex2_subnormal(z[n][2 * h + 1] - (base[n][1] + kv - kSumUnitLog2));
+                    }
+                    unscale[h] = 0.f;
+                }
+            }
             uint32_t p[NT][WIDE ? 4 : 2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -698,15 +714,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     w[h] = ex2(z[n][h] - base[n][h & 1]);
-                    if (!far)
-                        sum[n][h & 1] = fmaf(w[h], unscale[h >> 1], sum[n][h & 1]);
-                }
-                if (far) {
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        const float kv = __uint_as_float(0x4B000000u | v_exp[h >> 1]) - 8388735.f;  // finite, whatever the row
-                        sum[n][h & 1] += ex2_subnormal(z[n][h] - (base[n][h & 1] + kv - kSumUnitLog2));
-                    }
+                    sum[n][h & 1] = fmaf(w[h], unscale[h >> 1], sum[n][h & 1]);
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
