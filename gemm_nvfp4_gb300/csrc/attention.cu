@@ -14,10 +14,11 @@ namespace {
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Which kernel: by the rows that share a KV head's keys.  At 32 rows the chunk
-// kernel took 33.6 us where the decode kernel took 40.6 (8 sequences of 4000 E4M3
-// keys, 32 and 8 heads), and 40.1 where it took 37.2 (one of 30000); at 24 rows
-// 33.4 against 32.5, and 39.8 against 29.4.  fp32 outputs keep the decode kernel's
-// wide weights.
+// kernel takes 38.4 us where the decode kernel takes 42.3 (8 sequences of 4000 E4M3
+// keys, 32 and 8 heads) and 64.0 where it takes 69.2 (32 of 2000 NVFP4), but 79.8 where
+// it takes 73.1 (32 of 2000 E4M3) and 42.4 where it takes 38.3 (one of 30000); at 24
+// rows 38.2 against 34.7 and 42.3 against 31.3.  fp32 outputs keep the decode
+// kernel's wide weights.
 bool use_chunk(int64_t rows, int out_dtype) { return rows > 24 && out_dtype == NVFP4_OUT_BF16; }
 
 // Sizes alone; what nvfp4_paged_attention_workspace_bytes looks at.

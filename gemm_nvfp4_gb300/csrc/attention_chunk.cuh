@@ -40,8 +40,8 @@
 // breaks these rules is done again by the decode kernel, launched behind this one,
 // which keeps every key's exponent by itself; ordinarily that launch ends at
 // once.  (Handling such tiles here, in a loop of their own with each key's exponent
-// in the softmax, took 5 to 25 % of a long chunk's time even where no tile was one:
-// the roles' loops fill the instruction cache.)  Outputs are bf16 only.
+// in the softmax, took up to 20 % of a long chunk's time even where no tile was one:
+// the roles' loops fill the instruction cache, and the checks alone take 5 %.)  Outputs are bf16 only.
 //
 // A tile's scores are made in two halves of 64 keys, each in columns of its own,
 // which its weights then take: the next half's scores are made while the
@@ -49,12 +49,13 @@
 // score) moves only when the weights of a half sum to more than 2^15, so there is
 // no pass for the maximum.
 //
-// Measured on one GB300: 2048 tokens behind 14336 cached ones (E4M3, 40 and 8 heads
-// of 128, 644 GFLOP) 506 us, 1.27 PFLOP/s, 0.65 of the measured bf16 rate;
-// 2 x 512 tokens in a window of 4096 97 us; 8 trees of 16 tokens over 2016 to
-// 6017 NVFP4 keys 35.4 us; four ragged prefills of up to 1500 tokens (heads of 64,
-// NVFP4) 41 us.  A tile of 256 rows and 128 keys takes 3900 clocks,
-// 3300 of them the softmax warps' own chain; the MMAs alone would take 2600.
+// Measured on one GB300, with the launch behind it (2 to 3 us of each): 2048 tokens
+// behind 14336 cached ones (E4M3, 40 and 8 heads of 128, 644 GFLOP) 546 us, 1.18
+// PFLOP/s, 0.61 of the measured bf16 rate; 2 x 512 tokens in a window of 4096 101 us;
+// 8 trees of 16 tokens over 2016 to 6017 NVFP4 keys 38.7 us; four ragged prefills of
+// up to 1500 tokens (heads of 64, NVFP4) 43.4 us.  A tile of 256 rows and 128 keys takes
+// about 4200 clocks, 3300 of them the softmax warps' own chain; the MMAs alone would
+// take 2600.
 #pragma once
 
 #include <cstdint>
