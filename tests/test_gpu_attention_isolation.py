@@ -173,3 +173,27 @@ def test_sums_over_values_far_apart(fmt, q_len, hq, apart, low, high, weak):
         v *= torch.where(strong, 2.0 ** low, 2.0 ** high)[:, None, None]
         b.put(seq, k.to(torch.bfloat16), v.to(torch.bfloat16))
     run_and_check(b)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("q_len,hq", [(16, 8), (60, 8)])
+def test_captured_calls_that_are_made_again(fmt, q_len, hq):
+    """One captured call, replayed over a cache whose rows lie far apart in some replays and not in others."""
+    b = batch(fmt, q_len, hq, 128, seed=5)
+    k, v = (torch.randn(200, 2, 128, device=DEV, generator=torch.Generator(DEV).manual_seed(s)).to(torch.bfloat16) for s in (6, 7))
+    loud = v.clone()
+    loud[-1] *= 2.0 ** 40
+    out = torch.empty_like(b.q)
+    ws = torch.zeros(g.nvfp4_paged_attention_workspace_bytes(b.cache, b.q, 2, q_len), dtype=torch.uint8, device=DEV)
+    b.run(out=out, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.run(out=out, workspace=ws)
+        b.run(out=out, workspace=ws)
+    for values in (v, loud, loud, v):
+        b.put(0, k, values)
+        want = b.run()
+        graph.replay()
+        assert torch.equal(out, want)
+        assert (ws[:256] == 0).all()
