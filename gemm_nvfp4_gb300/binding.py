@@ -560,35 +560,28 @@ def nvfp4_kv_page_bytes(page_size: int, n_kv_heads: int, head_dim: int, format: 
 # Handle of the current stream without a Stream object around it: these calls
 # take a few microseconds, and making that object is one or two of them.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+@functools.lru_cache(maxsize=1)
+def _one_gpu() -> bool:
+    return torch.cuda.device_count() == 1
 
 
-def _launch(call, where, tensors, *args):
-    """call(*args) with the device of the tensors (those that are not None) current; they must share one."""
-    device = -1
-    for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if d < 0 or (device >= 0 and d != device):
-                raise ValueError(f"{where}: all tensors must be on one CUDA device, got "
-                                 f"{', '.join(str(x.device) for x in tensors if x is not None)}")
-            device = d
-    if device == _current_device():
-        st = call(*args)
-    else:
-        with torch.cuda.device(device):
-            st = call(*args)
-    if st:
-        _check(st, where)
+def _on_device_of(where, *tensors):
+    """Makes the device of the tensors (those that are not None) current; they must share one CUDA device.  (The calls
+    come here only where being CUDA tensors does not settle it: looking at eight devices takes a microsecond.)"""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1 or next(iter(devices)).type != "cuda":
+        raise ValueError(f"{where}: all tensors must be on one CUDA device, got {', '.join(sorted(map(str, devices)))}")
+    return torch.cuda.device(devices.pop())
 
 
 def _stream_of(t: torch.Tensor, stream) -> int:
     """Stream handle: `stream`, or the current one of the device that holds t."""
     if stream is not None:
         return stream.cuda_stream
-    if t.get_device() < 0:
-        return None  # refused before anything is launched
-    return _raw_stream(t.get_device()) if _raw_stream else torch.cuda.current_stream(t.device).cuda_stream
+    device = t.get_device()
+    if device < 0:
+        return None  # not a CUDA tensor: refused before anything is launched
+    return _raw_stream(device) if _raw_stream else torch.cuda.current_stream(t.device).cuda_stream
 
 
 @dataclass
@@ -662,8 +655,16 @@ def nvfp4_kv_append(cache: KVCache, k: torch.Tensor, v: torch.Tensor, slots: tor
         raise ValueError(f"k has {k.shape[0]} tokens, v {v.shape[0]}")
     _check_slots(slots, k.shape[0])
     ws, ws_bytes = _buffer(workspace)
-    _launch(load_library().nvfp4_kv_append, "nvfp4_kv_append", (slots, cache.pool, k, v, workspace), ctypes.byref(c),
-            k.data_ptr(), k_ld, v.data_ptr(), v_ld, slots.data_ptr(), k.shape[0], ws, ws_bytes, _stream_of(slots, stream))
+    args = (ctypes.byref(c), k.data_ptr(), k_ld, v.data_ptr(), v_ld, slots.data_ptr(), k.shape[0], ws, ws_bytes,
+            _stream_of(slots, stream))
+    if (slots.is_cuda and cache.pool.is_cuda and k.is_cuda and v.is_cuda and (workspace is None or workspace.is_cuda)
+            and _one_gpu()):
+        st = load_library().nvfp4_kv_append(*args)
+    else:
+        with _on_device_of("nvfp4_kv_append", slots, cache.pool, k, v, workspace):
+            st = load_library().nvfp4_kv_append(*args)
+    if st:
+        _check(st, "nvfp4_kv_append")
 
 
 def nvfp4_kv_read(cache: KVCache, slots: torch.Tensor, out: tuple[torch.Tensor, torch.Tensor] | None = None,
@@ -680,8 +681,16 @@ def nvfp4_kv_read(cache: KVCache, slots: torch.Tensor, out: tuple[torch.Tensor, 
     _check_slots(slots, k.shape[0])
     _check_slots(slots, v.shape[0])
     ws, ws_bytes = _buffer(workspace)
-    _launch(load_library().nvfp4_kv_read, "nvfp4_kv_read", (slots, cache.pool, k, v, workspace), ctypes.byref(c),
-            k.data_ptr(), k_ld, v.data_ptr(), v_ld, slots.data_ptr(), k.shape[0], ws, ws_bytes, _stream_of(slots, stream))
+    args = (ctypes.byref(c), k.data_ptr(), k_ld, v.data_ptr(), v_ld, slots.data_ptr(), k.shape[0], ws, ws_bytes,
+            _stream_of(slots, stream))
+    if (slots.is_cuda and cache.pool.is_cuda and k.is_cuda and v.is_cuda and (workspace is None or workspace.is_cuda)
+            and _one_gpu()):
+        st = load_library().nvfp4_kv_read(*args)
+    else:
+        with _on_device_of("nvfp4_kv_read", slots, cache.pool, k, v, workspace):
+            st = load_library().nvfp4_kv_read(*args)
+    if st:
+        _check(st, "nvfp4_kv_read")
     return out
 
 
@@ -744,7 +753,13 @@ def nvfp4_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Te
         # zero-filled: the call keeps arrival counters in it
         workspace = _zeroed(stream, lib.nvfp4_paged_attention_workspace_bytes(ctypes.byref(a)), q.device)
     ws, ws_bytes = _buffer(workspace)
-    _launch(lib.nvfp4_paged_attention, "nvfp4_paged_attention",
-            (q, cache.pool, block_table, kv_lens, q_offsets, tree, out, workspace), ctypes.byref(a), ws, ws_bytes,
-            _stream_of(q, stream))
+    args = (ctypes.byref(a), ws, ws_bytes, _stream_of(q, stream))
+    if (q.is_cuda and cache.pool.is_cuda and block_table.is_cuda and kv_lens.is_cuda and out.is_cuda and workspace.is_cuda
+            and (q_offsets is None or q_offsets.is_cuda) and (tree is None or tree.is_cuda) and _one_gpu()):
+        st = lib.nvfp4_paged_attention(*args)
+    else:
+        with _on_device_of("nvfp4_paged_attention", q, cache.pool, block_table, kv_lens, q_offsets, tree, out, workspace):
+            st = lib.nvfp4_paged_attention(*args)
+    if st:
+        _check(st, "nvfp4_paged_attention")
     return out
