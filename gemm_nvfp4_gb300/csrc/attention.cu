@@ -14,10 +14,10 @@ namespace {
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Which kernel: by the rows that share a KV head's keys.  At 32 rows the chunk
-// kernel takes 38.4 us where the decode kernel takes 42.3 (8 sequences of 4000 E4M3
-// keys, 32 and 8 heads) and 64.0 where it takes 69.2 (32 of 2000 NVFP4), but 79.8 where
-// it takes 73.1 (32 of 2000 E4M3) and 42.4 where it takes 38.3 (one of 30000); at 24
-// rows 38.2 against 34.7 and 42.3 against 31.3.  fp32 outputs keep the decode
+// kernel takes 38.0 us where the decode kernel took 42.3 in 32-row items (8 sequences
+// of 4000 E4M3 keys, 32 and 8 heads) and 62.9 where it took 69.2 (32 of 2000 NVFP4), but
+// 74.4 where it took 73.1 (32 of 2000 E4M3) and 45.8 where it took 38.3 (one of 30000);
+// at 24 rows 38.0 against 34.4 and 46.1 against 31.1.  fp32 outputs keep the decode
 // kernel's wide weights.
 bool use_chunk(int64_t rows, int out_dtype) { return rows > 24 && out_dtype == NVFP4_OUT_BF16; }
 
@@ -127,16 +127,10 @@ int nvfp4_paged_attention(const nvfp4_paged_attention_args *args, void *workspac
     if (rc != NVFP4_OK)
         return rc;
     const bool e4m3 = args->cache.format == NVFP4_KV_E4M3;
-    const auto decode = e4m3 ? attn::launch_decode_e4m3 : attn::launch_decode_nvfp4;
-    const auto chunk = e4m3 ? attn::launch_chunk_e4m3 : attn::launch_chunk_nvfp4;
-    c.redo = nullptr;
-    cudaError_t e = cudaSuccess;
-    if (attn::use_chunk((int64_t)c.max_q_len * c.group, args->out_dtype)) {
-        c.redo = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(workspace) + attn::kRedoOffset);
-        e = chunk(c, args->cache.head_dim, workspace, sms, (cudaStream_t)stream);
-    }
-    if (e == cudaSuccess)
-        e = decode(c, args->cache.head_dim, workspace, sms, (cudaStream_t)stream);
+    const auto launch = attn::use_chunk((int64_t)c.max_q_len * c.group, args->out_dtype)
+                            ? (e4m3 ? attn::launch_chunk_e4m3 : attn::launch_chunk_nvfp4)
+                            : (e4m3 ? attn::launch_decode_e4m3 : attn::launch_decode_nvfp4);
+    const cudaError_t e = launch(c, args->cache.head_dim, workspace, sms, (cudaStream_t)stream);
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 

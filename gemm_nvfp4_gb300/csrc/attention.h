@@ -26,10 +26,6 @@ struct Call {
     int32_t item_cost;       // attention_plan.cuh
     int32_t out_bf16, causal;
     float scale_log2;  // scale * log2(e): the softmax works in powers of two
-    // The chunk kernel sets redo[0] if its f16 operands do not hold what the call needs; the decode kernel, launched
-    // behind it, then does the call again.  (redo[1] counts its CTAs; the last one clears both.)  Null: an ordinary call
-    // of the decode kernel.
-    uint32_t *redo;
 };
 
 // One sequence of a call, clamped to what the call's buffers hold.

@@ -36,12 +36,13 @@
 // largest row that all see (or of the smallest, if all see none), as far as f16 holds
 // the others' codes times up to kAbove.  2^6 (kUnseen) more than that makes the
 // weights' loss 2^-24 per key where it was 2^-28; ordinary V rows need it, where no key of
-// a tile is seen by all (one query head per KV head, NVFP4).  A call with a tile that
-// breaks these rules is done again by the decode kernel, launched behind this one,
-// which keeps every key's exponent by itself; ordinarily that launch ends at
-// once.  (Handling such tiles here, in a loop of their own with each key's exponent
-// in the softmax, took up to 20 % of a long chunk's time even where no tile was one:
-// the roles' loops fill the instruction cache, and the checks alone take 5 %.)  Outputs are bf16 only.
+// a tile is seen by all (one query head per KV head, NVFP4).  A tile that
+// breaks these rules is left out (its pages count as not there), and a segment that had
+// one adds such tiles at its end, in fp32 and with each key's exponents apart
+// (far_tiles).  (A loop of its own for them among the softmax warps' tiles took up to
+// 20 % of a long chunk's time even where no tile was one: the roles' loops fill the
+// instruction cache, and the checks alone take 5 %.  A second launch of the few-row kernel, which ended at once
+// where there was none, took 2 to 3 us a call.)  Outputs are bf16 only.
 //
 // A tile's scores are made in two halves of 64 keys, each in columns of its own,
 // which its weights then take: the next half's scores are made while the
@@ -49,13 +50,12 @@
 // score) moves only when the weights of a half sum to more than 2^15, so there is
 // no pass for the maximum.
 //
-// Measured on one GB300, with the launch behind it (2 to 3 us of each): 2048 tokens
-// behind 14336 cached ones (E4M3, 40 and 8 heads of 128, 644 GFLOP) 546 us, 1.18
-// PFLOP/s, 0.61 of the measured bf16 rate; 2 x 512 tokens in a window of 4096 101 us;
-// 8 trees of 16 tokens over 2016 to 6017 NVFP4 keys 38.7 us; four ragged prefills of
-// up to 1500 tokens (heads of 64, NVFP4) 43.4 us.  A tile of 256 rows and 128 keys takes
-// about 4200 clocks, 3300 of them the softmax warps' own chain; the MMAs alone would
-// take 2600.
+// Measured on one GB300: 2048 tokens behind 14336 cached ones (E4M3, 40 and 8 heads
+// of 128, 644 GFLOP) 550 us, 1.17 PFLOP/s, 0.60 of the measured bf16 rate;
+// 2 x 512 tokens in a window of 4096 101 us; 8 trees of 16 tokens over 2016 to
+// 6017 NVFP4 keys 37.9 us; four ragged prefills of up to 1500 tokens (heads of 64,
+// NVFP4) 41.9 us.  A tile of 256 rows and 128 keys takes about 4200 clocks,
+// 3300 of them the softmax warps' own chain; the MMAs alone would take 2600.
 #pragma once
 
 #include <cstdint>
@@ -159,6 +159,7 @@ struct Shared {
     RawInfo raw[2][kMostRaw];
     Segment seg;
     uint32_t tmem, last, tiles;
+    uint32_t far_tile;  // the last tile of the CTA whose rows lie far from its units, counted from 1
     int64_t scratch[kThreads / 32 + 5];
 };
 static_assert(sizeof(Shared) <= kSharedBytes, "barriers");
@@ -172,13 +173,6 @@ NVFP4_DEVINL bool elect_one()
     uint32_t p;
     asm volatile("{ .reg .pred q; .reg .b32 r; elect.sync r|q, 0xFFFFFFFF; selp.u32 %0, 1, 0, q; }" : "=r"(p));
     return p != 0;
-}
-
-NVFP4_DEVINL float ex2(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
 }
 
 NVFP4_DEVINL uint32_t f32x2_to_f16x2(float lo, float hi)
@@ -462,14 +456,21 @@ NVFP4_DEVINL uint32_t range_bytes(int first, int lo, int hi)
 // Exponent byte of V's unit in a tile whose rows see different keys; its largest
 // exponent is `top`.  all: bytes of the keys that every row sees.
 template <int ABOVE>
-NVFP4_DEVINL int mixed_unit(uint32_t four, uint32_t all, int top, bool *redo)
+NVFP4_DEVINL int mixed_unit(uint32_t four, uint32_t all, int top, bool *bad)
 {
     int from = largest_exp(four & all);
     if (from <= 27)  // a row may see any one of the others alone
         from = min(top, (int)__reduce_min_sync(0xFFFFFFFFu, (uint32_t)smallest_of(four)));
     const int unit = max(from, top - ABOVE);
-    *redo |= unit > from + kUnseen;
+    *bad |= unit > from + kUnseen;
     return unit;
+}
+
+// Whether a tile's rows lie too far from its units; bad: so says mixed_unit.
+NVFP4_DEVINL bool is_far(uint32_t k4, uint32_t v4, int k_unit, int v_unit, bool bad)
+{
+    bad |= smallest_of(k4) < k_unit - kBelow || smallest_of(v4) < v_unit - kBelow || (uint32_t)(v_unit - 127 + kNear) > 2u * kNear;
+    return __any_sync(0xFFFFFFFFu, bad);
 }
 
 // A thread converts, in each of its kRowsMine rows of a tile of K or V, one
@@ -562,13 +563,12 @@ NVFP4_DEVINL void clear_nan_codes(uint32_t raw, int run, int tid)
 // the other's arithmetic (the same eight warps doing K, then V, of each tile took
 // 2400 clocks a tile).
 template <int FMT, int D, bool SPLIT>
-NVFP4_DEVINL bool convert_role(uint32_t tiles, int run, uint32_t *redo, Shared *sh, uint32_t smem, int is_v, int tid)
+NVFP4_DEVINL bool convert_role(uint32_t tiles, int run, Shared *sh, uint32_t smem, int is_v, int tid)
 {
     using C = Cfg<FMT, D, SPLIT>;
     using R = kv::Row<FMT, D>;
     constexpr int per = C::kPerBlock, mine = C::kRowsMine;
     const int lane = tid % 32;
-    bool redo_it = false;  // a row of the lane's lies too far from its tile's unit
     const uint32_t slots = is_v ? C::kRawVs : C::kRawKs;
     uint64_t *const full = is_v ? sh->v_full : sh->k_full, *const empty = is_v ? sh->v_empty : sh->k_empty;
     const uint32_t operand = smem + (is_v ? C::kVAt : C::kKAt);
@@ -590,13 +590,14 @@ NVFP4_DEVINL bool convert_role(uint32_t tiles, int run, uint32_t *redo, Shared *
         other &= keep;
         const bool mixed = info.mixed();
         int v_unit = unit_of(largest_exp(other));
+        bool bad = false;
         if (mixed) {
             if (FMT == NVFP4_KV_E4M3 && is_v)
                 clear_nan_codes<FMT, D, SPLIT>(raw, run, tid);
-            v_unit = mixed_unit<C::kAbove>(other, range_bytes(first, info.all_lo, info.all_hi), v_unit, &redo_it);
+            v_unit = mixed_unit<C::kAbove>(other, range_bytes(first, info.all_lo, info.all_hi), v_unit, &bad);
         }
         const int top = is_v ? v_unit : unit_of(largest_exp(own));
-        redo_it |= smallest_of(own) < top - kBelow || (uint32_t)(v_unit - 127 + kNear) > 2u * kNear;
+        const bool far = !is_v && is_far(own, other, top, v_unit, bad);
 #pragma unroll 1
         for (int i0 = 0; i0 < mine; i0 += 2) {
             uint32_t unit[2], rows[2];
@@ -612,7 +613,9 @@ NVFP4_DEVINL bool convert_role(uint32_t tiles, int run, uint32_t *redo, Shared *
             convert<FMT, D, SPLIT>(raw, run, operand + st * C::kOperand, tid, i0, unit, rows);
         }
         if (!is_v && tid == 0)
-            sh->info[tile % kInfos] = {kv::exp2_byte(top), (float)(v_unit - 127), info.present, 0};
+            sh->info[tile % kInfos] = {kv::exp2_byte(top), (float)(v_unit - 127), far ? 0u : info.present, 0};
+        if (far && tid == 0)
+            sh->far_tile = tile + 1;
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -620,8 +623,6 @@ NVFP4_DEVINL bool convert_role(uint32_t tiles, int run, uint32_t *redo, Shared *
             tc::mbar_arrive(&sh->raw_empty[is_v][slot]);
         }
     }
-    if (redo_it)
-        *redo = 1;
     return true;
 }
 
@@ -750,6 +751,151 @@ NVFP4_DEVINL void find_segment(const Call &c, const Range &range, Segment *g)
     g->n = any ? tiles_from(range, it, item_begin, u) : 0;
     g->tile0 = any ? it.tile0 + (int)(u - item_begin - c.item_cost) : 0;
 }
+
+// f32 of 8 elements of a row (from element 8 i on): its codes, times its block scale.
+template <int FMT, int D>
+NVFP4_DEVINL void eight_elements(const uint8_t *blk, int shift, int at, int i, float (&x)[8])
+{
+    using R = kv::Row<FMT, D>;
+    uint32_t h[4];
+    float scale = 1.f;
+    if constexpr (FMT == NVFP4_KV_E4M3) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(blk + at * R::kCode + i * 8);
+        h[0] = e4m3x2_to_f16x2((uint16_t)w.x), h[1] = e4m3x2_to_f16x2((uint16_t)(w.x >> 16));
+        h[2] = e4m3x2_to_f16x2((uint16_t)w.y), h[3] = e4m3x2_to_f16x2((uint16_t)(w.y >> 16));
+    } else {
+        sk::e2m1x8_to_f16x2(*reinterpret_cast<const uint32_t *>(blk + at * R::kCode + i * 4), h);
+        scale = e4m3_to_f32(blk[(R::kCode << shift) + at * R::kScale + i / 2]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float lo, hi;
+        asm("{ .reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b; }" : "=f"(lo), "=f"(hi) : "r"(h[j]));
+        x[2 * j] = lo * scale;
+        x[2 * j + 1] = hi * scale;
+    }
+}
+
+// The far tiles of a segment, which the tensor cores were told are not there: a
+// thread computes its row's scores and weights in fp32, with each key's own
+// exponents, and adds them to the row's accumulators, reference and sum.  About 0.2 ms
+// a tile (of 128 or 256 rows): its aims are to be right and short.
+template <int FMT, int D, bool SPLIT>
+NVFP4_DEVINL void far_tiles(const Call &c, const Segment &g, uint32_t q_at, uint32_t out, int group, int r, int lo, int hi,
+                            bool tree, uint64_t word, float factor, float *top, float *sum)
+{
+    using C = Cfg<FMT, D, SPLIT>;
+    using R = kv::Row<FMT, D>;
+    const int lane = r % 32, shift = c.pool.page_shift, mask = (1 << shift) - 1, past = g.it.seq.past;
+    const int32_t *const table = c.table + (int64_t)g.it.b * c.table_width;
+    const auto block = [&](int key) -> const uint8_t * {  // K's of the key's page, or null
+        const int page = key >= g.it.lo && key < g.it.hi ? table[key >> shift] : -1;
+        return page >= 0 && page < c.pool.n_pages ? kv::block_ptr(c.pool, page, g.it.head, 0) : nullptr;
+    };
+    int all_lo, all_hi;
+    common_keys(c, g.it, &all_lo, &all_hi);
+#pragma unroll 1
+    for (int i = SPLIT ? (int)((g.index ^ group) & 1) : 0; i < g.n; i += SPLIT ? 2 : 1) {
+        const int key0 = (g.tile0 + i) * kTile;
+        {
+            // the conversion's rules again
+            uint32_t k4 = 0, v4 = 0;
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+                const int key = key0 + 4 * lane + j;
+                if (const uint8_t *blk = block(key)) {
+                    const int at = ((R::kCode + R::kScale) << shift) + (key & mask);
+                    k4 |= (uint32_t)blk[at] << 8 * j;
+                    v4 |= (uint32_t)blk[at + c.pool.block_bytes] << 8 * j;
+                }
+            }
+            bool bad = false;
+            int v_unit = unit_of(largest_exp(v4));
+            if (max(key0, g.it.lo) < all_lo || min(key0 + kTile, g.it.hi) > all_hi)
+                v_unit = mixed_unit<C::kAbove>(v4, range_bytes(key0 + 4 * lane, all_lo, all_hi), v_unit, &bad);
+            if (!is_far(k4, v4, unit_of(largest_exp(k4)), v_unit, bad))
+                continue;
+        }
+        float next = *top, base = 0.f, shrink = 1.f, largest = -INFINITY, l = 0.f;
+        float z_of[kTile];  // (in local memory)
+        // first the largest z = score + V's exponent, then 32 elements of the output at a time
+#pragma unroll 1
+        for (int pass = -1; pass < D / 32; ++pass) {
+            float acc[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                acc[j] = 0.f;
+#pragma unroll 1
+            for (int key = key0; key < key0 + kTile; ++key) {
+                const uint8_t *const blk = block(key);
+                if (!blk)
+                    continue;
+                const int at = key & mask, e_at = ((R::kCode + R::kScale) << shift) + at;
+                const uint32_t ve = blk[e_at + c.pool.block_bytes];
+                const float kv = __uint_as_float(0x4B000000u | ve) - 8388735.f;
+                if (pass < 0) {
+                    bool see = key >= lo && key < hi;
+                    if (tree && key >= past)
+                        see &= key - past < 64 && (word >> ((key - past) & 63) & 1);
+                    float score = 0.f;
+#pragma unroll 1
+                    for (int d = 0; d < D / 8; ++d) {
+                        float x[8];
+                        eight_elements<FMT, D>(blk, shift, at, d, x);
+                        const uint4 q = tc::lds128(operand_chunk(q_at, r, d));
+                        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            float a, b;
+                            asm("{ .reg .f16 a, b; mov.b32 {a, b}, %2; cvt.f32.f16 %0, a; cvt.f32.f16 %1, b; }" : "=f"(a), "=f"(b) : "r"(w[j]));
+                            score = fmaf(a, x[2 * j], score);
+                            score = fmaf(b, x[2 * j + 1], score);
+                        }
+                    }
+                    score = score * factor * kv::exp2_byte(blk[e_at]);
+                    const float z = !see ? -INFINITY : ve == kv::kNanRow ? NAN : score + kv;
+                    z_of[key - key0] = z;
+                    largest = fmaxf(largest, z);
+                } else {
+                    const float z = z_of[key - key0], w = ex2(z - base);
+                    if (pass == 0)
+                        l += ex2_subnormal(z - (base + kv + 32.f));  // in units of kSumUnit
+                    if (w != 0.f) {  // (true for a NaN; a zero must not meet what an unseen row holds)
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) {
+                            float x[8];
+                            eight_elements<FMT, D>(blk + c.pool.block_bytes, shift, at, 4 * pass + d, x);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                acc[8 * d + j] = fmaf(w, x[j], acc[8 * d + j]);
+                        }
+                    }
+                }
+            }
+            if (pass < 0) {
+                next = fmaxf(*top, largest - kHeadroom);
+                base = next == -INFINITY ? 0.f : next;
+                shrink = *top == next ? 1.f : ex2(*top - next);
+                continue;
+            }
+            uint32_t x[32];
+            __syncwarp();
+            tc::tmem_ld_32x32b_x32(out + 32 * pass, x);
+            tc::tmem_ld_wait();
+            settle(x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                x[j] = __float_as_uint(fmaf(__uint_as_float(x[j]), shrink, acc[j]));
+            tc::tmem_st_32x32b_x32(out + 32 * pass, x);
+        }
+        if (*top != next)
+            *sum = times_pow2(*sum, *top - next);
+        *sum += l;
+        *top = next;
+    }
+    tc::tmem_st_wait();
+}
+static_assert(kSumUnit == 0x1p-32f, "far_tiles");
 
 // The segment lies in shared memory, not in registers: the loop over the tiles
 // needs those for the scores.
@@ -949,6 +1095,9 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, ui
         if (!ok)
             return false;
         tc::fence_after_sync();
+        if (sh->far_tile > index)
+            far_tiles<FMT, D, SPLIT>(c, g, smem + C::kQAt + (SPLIT ? 0 : group) * C::kOperand, out, group, r, lo, live ? hi : 0,
+                                     c.tree, word, factor, &top, &sum);
 
         // The row's result: with SPLIT, the two groups' joined, each group taking half of the elements.
         constexpr int kCols = SPLIT ? D / 2 : D;
@@ -962,6 +1111,8 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, ui
             // groups without a tile have nothing in tensor memory; 0 * NaN stays NaN in the others
             const float wa = a.x == -INFINITY ? 0.f : ex2(a.x - top), wb = b.x == -INFINITY ? 0.f : ex2(b.x - top);
             sum = fmaf(wa, a.y, wb * b.y);
+            if (fabsf(a.x - b.x) > -kTwoSteps)  // (far tiles' references can lie that far apart)
+                sum = times_pow2(a.y, a.x - top) + times_pow2(b.y, b.x - top);
             w_mine = wa;
             w_other = wb;
         }
@@ -1055,7 +1206,8 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const Range &range, Shared *sh, ui
 #pragma unroll 4
                     for (int i = 0; i < count; ++i) {
                         const float2 ml = stats_of(i);
-                        l = fmaf(ml.x == -INFINITY ? 0.f : ex2(ml.x - m), ml.y, l);
+                        l = ml.x - m < kTwoSteps ? l + times_pow2(ml.y, ml.x - m)
+                                                 : fmaf(ml.x == -INFINITY ? 0.f : ex2(ml.x - m), ml.y, l);
                     }
 #pragma unroll 1
                     for (int q = 0; q < kCols / 32; ++q) {
@@ -1120,6 +1272,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
         sh->seg.item_begin = item_begin;
         sh->seg.u = range.begin;
         sh->seg.index = 0;
+        sh->far_tile = 0;
         find_segment<C::kRows>(c, range, &sh->seg);
         for (int i = 0; i < kStages; ++i) {
             tc::mbar_init(&sh->k_full[i], kConvertWarps / 2);
@@ -1167,7 +1320,7 @@ __global__ void __launch_bounds__(kThreads, 1) chunk_kernel(Call c, uint8_t *wor
     } else if (warp < kSoftmaxWarps + kConvertWarps) {
         give_regs<kConvertRegs>();
         const int ct = tid - 32 * kSoftmaxWarps;
-        ok = convert_role<FMT, D, SPLIT>(tiles, min(1 << c.pool.page_shift, kTile), c.redo, sh, smem, ct / kConvertThreads,
+        ok = convert_role<FMT, D, SPLIT>(tiles, min(1 << c.pool.page_shift, kTile), sh, smem, ct / kConvertThreads,
                                          ct % kConvertThreads);
         code = kTimeoutConvert;
     } else {

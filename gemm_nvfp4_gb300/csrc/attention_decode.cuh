@@ -125,29 +125,6 @@ NVFP4_DEVINL uint32_t f32x2_to_f16x2(float lo, float hi)
     return r;
 }
 
-NVFP4_DEVINL float ex2(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-// 2^x, down to fp32's smallest numbers.
-NVFP4_DEVINL float ex2_subnormal(float x)
-{
-    float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
-// s * 2^d for d <= 0 where 2^d may be too small for a float, but s * 2^d is not.
-constexpr float kTwoSteps = -100.f;
-NVFP4_DEVINL float times_pow2(float s, float d)
-{
-    const float half = ex2(0.5f * d);
-    return s * half * half;
-}
-
 // An exponent byte less the first one that is near: below 2 kNear, a power of two, if
 // it is, so that one comparison tells it of the bits of two.
 NVFP4_DEVINL uint32_t from_near(uint32_t e) { return e - (127 - kNear); }
@@ -444,14 +421,6 @@ NVFP4_DEVINL void for_v_fragments(uint32_t stage, int g, int t, F &&f)
     }
 }
 
-// The end of a CTA.  In a call that is done again, the last one to come here clears
-// the request (every CTA has read it by then).
-NVFP4_DEVINL void leave(const Call &c)
-{
-    if (c.redo && threadIdx.x == 0 && atomicAdd(c.redo + 1, 1u) == gridDim.x - 1)
-        c.redo[0] = c.redo[1] = 0;
-}
-
 template <int FMT, int D, int NT, bool WIDE>
 __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_kernel(Call c, uint8_t *workspace)
 {
@@ -471,15 +440,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
 
     tc::griddep_launch_dependents();
     tc::griddep_wait();
-    if (c.redo && *c.redo == 0)
-        return;
     Range range;
     Item it;
     int64_t item_begin;
-    if (!find_range<C::kRows, kTile, kThreads>(c, scratch, &range, &it, &item_begin)) {
-        leave(c);
+    if (!find_range<C::kRows, kTile, kThreads>(c, scratch, &range, &it, &item_begin))
         return;
-    }
     const uint32_t ring = tc::smem_addr(smem) + warp * C::kStages * C::kStageBytes;
     const int page_mask = (1 << c.pool.page_shift) - 1;
     const LaneCopy copy = lane_copy<FMT, D, NT>(c, lane);
@@ -694,7 +659,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                     }
                 }
             }
-            if (far) {  // these keys' shares as they are; their weights add nothing below
+            if (far) {  // these keys' shares as they are, not from their weights
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     // finite, whatever the row
@@ -704,7 +669,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
                         sum[n][0] += ex2_subnormal(z[n][2 * h] - (base[n][0] + kv - kSumUnitLog2));
                         sum[n][1] += ex2_subnormal(z[n][2 * h + 1] - (base[n][1] + kv - kSumUnitLog2));
                     }
-                    unscale[h] = 0.f;
                 }
             }
             uint32_t p[NT][WIDE ? 4 : 2];
@@ -714,7 +678,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
                     w[h] = ex2(z[n][h] - base[n][h & 1]);
-                    sum[n][h & 1] = fmaf(w[h], unscale[h >> 1], sum[n][h & 1]);
+                    if (!far)
+                        sum[n][h & 1] = fmaf(w[h], unscale[h >> 1], sum[n][h & 1]);
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -881,7 +846,6 @@ __global__ void __launch_bounds__(kThreads, Cfg<FMT, D, NT>::kCtasPerSm) decode_
             __syncthreads();  // the arena and the row tables are free again
         }
     }
-    leave(c);
 }
 
 template <int FMT, int D, int NT, bool WIDE>
@@ -915,10 +879,13 @@ cudaError_t launch_rows(const Call &c, uint8_t *workspace, int num_sms, cudaStre
     // the fewest 8-row tiles that hold a sequence's rows: tiles without rows cost as much as full ones
     const int64_t rows = (int64_t)c.max_q_len * c.group;
     const int block = decode_block(rows);
+    if constexpr (WIDE) {  // (bf16 calls of more than 24 rows go to the chunk kernel)
+        if (block == 32)
+            return launch<FMT, D, 4, WIDE>(c, workspace, num_sms, stream);
+    }
     return block == 8    ? launch<FMT, D, 1, WIDE>(c, workspace, num_sms, stream)
            : block == 16 ? launch<FMT, D, 2, WIDE>(c, workspace, num_sms, stream)
-           : block == 24 ? launch<FMT, D, 3, WIDE>(c, workspace, num_sms, stream)
-                         : launch<FMT, D, 4, WIDE>(c, workspace, num_sms, stream);
+                         : launch<FMT, D, 3, WIDE>(c, workspace, num_sms, stream);
 }
 
 template <int FMT>

@@ -24,10 +24,32 @@
 namespace nvfp4 {
 namespace attn {
 
-// Workspace: the status word and Call::redo (in the first 256 bytes), an arrival counter per
+NVFP4_DEVINL float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 2^x, down to fp32's smallest numbers.
+NVFP4_DEVINL float ex2_subnormal(float x)
+{
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// s * 2^d for d <= 0 where 2^d may be too small for a float, but s * 2^d is not.
+constexpr float kTwoSteps = -100.f;
+NVFP4_DEVINL float times_pow2(float s, float d)
+{
+    const float half = ex2(0.5f * d);
+    return s * half * half;
+}
+
+// Workspace: the status word (in the first 256 bytes), an arrival counter per
 // CTA at byte 256, then two partial slots per CTA.
 constexpr int kMaxCtas = 320;
-constexpr size_t kRedoOffset = kStatusWordOffset + 8;
 constexpr size_t kCounterOffset = 256;
 constexpr size_t kPartialOffset = kCounterOffset + kMaxCtas * sizeof(uint32_t);
 

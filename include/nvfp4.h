@@ -449,9 +449,9 @@ int nvfp4_kv_read(const nvfp4_kv_cache *cache, uint16_t *k, int64_t k_ld, uint16
  * on top.  For fp32 outputs the weights keep fp32's range (as two bf16 numbers
  * each).  bf16 calls with more than 24 rows (new tokens times query heads of one KV
  * head) are made for K and V rows whose largest magnitudes lie within about 2^14 of
- * each other among the 128 keys around, and V's between 2^-40 and 2^56; where they
- * do not, the call is made again by the kernel for few rows, within the same bound
- * but in several times the time.  In them V rows that a token does not see can make
+ * each other among the 128 keys around, and V's between 2^-40 and 2^56; 128 keys where
+ * they do not are computed within the same bound, but take some 0.2 ms for every 128
+ * or 256 rows.  In these calls V rows that a token does not see can make
  * that last term up to n * 2^-24 * max |V|, if they lie among the same 128 keys and
  * are larger, and rows below 2^-88 count as zero beside larger ones.
  * Exact products: elements of q within 2^31 of the query's largest (smaller ones

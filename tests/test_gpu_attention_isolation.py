@@ -136,7 +136,7 @@ def test_keys_far_apart_that_are_seen(fmt, q_len, hq, r, small_k):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("q_len,hq", [(16, 8), (60, 8)])
-def test_calls_that_are_made_again_leave_a_clean_workspace(fmt, q_len, hq):
+def test_calls_with_far_rows_leave_a_clean_workspace(fmt, q_len, hq):
     """One workspace for calls whose rows lie far apart and for ordinary ones, in turn: the same results each time."""
     loud, calm = batch(fmt, q_len, hq, 128, seed=1), batch(fmt, q_len, hq, 128, seed=2)
     k, v = (torch.randn(200, 2, 128, device=DEV, generator=torch.Generator(DEV).manual_seed(s)) for s in (3, 4))
@@ -177,7 +177,7 @@ def test_sums_over_values_far_apart(fmt, q_len, hq, apart, low, high, weak):
 
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("q_len,hq", [(16, 8), (60, 8)])
-def test_captured_calls_that_are_made_again(fmt, q_len, hq):
+def test_captured_calls_with_far_rows(fmt, q_len, hq):
     """One captured call, replayed over a cache whose rows lie far apart in some replays and not in others."""
     b = batch(fmt, q_len, hq, 128, seed=5)
     k, v = (torch.randn(200, 2, 128, device=DEV, generator=torch.Generator(DEV).manual_seed(s)).to(torch.bfloat16) for s in (6, 7))
