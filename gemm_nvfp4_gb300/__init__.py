@@ -19,7 +19,9 @@ from .binding import (NVFP4_ERR_DEVICE_TIMEOUT, NVFP4_OK, NVFP4_STATUS_WORD_OFFS
                       nvfp4_quantize_bf16, nvfp4_selftest_wait_timeout, nvfp4_status_string, nvfp4_version,
                       nvfp4_workspace_bytes, NVFP4_ERR_DEVICE_INDEX, NVFP4_KV_E4M3, NVFP4_KV_NVFP4,
                       NVFP4_OP_KV_APPEND, KVCache, nvfp4_kv_append, nvfp4_kv_page_bytes, nvfp4_kv_read,
-                      nvfp4_paged_attention, nvfp4_paged_attention_workspace_bytes)
+                      nvfp4_paged_attention, nvfp4_paged_attention_workspace_bytes, RopeTable, nvfp4_rope,
+                      nvfp4_rope_pairs, nvfp4_prompt_attention, nvfp4_gemm_epilogue, nvfp4_fp6_gemm_epilogue,
+                      NVFP4_ACT_GELU, NVFP4_ACT_GELU_TANH, NVFP4_ACT_NONE, NVFP4_ACT_RELU, NVFP4_ACT_RELU2, NVFP4_ACT_SILU)
 
 __all__ = [
     "NVFP4Error", "NVFP4Weight", "FP6Weight",
@@ -36,4 +38,7 @@ __all__ = [
     "KVCache", "nvfp4_kv_page_bytes", "nvfp4_kv_append", "nvfp4_kv_read", "nvfp4_paged_attention",
     "nvfp4_paged_attention_workspace_bytes", "NVFP4_KV_E4M3", "NVFP4_KV_NVFP4", "NVFP4_OP_KV_APPEND",
     "NVFP4_ERR_DEVICE_INDEX",
+    "RopeTable", "nvfp4_rope", "nvfp4_rope_pairs", "nvfp4_prompt_attention",
+    "nvfp4_gemm_epilogue", "nvfp4_fp6_gemm_epilogue", "NVFP4_ACT_NONE", "NVFP4_ACT_SILU", "NVFP4_ACT_GELU",
+    "NVFP4_ACT_GELU_TANH", "NVFP4_ACT_RELU", "NVFP4_ACT_RELU2",
 ]

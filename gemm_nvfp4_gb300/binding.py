@@ -39,6 +39,13 @@ NVFP4_OP_KV_APPEND = 6
 NVFP4_OUT_F32 = 0
 NVFP4_OUT_BF16 = 1
 
+NVFP4_ACT_NONE = 0
+NVFP4_ACT_SILU = 1
+NVFP4_ACT_GELU = 2
+NVFP4_ACT_GELU_TANH = 3
+NVFP4_ACT_RELU = 4
+NVFP4_ACT_RELU2 = 5
+
 NVFP4_KV_E4M3 = 0
 NVFP4_KV_NVFP4 = 1
 
@@ -68,6 +75,39 @@ class PagedAttentionArgsC(ctypes.Structure):
                 ("n_seqs", ctypes.c_int64), ("total_q", ctypes.c_int64), ("max_q_len", ctypes.c_int64),
                 ("window", ctypes.c_int64), ("n_q_heads", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
                 ("causal", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class RopePairC(ctypes.Structure):
+    """nvfp4_rope_pair of include/nvfp4.h."""
+    _fields_ = [("turn", ctypes.c_uint64), ("axis", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class RopeArgsC(ctypes.Structure):
+    """nvfp4_rope_args of include/nvfp4.h."""
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("q_ld", ctypes.c_int64), ("k_ld", ctypes.c_int64),
+                ("q_out", ctypes.c_void_p), ("k_out", ctypes.c_void_p), ("q_out_ld", ctypes.c_int64),
+                ("k_out_ld", ctypes.c_int64), ("positions", ctypes.c_void_p), ("positions_ld", ctypes.c_int64),
+                ("pairs", ctypes.c_void_p), ("n_tokens", ctypes.c_int64), ("n_axes", ctypes.c_int32),
+                ("n_pairs", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("n_k_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("adjacent", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class EpilogueC(ctypes.Structure):
+    """nvfp4_epilogue of include/nvfp4.h."""
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("residual_ld", ctypes.c_int64),
+                ("bias_dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32), ("activation", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class PromptAttentionArgsC(ctypes.Structure):
+    """nvfp4_prompt_attention_args of include/nvfp4.h."""
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_ld", ctypes.c_int64),
+                ("k_ld", ctypes.c_int64), ("v_ld", ctypes.c_int64), ("out", ctypes.c_void_p), ("out_ld", ctypes.c_int64),
+                ("offsets", ctypes.c_void_p), ("n_seqs", ctypes.c_int64), ("total", ctypes.c_int64),
+                ("window", ctypes.c_int64), ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 class NVFP4Error(RuntimeError):
@@ -145,6 +185,18 @@ def load_library():
         lib.nvfp4_paged_attention_workspace_bytes.argtypes = [args_p]
         lib.nvfp4_paged_attention.restype = i32
         lib.nvfp4_paged_attention.argtypes = [args_p, P, sz, P]
+        ep_p = ctypes.POINTER(EpilogueC)
+        lib.nvfp4_gemm_epilogue.restype = i32
+        lib.nvfp4_gemm_epilogue.argtypes = [P, i64, P, P, P, i64, i64, ep_p, P, i32, P, sz, P]
+        lib.nvfp4_fp6_gemm_epilogue.restype = i32
+        lib.nvfp4_fp6_gemm_epilogue.argtypes = [P, i64, P, P, i64, i64, ep_p, P, i32, P, sz, P]
+        lib.nvfp4_rope_pairs.restype = i32
+        lib.nvfp4_rope_pairs.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int32), ctypes.c_int32,
+                                         P]
+        lib.nvfp4_rope.restype = i32
+        lib.nvfp4_rope.argtypes = [ctypes.POINTER(RopeArgsC), P]
+        lib.nvfp4_prompt_attention.restype = i32
+        lib.nvfp4_prompt_attention.argtypes = [ctypes.POINTER(PromptAttentionArgsC), P, sz, P]
         lib.nvfp4_device_status.restype = i32
         lib.nvfp4_device_status.argtypes = [P, sz, i32, ctypes.POINTER(ctypes.c_uint32), P]
         lib.nvfp4_selftest_wait_timeout.restype = i32
@@ -762,4 +814,203 @@ def nvfp4_paged_attention(q: torch.Tensor, cache: KVCache, block_table: torch.Te
             st = lib.nvfp4_paged_attention(*args)
     if st:
         _check(st, "nvfp4_paged_attention")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Products with an epilogue
+# ---------------------------------------------------------------------------
+
+def _product_epilogue(where, call, op, x, M, K, weight, bias, activation, residual, out_dtype, out, workspace, stream):
+    if x.dtype != torch.bfloat16 or x.dim() != 2 or x.shape[1] != K or not x.is_contiguous():
+        raise ValueError(f"x must be a contiguous bf16 [tokens, {K}], got {x.dtype} {list(x.shape)}")
+    N = x.shape[0]
+    if bias is not None and (bias.shape != (M,) or not bias.is_contiguous()):
+        raise ValueError(f"bias must be a contiguous [{M}], got {list(bias.shape)}")
+    if residual is not None and (residual.shape != (N, M) or (M > 1 and residual.stride(1) != 1)):
+        raise ValueError(f"residual must be [{N}, {M}] with unit stride along its rows, got {list(residual.shape)}")
+    if out is None:
+        out = _new(stream, N, M, dtype=out_dtype, device=x.device)
+    if out.shape != (N, M) or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous [{N}, {M}], got {list(out.shape)}")
+    e = EpilogueC(None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(),
+                  0 if residual is None else (residual.stride(0) if N > 1 else M),
+                  0 if bias is None else _out_code(bias.dtype), 0 if residual is None else _out_code(residual.dtype),
+                  activation, 0)
+    if workspace is None:
+        # zero-filled: the calls with few tokens keep split-K counters in it
+        workspace = _zeroed(stream, max(16, nvfp4_workspace_bytes(op, N, M, K)), x.device)
+    ws, ws_bytes = _buffer(workspace)
+    args = (x.data_ptr(), N, *(t.data_ptr() for t in weight), M, K, ctypes.byref(e), out.data_ptr(), _out_code(out.dtype),
+            ws, ws_bytes, _stream_of(x, stream))
+    if (x.is_cuda and out.is_cuda and workspace.is_cuda and all(t.is_cuda for t in weight)
+            and (bias is None or bias.is_cuda) and (residual is None or residual.is_cuda) and _one_gpu()):
+        st = call(*args)
+    else:
+        with _on_device_of(where, x, *weight, bias, residual, out, workspace):
+            st = call(*args)
+    if st:
+        _check(st, where)
+    return out
+
+
+def nvfp4_gemm_epilogue(x: torch.Tensor, W: NVFP4Weight, bias: torch.Tensor | None = None,
+                        activation: int = NVFP4_ACT_NONE, residual: torch.Tensor | None = None, out_dtype=torch.float32,
+                        out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                        stream=None) -> torch.Tensor:
+    """y[N, M] = residual + act(x[N, K] (bf16) . dequant(W)^T + bias), any N >= 1; bias [M] and residual [N, M] (rows may
+    be strided) bf16 or fp32; `out` may be the residual itself."""
+    return _product_epilogue("nvfp4_gemm_epilogue", load_library().nvfp4_gemm_epilogue, NVFP4_OP_GEMM_PREFILL, x, W.M, W.K,
+                             (W.codes, W.scales, W.tensor_scale), bias, activation, residual, out_dtype, out, workspace, stream)
+
+
+def nvfp4_fp6_gemm_epilogue(x: torch.Tensor, W: FP6Weight, bias: torch.Tensor | None = None,
+                            activation: int = NVFP4_ACT_NONE, residual: torch.Tensor | None = None,
+                            out_dtype=torch.float32, out: torch.Tensor | None = None,
+                            workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """nvfp4_gemm_epilogue for FP6 weights."""
+    return _product_epilogue("nvfp4_fp6_gemm_epilogue", load_library().nvfp4_fp6_gemm_epilogue, NVFP4_OP_FP6_GEMM, x, W.M,
+                             W.K, (W.codes, W.scales), bias, activation, residual, out_dtype, out, workspace, stream)
+
+
+# ---------------------------------------------------------------------------
+# Rotary positions
+# ---------------------------------------------------------------------------
+
+def nvfp4_rope_pairs(inv_freq, axis=None) -> torch.Tensor:
+    """Table entries (a CPU uint8 [n_pairs, 16]) for frequencies in radians per position (a sequence or a 1-D tensor,
+    taken as fp64) and each pair's axis (all 0 without)."""
+    freq = [float(f) for f in inv_freq]
+    n = len(freq)
+    if axis is not None and len(axis) != n:
+        raise ValueError(f"{n} frequencies, {len(axis)} axes")
+    pairs = torch.zeros(n, 16, dtype=torch.uint8)
+    axes = None if axis is None else (ctypes.c_int32 * n)(*(int(a) for a in axis))
+    st = load_library().nvfp4_rope_pairs((ctypes.c_double * n)(*freq), axes, n, pairs.data_ptr())
+    _check(st, "nvfp4_rope_pairs")
+    return pairs
+
+
+@dataclass
+class RopeTable:
+    """Each pair's frequency and axis in device memory (include/nvfp4.h), made once for a model."""
+    pairs: torch.Tensor  # uint8 [n_pairs, 16]
+    n_axes: int          # axes that the pairs use: positions need as many rows
+
+    @classmethod
+    def make(cls, inv_freq, axis=None, device="cuda") -> "RopeTable":
+        """inv_freq: radians per position of each pair, e.g. base ** (-2 * i / rotary_dim); axis: each pair's row of the
+        positions (all 0 without)."""
+        pairs = nvfp4_rope_pairs(inv_freq, axis)
+        return cls(pairs.to(device), 1 + (max((int(a) for a in axis), default=0) if axis is not None else 0))
+
+    @property
+    def n_pairs(self) -> int:
+        return self.pairs.shape[0]
+
+
+def nvfp4_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table: RopeTable,
+               adjacent: bool = False, inverse: bool = False, scale: float = 1.0,
+               out: tuple[torch.Tensor, torch.Tensor | None] | None = None,
+               stream=None) -> tuple[torch.Tensor, torch.Tensor | None]:
+    """(q, k) turned by their tokens' positions.
+
+    q [tokens, n_q_heads, head_dim] and k [tokens, n_k_heads, head_dim] (or None), both bf16 or fp32, token rows may be
+    strided; positions int64 [tokens], or [axes, tokens] for a table with several axes.  out: two tensors of the
+    inputs' shapes and type, which may be the inputs themselves (in place)."""
+    if q.dim() != 3:
+        raise ValueError(f"q must be [tokens, heads, head_dim], got {list(q.shape)}")
+    tokens, heads, head_dim = q.shape
+    dtype = (q.dtype,)
+    code = _out_code(q.dtype)
+    k_heads = 0
+    if k is not None:
+        if k.dim() != 3:
+            raise ValueError(f"k must be [tokens, heads, head_dim], got {list(k.shape)}")
+        k_heads = k.shape[1]
+    if out is None:
+        out = (_new(stream, tokens, heads, head_dim, dtype=q.dtype, device=q.device),
+               None if k is None else _new(stream, tokens, k_heads, head_dim, dtype=q.dtype, device=q.device))
+    q_out, k_out = out
+    if (k is None) != (k_out is None):
+        raise ValueError("out must hold a tensor for k if and only if k is given")
+    q_ld, q_out_ld = _head_rows(q, heads, head_dim, dtype, "q"), _head_rows(q_out, heads, head_dim, dtype, "out[0]")
+    k_ld = k_out_ld = 0
+    if k is not None:
+        k_ld, k_out_ld = _head_rows(k, k_heads, head_dim, dtype, "k"), _head_rows(k_out, k_heads, head_dim, dtype, "out[1]")
+        if k.shape[0] != tokens or k_out.shape[0] != tokens:
+            raise ValueError(f"q has {tokens} tokens, k {k.shape[0]}, out[1] {k_out.shape[0]}")
+    if q_out.shape[0] != tokens:
+        raise ValueError(f"q has {tokens} tokens, out[0] {q_out.shape[0]}")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if positions.dtype != torch.int64 or positions.dim() not in (1, 2) or positions.shape[-1] != tokens or (
+            tokens > 1 and positions.stride(-1) != 1):
+        raise ValueError(f"positions must be int64 [{tokens}] or [axes, {tokens}] with unit stride along the tokens, got "
+                         f"{positions.dtype} {list(positions.shape)}")
+    if axes < table.n_axes:
+        raise ValueError(f"the table uses {table.n_axes} axes, positions have {axes}")
+    pairs = table.pairs
+    if pairs.dtype != torch.uint8 or pairs.dim() != 2 or pairs.shape[1] != 16 or not pairs.is_contiguous():
+        raise ValueError(f"the table's pairs must be a contiguous uint8 [n_pairs, 16], got {pairs.dtype} {list(pairs.shape)}")
+    a = RopeArgsC(q.data_ptr(), None if k is None else k.data_ptr(), q_ld, k_ld, q_out.data_ptr(),
+                  None if k is None else k_out.data_ptr(), q_out_ld, k_out_ld, positions.data_ptr(),
+                  positions.stride(0) if axes > 1 else tokens, pairs.data_ptr(), tokens, axes, pairs.shape[0], heads, k_heads,
+                  head_dim, code, 1 if adjacent else 0, 1 if inverse else 0, scale, 0)
+    args = (ctypes.byref(a), _stream_of(q, stream))
+    if (q.is_cuda and q_out.is_cuda and positions.is_cuda and pairs.is_cuda and (k is None or (k.is_cuda and k_out.is_cuda))
+            and _one_gpu()):
+        st = load_library().nvfp4_rope(*args)
+    else:
+        with _on_device_of("nvfp4_rope", q, q_out, k, k_out, positions, pairs):
+            st = load_library().nvfp4_rope(*args)
+    if st:
+        _check(st, "nvfp4_rope")
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Attention over whole prompts
+# ---------------------------------------------------------------------------
+
+def nvfp4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, offsets: torch.Tensor | None = None,
+                           scale: float | None = None, causal: bool = True, window: int = 0, out_dtype=torch.bfloat16,
+                           out: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                           stream=None) -> torch.Tensor:
+    """Attention of packed prompts over their own K and V.
+
+    q bf16 [tokens, n_q_heads, head_dim], k and v bf16 [tokens, n_kv_heads, head_dim] (token rows may be strided, as
+    column ranges of a QKV output are); offsets int32 [n_seqs + 1]: where each sequence begins and the last one ends
+    (None: one sequence).  scale defaults to head_dim ** -0.5.  Rows of `out` that belong to no sequence are left as
+    they are."""
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError(f"q and k must be [tokens, heads, head_dim], got {list(q.shape)} and {list(k.shape)}")
+    total, heads, head_dim = q.shape
+    kv_heads = k.shape[1]
+    q_ld = _head_rows(q, heads, head_dim, _BF16, "q")
+    k_ld = _head_rows(k, kv_heads, head_dim, _BF16, "k")
+    v_ld = _head_rows(v, kv_heads, head_dim, _BF16, "v")
+    if out is None:
+        out = _new(stream, total, heads, head_dim, dtype=out_dtype, device=q.device)
+    out_ld = _head_rows(out, heads, head_dim, (torch.bfloat16, torch.float32), "out")
+    if k.shape[0] != total or v.shape[0] != total or out.shape[0] != total:
+        raise ValueError(f"q has {total} tokens, k {k.shape[0]}, v {v.shape[0]}, out {out.shape[0]}")
+    n_seqs = 1
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.shape[0] < 1:
+            raise ValueError(f"offsets must be [n_seqs + 1], got {list(offsets.shape)}")
+        n_seqs = offsets.shape[0] - 1
+    a = PromptAttentionArgsC(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_ld, k_ld, v_ld, out.data_ptr(), out_ld,
+        None if offsets is None else _device_ints(offsets, torch.int32, (n_seqs + 1,), "offsets"), n_seqs, total, window,
+        heads, kv_heads, head_dim, _out_code(out.dtype), 1 if causal else 0, head_dim ** -0.5 if scale is None else scale)
+    ws, ws_bytes = _buffer(workspace)
+    args = (ctypes.byref(a), ws, ws_bytes, _stream_of(q, stream))
+    if (q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda and (offsets is None or offsets.is_cuda)
+            and (workspace is None or workspace.is_cuda) and _one_gpu()):
+        st = load_library().nvfp4_prompt_attention(*args)
+    else:
+        with _on_device_of("nvfp4_prompt_attention", q, k, v, out, offsets, workspace):
+            st = load_library().nvfp4_prompt_attention(*args)
+    if st:
+        _check(st, "nvfp4_prompt_attention")
     return out

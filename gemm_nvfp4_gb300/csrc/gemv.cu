@@ -33,6 +33,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "epilogue.cuh"
 #include "kernels.h"
 
 namespace nvfp4 {
@@ -54,6 +55,7 @@ struct GemvArgs {
     float *partial;   // [P][2 slots][NW][16 rows][16 tokens]
     int64_t tiles, chunks, total;
     int P;
+    Epilogue ep;      // EPI: what is done with the sums
 };
 
 template <int NW>
@@ -278,12 +280,16 @@ NVFP4_DEVINL float silu_mul(float g, float u)
     return __fdiv_rn(g, 1.0f + expf(-g)) * u;
 }
 
-NVFP4_DEVINL void store_out(void *y, int out_bf16, int64_t idx, float v)
+template <bool EPI>
+NVFP4_DEVINL void store_out(const GemvArgs &a, int tok, int64_t m, float v)
 {
-    if (out_bf16)
-        reinterpret_cast<uint16_t *>(y)[idx] = f32_to_bf16(v);
+    const int64_t idx = (int64_t)tok * a.M + m;
+    if constexpr (EPI)
+        v = epilogue_value(a.ep, v, tok, m);
+    if (a.out_bf16)
+        reinterpret_cast<uint16_t *>(a.y)[idx] = f32_to_bf16(v);
     else
-        reinterpret_cast<float *>(y)[idx] = v;
+        reinterpret_cast<float *>(a.y)[idx] = v;
 }
 
 // FMT 0: NVFP4 (accumulators hold sum * 2^-8, times the tensor scale);
@@ -300,7 +306,7 @@ NVFP4_DEVINL float finish(const float (&v)[NW], const float (&ts)[NW])
     return silu_mul(g, u);
 }
 
-template <int NW, int NT, bool ALIGNED, int FMT>
+template <int NW, int NT, bool ALIGNED, int FMT, bool EPI>
 __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(GemvArgs a)
 {
     using Ch = typename std::conditional<FMT == 0, Chunk<NW>, Chunk6<NW>>::type;
@@ -397,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemv_kernel(GemvArgs a)
             }
             if (c0 == 0 && c1 == a.chunks) {
                 if (tok < a.N && m < a.M)
-                    store_out(a.y, a.out_bf16, (int64_t)tok * a.M + m, finish<NW, FMT>(v, ts));
+                    store_out<EPI>(a, tok, m, finish<NW, FMT>(v, ts));
             } else {
                 const int slot = (tile == first_tile) ? 0 : 1;
 #pragma unroll
@@ -418,7 +424,7 @@ NVFP4_DEVINL int cta_of(int64_t q, int64_t total, int P)
 // One block per CTA boundary: the tile holding boundary lo_b (if it lies
 // strictly inside a tile and is that tile's first inner boundary) is summed
 // over the CTAs that touch it, in CTA order.
-template <int NW, int FMT>
+template <int NW, int FMT, bool EPI>
 __global__ void __launch_bounds__(256) gemv_fixup_kernel(GemvArgs a)
 {
     const int b = blockIdx.x + 1;
@@ -452,15 +458,15 @@ __global__ void __launch_bounds__(256) gemv_fixup_kernel(GemvArgs a)
         }
     }
     if (tok < a.N && m < a.M)
-        store_out(a.y, a.out_bf16, (int64_t)tok * a.M + m, finish<NW, FMT>(v, ts));
+        store_out<EPI>(a, tok, m, finish<NW, FMT>(v, ts));
 }
 
-template <int NW, int NT, bool ALIGNED, int FMT = 0>
+template <int NW, int NT, bool ALIGNED, int FMT = 0, bool EPI = false>
 static cudaError_t launch_t(const GemvArgs &a, cudaStream_t stream)
 {
-    gemv_kernel<NW, NT, ALIGNED, FMT><<<a.P, kThreads, 0, stream>>>(a);
+    gemv_kernel<NW, NT, ALIGNED, FMT, EPI><<<a.P, kThreads, 0, stream>>>(a);
     if (a.P > 1)
-        gemv_fixup_kernel<NW, FMT><<<a.P - 1, 256, 0, stream>>>(a);
+        gemv_fixup_kernel<NW, FMT, EPI><<<a.P - 1, 256, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -481,7 +487,7 @@ int64_t gemv_grid(int64_t M, int64_t K, int num_sms)
 
 cudaError_t launch_gemv(const uint16_t *x, int N, int64_t M, int64_t K, const uint8_t *const *codes,
                         const uint8_t *const *scales, const float *const *ts, int n_weights, void *y,
-                        int out_bf16, void *workspace, int num_sms, cudaStream_t stream)
+                        int out_bf16, void *workspace, int num_sms, cudaStream_t stream, const Epilogue *epilogue)
 {
     GemvArgs a{};
     a.x = x;
@@ -504,8 +510,15 @@ cudaError_t launch_gemv(const uint16_t *x, int N, int64_t M, int64_t K, const ui
     if (a.total == 0)
         return cudaSuccess;
     if (skinny_tc_supported(M, K))
-        return launch_skinny_tc(x, N, M, K, codes, scales, ts, n_weights, y, out_bf16, workspace, num_sms, stream);
+        return launch_skinny_tc(x, N, M, K, codes, scales, ts, n_weights, y, out_bf16, workspace, num_sms, stream,
+                                epilogue);
     const bool aligned = (K % 32) == 0;
+    if (epilogue && n_weights == 1) {
+        a.ep = *epilogue;
+        if (N <= 8)
+            return aligned ? launch_t<1, 1, true, 0, true>(a, stream) : launch_t<1, 1, false, 0, true>(a, stream);
+        return aligned ? launch_t<1, 2, true, 0, true>(a, stream) : launch_t<1, 2, false, 0, true>(a, stream);
+    }
     if (n_weights == 1) {
         if (N <= 8)
             return aligned ? launch_t<1, 1, true>(a, stream) : launch_t<1, 1, false>(a, stream);
@@ -523,7 +536,7 @@ size_t gemv_mma_workspace_bytes(int n_weights)
 
 cudaError_t launch_gemv_fp6(const uint16_t *x, int N, int64_t M, int64_t K, const uint8_t *const *codes,
                             const uint8_t *const *scales, int n_weights, void *y, int out_bf16, void *workspace,
-                            int num_sms, cudaStream_t stream)
+                            int num_sms, cudaStream_t stream, const Epilogue *epilogue)
 {
     GemvArgs a{};
     a.x = x;
@@ -545,6 +558,10 @@ cudaError_t launch_gemv_fp6(const uint16_t *x, int N, int64_t M, int64_t K, cons
     a.P = (int)gemv_grid(M, K, num_sms);
     if (a.total == 0)
         return cudaSuccess;
+    if (epilogue && n_weights == 1) {
+        a.ep = *epilogue;
+        return N <= 8 ? launch_t<1, 1, true, 1, true>(a, stream) : launch_t<1, 2, true, 1, true>(a, stream);
+    }
     if (n_weights == 1)
         return N <= 8 ? launch_t<1, 1, true, 1>(a, stream) : launch_t<1, 2, true, 1>(a, stream);
     return N <= 8 ? launch_t<2, 1, true, 1>(a, stream) : launch_t<2, 2, true, 1>(a, stream);

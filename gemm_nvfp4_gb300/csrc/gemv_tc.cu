@@ -55,6 +55,7 @@
 #include <algorithm>
 #include <mutex>
 
+#include "epilogue.cuh"
 #include "common.cuh"
 #include "kernels.h"
 #include "skinny.cuh"
@@ -150,6 +151,7 @@ struct Args {
     int cs;         // > 1: cluster-K (clusters of cs CTAs split every tile's K); 1: stream-K
     int ncl;        // cluster-K: number of clusters
     const uint8_t *scales6[2];  // FP6: UE8M0 scales [M][K/128] (read by the dequantisers)
+    Epilogue ep;    // EPI: what is done with the sums
 };
 
 // Workspace layout (bytes): header 256 (factor[16], flags[16], err), per-tile
@@ -353,10 +355,12 @@ __global__ void __launch_bounds__(kPrepThreads) skinny_prep_kernel(const uint16_
 // ---------------------------------------------------------------------------
 
 // Output value of row m, token n from the fp32 sums of the matrices.
-template <int NW>
+template <int NW, bool EPI>
 NVFP4_DEVINL void store_out(const Args &a, const float *fac, int n, int64_t m, float s0, float s1)
 {
-    const float val = NW == 1 ? s0 * fac[n] : silu_mul(s0 * fac[n], s1 * fac[NTOK + n]);
+    float val = NW == 1 ? s0 * fac[n] : silu_mul(s0 * fac[n], s1 * fac[NTOK + n]);
+    if constexpr (EPI)
+        val = epilogue_value(a.ep, val, n, m);
     const int64_t idx = (int64_t)n * a.M + m;
     if (a.out_bf16)
         reinterpret_cast<uint16_t *>(a.y)[idx] = f32_to_bf16(val);
@@ -377,7 +381,7 @@ struct SegInfo {
 // after a barrier of the epilogue threads (the barrier orders every thread's
 // partial stores before the release).  Returns in `si` whether this CTA
 // arrived last and must add the tile's partials (reduce_tile).
-template <int NW>
+template <int NW, bool EPI>
 __device__ __noinline__ void publish_segment(const Args &a, const float *fac, const float (&v)[NW][16], int tile,
                                              bool whole, int first_tile, int b, int r, SegInfo *si)
 {
@@ -388,7 +392,7 @@ __device__ __noinline__ void publish_segment(const Args &a, const float *fac, co
 #pragma unroll
             for (int n = 0; n < NTOK; ++n)
                 if (n < a.N)
-                    store_out<NW>(a, fac, n, m, v[0][n], v[NW - 1][n]);
+                    store_out<NW, EPI>(a, fac, n, m, v[0][n], v[NW - 1][n]);
         if (r == 0)
             si->reduce = 0;
         return;
@@ -422,7 +426,7 @@ __device__ __noinline__ void publish_segment(const Args &a, const float *fac, co
 // order (deterministic) and write the outputs.  Threads t = 0..nthr-1 share
 // the work: pair p = (token n, rows 4q..4q+3) for p = t, t + nthr, ...; each
 // pair's partials are read with 16-byte loads, kBatch CTAs in flight.
-template <int NW>
+template <int NW, bool EPI>
 __device__ __noinline__ void reduce_tile(const Args &a, const float *fac, const SegInfo si, int t, int nthr)
 {
     constexpr int kBatch = 4;
@@ -463,7 +467,7 @@ __device__ __noinline__ void reduce_tile(const Args &a, const float *fac, const 
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (m0 + e < a.M)
-                store_out<NW>(a, fac, n, m0 + e, g[e], h[e]);
+                store_out<NW, EPI>(a, fac, n, m0 + e, g[e], h[e]);
     }
 }
 
@@ -474,7 +478,7 @@ __device__ __noinline__ void reduce_tile(const Args &a, const float *fac, const 
 // the partials of ranks 0, 1, ... in that order through distributed shared
 // memory, writes the outputs and then frees every rank's buffer.  A rank
 // waits for that before reusing the buffer (and before exiting).
-template <int NW>
+template <int NW, bool EPI>
 __device__ __noinline__ void ck_epilogue(const Args &a, const float *fac, const float (&v)[NW][16], int64_t tile,
                                          int r, int et, int seg, float *buf, uint64_t *ck_full, uint64_t *ck_free)
 {
@@ -524,15 +528,8 @@ __device__ __noinline__ void ck_epilogue(const Args &a, const float *fac, const 
     if (m < a.M)
 #pragma unroll
         for (int n = 0; n < NTOK; ++n)
-            if (n < a.N) {
-                const float val = NW == 1 ? acc[0][n] * fac[n]
-                                          : silu_mul(acc[0][n] * fac[n], acc[NW - 1][n] * fac[NTOK + n]);
-                const int64_t idx = (int64_t)n * a.M + m;
-                if (a.out_bf16)
-                    reinterpret_cast<uint16_t *>(a.y)[idx] = f32_to_bf16(val);
-                else
-                    reinterpret_cast<float *>(a.y)[idx] = val;
-            }
+            if (n < a.N)
+                store_out<NW, EPI>(a, fac, n, m, acc[0][n], acc[NW - 1][n]);
     tc::named_bar_sync(1, kEpiThreads);  // every read of the ranks' buffers is done
     if (et < a.cs)
         tc::mbar_arrive_remote(tc::mapa(ck_free, (uint32_t)et));
@@ -624,7 +621,7 @@ NVFP4_DEVINL void mma_issuer(const Args &a, const IssuerArgs &p, int q)
     }
 }
 
-template <int NW, int FMT = 0>
+template <int NW, int FMT = 0, bool EPI = false>
 __global__ void __launch_bounds__(kThreads, 1)
 skinny_tc_kernel(const __grid_constant__ CUtensorMap m_codes0, const __grid_constant__ CUtensorMap m_codes1,
                  const __grid_constant__ CUtensorMap m_scales0, const __grid_constant__ CUtensorMap m_scales1,
@@ -863,7 +860,7 @@ skinny_tc_kernel(const __grid_constant__ CUtensorMap m_codes0, const __grid_cons
                 if (lane == 0)
                     tc::mbar_arrive(&d_empty[db]);
                 if (a.cs > 1) {
-                    ck_epilogue<NW>(a, fac_s, sum, tile, r, et, seg, ck_buf, ck_full, ck_free);
+                    ck_epilogue<NW, EPI>(a, fac_s, sum, tile, r, et, seg, ck_buf, ck_full, ck_free);
                     if (++j == rg.je) {
                         j = rg.jb;
                         tile += rg.tstep;
@@ -872,11 +869,11 @@ skinny_tc_kernel(const __grid_constant__ CUtensorMap m_codes0, const __grid_cons
                 }
                 // this CTA did the whole tile: units 0 .. C-1
                 const bool whole = seg_j0 == 0 && j == a.C - 1;
-                publish_segment<NW>(a, fac_s, sum, (int)tile, whole, (int)tile_lo, b, r, seg_s);
+                publish_segment<NW, EPI>(a, fac_s, sum, (int)tile, whole, (int)tile_lo, b, r, seg_s);
                 if (i == n_units - 1)
                     break;  // the CTA's last segment is reduced by all threads below
                 if (seg_s->reduce)
-                    reduce_tile<NW>(a, fac_s, *seg_s, r, kEpiThreads);
+                    reduce_tile<NW, EPI>(a, fac_s, *seg_s, r, kEpiThreads);
             }
             if (++j == rg.je) {
                 j = rg.jb;
@@ -889,7 +886,7 @@ skinny_tc_kernel(const __grid_constant__ CUtensorMap m_codes0, const __grid_cons
         // The dequantisers have finished: they help with the last segment.
         tc::named_bar_sync(2, kEpiThreads + kDqWarps * 32);
         if (seg_s->reduce)
-            reduce_tile<NW>(a, fac_s, *seg_s, r, kEpiThreads + kDqWarps * 32);
+            reduce_tile<NW, EPI>(a, fac_s, *seg_s, r, kEpiThreads + kDqWarps * 32);
     } else if (warp >= kFirstDqWarp) {
         // ---- dequantisers (warps 12..27): group g takes items t = g (mod 4) ----
         tc::griddep_wait();
@@ -1037,7 +1034,7 @@ skinny_tc_kernel(const __grid_constant__ CUtensorMap m_codes0, const __grid_cons
         // help the epilogue threads add the partials of the CTA's last segment
         tc::named_bar_sync(2, kEpiThreads + kDqWarps * 32);
         if (seg_s->reduce)
-            reduce_tile<NW>(a, fac_s, *seg_s, kEpiThreads + (threadIdx.x - kFirstDqWarp * 32),
+            reduce_tile<NW, EPI>(a, fac_s, *seg_s, kEpiThreads + (threadIdx.x - kFirstDqWarp * 32),
                             kEpiThreads + kDqWarps * 32);
     }
 
@@ -1091,13 +1088,13 @@ bool make_map(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NW, int FMT = 0>
+template <int NW, int FMT = 0, bool EPI = false>
 cudaError_t set_smem_attr()
 {
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr_err[kMaxDevices];
     return once_per_device(once, attr_err, [] {
-        return cudaFuncSetAttribute(skinny_tc_kernel<NW, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(skinny_tc_kernel<NW, FMT, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)Cfg<NW, FMT>::kSmemBytes);
     });
 }
@@ -1150,15 +1147,15 @@ int max_active_clusters(int cs)
     return cache[dev][ci];
 }
 
-template <int NW, int FMT = 0>
+template <int NW, int FMT = 0, bool EPI = false>
 cudaError_t launch_main(const CUtensorMap (&maps)[5], const Args &a, cudaStream_t stream)
 {
-    const cudaError_t attr_err = set_smem_attr<NW, FMT>();
+    const cudaError_t attr_err = set_smem_attr<NW, FMT, EPI>();
     if (attr_err != cudaSuccess)
         return attr_err;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = main_config<NW, FMT>(a, stream, attr);
-    return cudaLaunchKernelEx(&cfg, skinny_tc_kernel<NW, FMT>, maps[0], maps[1], maps[2], maps[3], maps[4], a);
+    return cudaLaunchKernelEx(&cfg, skinny_tc_kernel<NW, FMT, EPI>, maps[0], maps[1], maps[2], maps[3], maps[4], a);
 }
 
 // Split of the K dimension of every tile: stream-K over all SMs (any split,
@@ -1233,7 +1230,7 @@ size_t skinny_tc_workspace_bytes(int64_t M, int64_t K, int n_weights)
 
 cudaError_t launch_skinny_tc(const uint16_t *x, int N, int64_t M, int64_t K, const uint8_t *const *codes,
                              const uint8_t *const *scales, const float *const *ts, int n_weights, void *y,
-                             int out_bf16, void *workspace, int num_sms, cudaStream_t stream)
+                             int out_bf16, void *workspace, int num_sms, cudaStream_t stream, const Epilogue *epilogue)
 {
     using namespace sk;
     const WsLayout L = ws_layout(M, K, n_weights);
@@ -1305,12 +1302,16 @@ cudaError_t launch_skinny_tc(const uint16_t *x, int N, int64_t M, int64_t K, con
         if (e != cudaSuccess)
             return e;
     }
+    if (epilogue && n_weights == 1) {
+        a.ep = *epilogue;
+        return launch_main<1, 0, true>(maps, a, stream);
+    }
     return n_weights == 1 ? launch_main<1>(maps, a, stream) : launch_main<2>(maps, a, stream);
 }
 
 cudaError_t launch_skinny_tc_fp6(const uint16_t *x, int N, int64_t M, int64_t K, const uint8_t *const *codes,
                                  const uint8_t *const *scales, int n_weights, void *y, int out_bf16,
-                                 void *workspace, int num_sms, cudaStream_t stream)
+                                 void *workspace, int num_sms, cudaStream_t stream, const Epilogue *epilogue)
 {
     using namespace sk;
     const WsLayout L = ws_layout(M, K, n_weights);
@@ -1352,6 +1353,10 @@ cudaError_t launch_skinny_tc_fp6(const uint16_t *x, int N, int64_t M, int64_t K,
     if (!make_map(&maps[4], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, x, (uint64_t)K, (uint64_t)N, (uint64_t)K * 2, 64,
                   (uint32_t)N, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
+    if (epilogue && n_weights == 1) {
+        a.ep = *epilogue;
+        return launch_main<1, 1, true>(maps, a, stream);
+    }
     return n_weights == 1 ? launch_main<1, 1>(maps, a, stream) : launch_main<2, 1>(maps, a, stream);
 }
 

@@ -58,11 +58,20 @@ cudaError_t launch_fp6_quantize_bf16(const uint16_t *w, int64_t M, int64_t K, ui
 cudaError_t launch_import_blocked_scales(const uint8_t *blocked, int64_t M, int64_t K, uint8_t *scales,
                                          cudaStream_t stream);
 
+// What a product call adds to its sums (epilogue.cuh); bias and residual may be null.
+struct Epilogue {
+    const void *bias, *residual;
+    int64_t residual_ld;
+    int32_t bias_bf16, residual_bf16;
+    int32_t act;  // nvfp4_activation
+};
+
 // n_weights = 1: y = x . W^T; n_weights = 2: h = silu(x . Wg^T) * (x . Wu^T)
 // with codes/scales/ts[0] = gate, [1] = up.
 cudaError_t launch_gemv(const uint16_t *x, int N, int64_t M, int64_t K, const uint8_t *const *codes,
                         const uint8_t *const *scales, const float *const *ts, int n_weights, void *y,
-                        int out_bf16, void *workspace, int num_sms, cudaStream_t stream);
+                        int out_bf16, void *workspace, int num_sms, cudaStream_t stream,
+                        const Epilogue *epilogue = nullptr);
 
 int64_t gemv_grid(int64_t M, int64_t K, int num_sms);
 
@@ -73,13 +82,13 @@ int64_t gemv_grid(int64_t M, int64_t K, int num_sms);
 size_t gemv_mma_workspace_bytes(int n_weights);
 cudaError_t launch_gemv_fp6(const uint16_t *x, int N, int64_t M, int64_t K, const uint8_t *const *codes,
                             const uint8_t *const *scales, int n_weights, void *y, int out_bf16, void *workspace,
-                            int num_sms, cudaStream_t stream);
+                            int num_sms, cudaStream_t stream, const Epilogue *epilogue = nullptr);
 cudaError_t launch_skinny_tc_fp6(const uint16_t *x, int N, int64_t M, int64_t K, const uint8_t *const *codes,
                                  const uint8_t *const *scales, int n_weights, void *y, int out_bf16,
-                                 void *workspace, int num_sms, cudaStream_t stream);
+                                 void *workspace, int num_sms, cudaStream_t stream, const Epilogue *epilogue = nullptr);
 cudaError_t launch_prefill_fp6(const uint16_t *x, int64_t N, int64_t M, int64_t K, const uint8_t *const *codes,
                                const uint8_t *const *scales, int n_weights, void *y, int out_bf16,
-                               void *workspace, int num_sms, cudaStream_t stream);
+                               void *workspace, int num_sms, cudaStream_t stream, const Epilogue *epilogue = nullptr);
 
 }  // namespace nvfp4
 
@@ -89,7 +98,8 @@ size_t prefill_workspace_bytes(int64_t N, int64_t M, int64_t K, int n_weights, i
 
 cudaError_t launch_prefill(const uint16_t *x, int64_t N, int64_t M, int64_t K, const uint8_t *const *codes,
                            const uint8_t *const *scales, const float *const *ts, int n_weights, void *y,
-                           int out_bf16, void *workspace, int num_sms, cudaStream_t stream);
+                           int out_bf16, void *workspace, int num_sms, cudaStream_t stream,
+                           const Epilogue *epilogue = nullptr);
 
 }  // namespace nvfp4
 
@@ -101,7 +111,8 @@ bool skinny_tc_supported(int64_t M, int64_t K);
 size_t skinny_tc_workspace_bytes(int64_t M, int64_t K, int n_weights);
 cudaError_t launch_skinny_tc(const uint16_t *x, int N, int64_t M, int64_t K, const uint8_t *const *codes,
                              const uint8_t *const *scales, const float *const *ts, int n_weights, void *y,
-                             int out_bf16, void *workspace, int num_sms, cudaStream_t stream);
+                             int out_bf16, void *workspace, int num_sms, cudaStream_t stream,
+                             const Epilogue *epilogue = nullptr);
 
 // Workspace of the skinny product for any K (tcgen05 path or the mma.sync path).
 size_t skinny_workspace_bytes(int64_t M, int64_t K, int n_weights);
@@ -129,7 +140,8 @@ constexpr uint32_t kStatusKvFirst = 41;
 constexpr uint32_t kStatusKvAppendSlot = 41;  // append: slot beyond the pool
 constexpr uint32_t kStatusKvReadSlot = 42;    // read: slot beyond the pool
 constexpr uint32_t kStatusKvAttention = 43;   // attention: page, length or offset outside its bounds
-constexpr uint32_t kStatusKvLast = 43;
+constexpr uint32_t kStatusPromptOffsets = 44; // attention of prompts: offsets that do not ascend within total
+constexpr uint32_t kStatusKvLast = 44;
 constexpr size_t kKvWorkspaceBytes = 256;     // append and read: the status word
 
 // Streaming multiprocessors of the current device, cached per device; an nvfp4_status.

@@ -90,7 +90,7 @@ int zero_output(void *y, int64_t N, int64_t M, int out_dtype, cudaStream_t s)
 
 int run_products(const uint16_t *x, int64_t N, int64_t M, int64_t K, const uint8_t *const *codes,
                  const uint8_t *const *scales, const float *const *ts, int n_weights, void *y, int out_dtype,
-                 void *ws, cudaStream_t stream)
+                 void *ws, cudaStream_t stream, const Epilogue *epilogue = nullptr)
 {
     int sms = 0;
     int rc = current_num_sms(&sms);
@@ -99,12 +99,33 @@ int run_products(const uint16_t *x, int64_t N, int64_t M, int64_t K, const uint8
     // N <= 16: one skinny launch.  Larger N: tensor-core prefill.
     if (N <= kMaxSkinnyN) {
         cudaError_t e = launch_gemv(x, (int)N, M, K, codes, scales, ts, n_weights, y,
-                                    out_dtype == NVFP4_OUT_BF16, ws, sms, stream);
+                                    out_dtype == NVFP4_OUT_BF16, ws, sms, stream, epilogue);
         return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
     }
     cudaError_t e = launch_prefill(x, N, M, K, codes, scales, ts, n_weights, y, out_dtype == NVFP4_OUT_BF16,
-                                   ws, sms, stream);
+                                   ws, sms, stream, epilogue);
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+
+// Checks an epilogue of an [N][M] output, and makes the kernels' form of it.
+int make_epilogue(const nvfp4_epilogue *e, int64_t N, int64_t M, Epilogue *out)
+{
+    if (!e || e->activation < NVFP4_ACT_NONE || e->activation > NVFP4_ACT_RELU2)
+        return NVFP4_ERR_INVALID_ARG;
+    const auto dtype_ok = [](int d) { return d == NVFP4_OUT_F32 || d == NVFP4_OUT_BF16; };
+    const auto element = [](int d) { return d == NVFP4_OUT_BF16 ? 2 : 4; };
+    if (e->bias && (!dtype_ok(e->bias_dtype) || !aligned(e->bias, element(e->bias_dtype))))
+        return NVFP4_ERR_INVALID_ARG;
+    if (e->residual && (!dtype_ok(e->residual_dtype) || !aligned(e->residual, element(e->residual_dtype)) ||
+                        e->residual_ld < M || !size_ok(N, e->residual_ld)))
+        return NVFP4_ERR_INVALID_ARG;
+    out->bias = e->bias;
+    out->residual = e->residual;
+    out->residual_ld = e->residual_ld;
+    out->bias_bf16 = e->bias_dtype == NVFP4_OUT_BF16;
+    out->residual_bf16 = e->residual_dtype == NVFP4_OUT_BF16;
+    out->act = e->activation;
+    return NVFP4_OK;
 }
 
 }  // namespace
@@ -143,7 +164,7 @@ const char *nvfp4_status_string(int status)
         return "NVFP4_ERR_DEVICE_TIMEOUT: a kernel's bounded pipeline wait gave up; outputs since the status "
                "word was last cleared are undefined";
     case NVFP4_ERR_DEVICE_INDEX:
-        return "NVFP4_ERR_DEVICE_INDEX: a KV-cache kernel met a slot, page, length or offset outside its bounds";
+        return "NVFP4_ERR_DEVICE_INDEX: a KV-cache or attention kernel met a slot, page, length or offset outside its bounds";
     default: return "NVFP4 unknown status";
     }
 }
@@ -283,7 +304,7 @@ int nvfp4_fp6_quantize_bf16(const uint16_t *w, int64_t M, int64_t K, uint8_t *co
 
 static int fp6_products(const uint16_t *x, int64_t N, int64_t M, int64_t K, const uint8_t *const *codes,
                         const uint8_t *const *scales, int n_weights, void *y, int out_dtype, void *ws,
-                        size_t ws_bytes, cudaStream_t stream)
+                        size_t ws_bytes, cudaStream_t stream, const Epilogue *epilogue = nullptr)
 {
     if (N < 0 || M < 0 || K < 0)
         return NVFP4_ERR_INVALID_ARG;
@@ -314,11 +335,11 @@ static int fp6_products(const uint16_t *x, int64_t N, int64_t M, int64_t K, cons
     const int bf16 = out_dtype == NVFP4_OUT_BF16;
     cudaError_t e;
     if (N > kMaxSkinnyN)
-        e = launch_prefill_fp6(x, N, M, K, codes, scales, n_weights, y, bf16, ws, sms, stream);
+        e = launch_prefill_fp6(x, N, M, K, codes, scales, n_weights, y, bf16, ws, sms, stream, epilogue);
     else if (skinny_tc_supported(M, K))
-        e = launch_skinny_tc_fp6(x, (int)N, M, K, codes, scales, n_weights, y, bf16, ws, sms, stream);
+        e = launch_skinny_tc_fp6(x, (int)N, M, K, codes, scales, n_weights, y, bf16, ws, sms, stream, epilogue);
     else
-        e = launch_gemv_fp6(x, (int)N, M, K, codes, scales, n_weights, y, bf16, ws, sms, stream);
+        e = launch_gemv_fp6(x, (int)N, M, K, codes, scales, n_weights, y, bf16, ws, sms, stream, epilogue);
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
@@ -400,6 +421,46 @@ int nvfp4_gemm_prefill(const uint16_t *x, int64_t N, const uint8_t *codes, const
     const uint8_t *s[1] = {scales};
     const float *t[1] = {tensor_scale};
     return run_products(x, N, M, K, c, s, t, 1, y, out_dtype, workspace, (cudaStream_t)stream);
+}
+
+int nvfp4_gemm_epilogue(const uint16_t *x, int64_t N, const uint8_t *codes, const uint8_t *scales,
+                        const float *tensor_scale, int64_t M, int64_t K, const nvfp4_epilogue *epilogue, void *y,
+                        int out_dtype, void *workspace, size_t workspace_bytes, nvfp4_stream_t stream)
+{
+    int rc = check_product(x, N, M, K, codes, scales, tensor_scale, y, out_dtype);
+    Epilogue e;
+    if (rc == NVFP4_OK)
+        rc = make_epilogue(epilogue, N, M, &e);
+    if (rc != NVFP4_OK)
+        return rc;
+    if (K == 0)
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    if (N == 0 || M == 0)
+        return NVFP4_OK;
+    rc = check_workspace(workspace, workspace_bytes, nvfp4_workspace_bytes(NVFP4_OP_GEMM_PREFILL, N, M, K));
+    if (rc != NVFP4_OK)
+        return rc;
+    const uint8_t *c[1] = {codes};
+    const uint8_t *s[1] = {scales};
+    const float *t[1] = {tensor_scale};
+    return run_products(x, N, M, K, c, s, t, 1, y, out_dtype, workspace, (cudaStream_t)stream, &e);
+}
+
+int nvfp4_fp6_gemm_epilogue(const uint16_t *x, int64_t N, const uint8_t *codes, const uint8_t *scales, int64_t M,
+                            int64_t K, const nvfp4_epilogue *epilogue, void *y, int out_dtype, void *workspace,
+                            size_t workspace_bytes, nvfp4_stream_t stream)
+{
+    if (N < 0 || M < 0)
+        return NVFP4_ERR_INVALID_ARG;
+    Epilogue e;
+    const int rc = make_epilogue(epilogue, N, M, &e);
+    if (rc != NVFP4_OK)
+        return rc;
+    if (K == 0)
+        return NVFP4_ERR_UNSUPPORTED_SHAPE;
+    const uint8_t *c[1] = {codes};
+    const uint8_t *s[1] = {scales};
+    return fp6_products(x, N, M, K, c, s, 1, y, out_dtype, workspace, workspace_bytes, (cudaStream_t)stream, &e);
 }
 
 // Status word checks shared by the two calls below: a workspace that holds it.

@@ -57,6 +57,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "epilogue.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"
 
@@ -133,6 +134,7 @@ struct Args {
     int64_t units;        // stream-K units
     int sk_grid;          // CTAs sharing them (<= units)
     float *partial;       // [2 * gridDim][TN][BM] raw fp32 accumulators: a CTA's first and last segment
+    Epilogue ep;          // EPI: what is done with the sums
 };
 
 // Tile index -> (row tile, token tile) in the raster order: groups of `group`
@@ -314,9 +316,42 @@ struct WeightMaps {
     CUtensorMap scales[2];
 };
 
+// EPI: row m of 32 tokens from n0 on, from the accumulators (without TA: two halves of
+// each sum).  Residuals are loaded eight at a time before the stores, which may alias them.
+template <bool TA>
+NVFP4_DEVINL void store_column(const Args &a, const uint32_t (&r)[2][32], float ts, int64_t n0, int64_t m)
+{
+    const float bias = epilogue_bias(a.ep, m);
+#pragma unroll
+    for (int j0 = 0; j0 < 32; j0 += 8) {
+        float res[8];
+        if (a.ep.residual) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                res[j] = n0 + j0 + j < a.N ? epilogue_residual(a.ep, n0 + j0 + j, m) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t n = n0 + j0 + j;
+            if (n < a.N) {
+                const float sum = TA ? __uint_as_float(r[0][j0 + j])
+                                     : __uint_as_float(r[0][j0 + j]) + __uint_as_float(r[1][j0 + j]);
+                float v = activate(a.ep.act, sum * ts + bias);
+                if (a.ep.residual)
+                    v += res[j];
+                const int64_t idx = n * a.M + m;
+                if (a.out_bf16)
+                    reinterpret_cast<uint16_t *>(a.y)[idx] = f32_to_bf16(v);
+                else
+                    reinterpret_cast<float *>(a.y)[idx] = v;
+            }
+        }
+    }
+}
+
 // TN: tokens per tile (MMA N), 256 or 192; the host picks it per call so that
 // the grid fills the SMs' waves (the accumulation order does not depend on it).
-template <int NW, bool ALIGNED, int FMT = 0, bool TMAC = false, int TN = BN, bool SPLIT = false>
+template <int NW, bool ALIGNED, int FMT = 0, bool TMAC = false, int TN = BN, bool SPLIT = false, bool EPI = false>
 __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ WeightMaps wmaps, Args a)
 {
@@ -608,6 +643,8 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             slot[(size_t)(col + j) * BM] = __uint_as_float(r[0][j]);
+                    } else if (EPI && mrow < a.M) {
+                        store_column<TA>(a, r, ts[0], (int64_t)sn0 + col, mrow);
                     } else if (mrow < a.M) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
@@ -874,8 +911,19 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
 }
 
 // Rows mq .. mq + 3 of token n of the output, from fp32 values.
+template <bool EPI>
 NVFP4_DEVINL void store_rows4(const Args &a, int64_t n, int64_t mq, float4 v)
 {
+    if constexpr (EPI) {
+        if (mq < a.M)
+            v.x = epilogue_value(a.ep, v.x, n, mq);
+        if (mq + 1 < a.M)
+            v.y = epilogue_value(a.ep, v.y, n, mq + 1);
+        if (mq + 2 < a.M)
+            v.z = epilogue_value(a.ep, v.z, n, mq + 2);
+        if (mq + 3 < a.M)
+            v.w = epilogue_value(a.ep, v.w, n, mq + 3);
+    }
     const int64_t idx = n * a.M + mq;
     if ((a.M & 3) == 0 && mq + 3 < a.M) {  // 16- / 8-byte aligned, all in range
         if (a.out_bf16)
@@ -912,7 +960,7 @@ NVFP4_DEVINL void store_rows4(const Args &a, int64_t n, int64_t mq, float4 v)
 // picks when every intermediate fits (a fraction of the cost of 64-bit
 // divisions).  A contributor or tile outside the plan's ranges (impossible
 // with the host's plan) records status 10 and skips the item.
-template <bool NARROW>
+template <bool NARROW, bool EPI>
 __global__ void __launch_bounds__(kRedThreads, 4) split_reduce_kernel(Args a)
 {
     using I = typename std::conditional<NARROW, uint32_t, int64_t>::type;
@@ -991,7 +1039,7 @@ __global__ void __launch_bounds__(kRedThreads, 4) split_reduce_kernel(Args a)
         for (int j = 0; j < 2; ++j) {
             const int col = col0 + 8 * j;
             if (col < ncols)
-                store_rows4(a, n0 + col, mq,
+                store_rows4<EPI>(a, n0 + col, mq,
                             make_float4(acc[j].x * tsv, acc[j].y * tsv, acc[j].z * tsv, acc[j].w * tsv));
         }
     }
@@ -1016,14 +1064,14 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-template <int NW, bool ALIGNED, int FMT = 0, bool TMAC = false, int TN = BN, bool SPLIT = false>
+template <int NW, bool ALIGNED, int FMT = 0, bool TMAC = false, int TN = BN, bool SPLIT = false, bool EPI = false>
 cudaError_t launch_t(const CUtensorMap &map, const WeightMaps &wm, const Args &a, cudaStream_t stream)
 {
     using C = Cfg<NW, TMAC, FMT, TN>;
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr_errs[kMaxDevices];
     const cudaError_t attr_err = once_per_device(once, attr_errs, [] {
-        return cudaFuncSetAttribute(prefill_kernel<NW, ALIGNED, FMT, TMAC, TN, SPLIT>,
+        return cudaFuncSetAttribute(prefill_kernel<NW, ALIGNED, FMT, TMAC, TN, SPLIT, EPI>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmemBytes);
     });
     if (attr_err != cudaSuccess)
@@ -1042,9 +1090,9 @@ cudaError_t launch_t(const CUtensorMap &map, const WeightMaps &wm, const Args &a
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, prefill_kernel<NW, ALIGNED, FMT, TMAC, TN, SPLIT>, map, wm, a);
+        return cudaLaunchKernelEx(&cfg, prefill_kernel<NW, ALIGNED, FMT, TMAC, TN, SPLIT, EPI>, map, wm, a);
     }
-    prefill_kernel<NW, ALIGNED, FMT, TMAC, TN, SPLIT>
+    prefill_kernel<NW, ALIGNED, FMT, TMAC, TN, SPLIT, EPI>
         <<<grid, TMAC ? kThreadsTma : kThreads, C::kSmemBytes, stream>>>(map, wm, a);
     return cudaGetLastError();
 }
@@ -1054,6 +1102,7 @@ cudaError_t launch_t(const CUtensorMap &map, const WeightMaps &wm, const Args &a
 // launch's completion before reading a partial.  Four CTAs fit on an SM;
 // the grid stops at eight CTAs per SM and takes any further items in its
 // grid-stride loop.
+template <bool EPI>
 inline cudaError_t launch_split_reduce(const Args &a, int num_sms, cudaStream_t stream)
 {
     const int64_t items = a.units / a.kq * (BN / kRedCols);
@@ -1074,8 +1123,8 @@ inline cudaError_t launch_split_reduce(const Args &a, int num_sms, cudaStream_t 
     const bool narrow = (uint64_t)(a.units + 1) * (uint64_t)a.sk_grid < lim &&
                         (uint64_t)(a.sk_base + a.units) < lim;
     if (narrow)
-        return cudaLaunchKernelEx(&cfg, split_reduce_kernel<true>, a);
-    return cudaLaunchKernelEx(&cfg, split_reduce_kernel<false>, a);
+        return cudaLaunchKernelEx(&cfg, split_reduce_kernel<true, EPI>, a);
+    return cudaLaunchKernelEx(&cfg, split_reduce_kernel<false, EPI>, a);
 }
 
 // Token tile for a TMA-fed launch: 192 instead of 256 when that fills the
@@ -1219,9 +1268,12 @@ size_t prefill_workspace_bytes(int64_t N, int64_t M, int64_t K, int n_weights, i
     return 256 + (size_t)2 * ctas * pf::BN * pf::BM * sizeof(float);
 }
 
+// EPI: with an epilogue (one matrix).
+template <bool EPI>
 static cudaError_t prefill_impl(const uint16_t *x, int64_t N, int64_t M, int64_t K, const uint8_t *const *codes,
                                 const uint8_t *const *scales, const float *const *ts, int n_weights, void *y,
-                                int out_bf16, void *workspace, int fmt, int num_sms, cudaStream_t stream)
+                                int out_bf16, void *workspace, int fmt, int num_sms, cudaStream_t stream,
+                                const Epilogue *epilogue)
 {
     auto encode = pf::encode_fn();
     if (!encode)
@@ -1253,6 +1305,8 @@ static cudaError_t prefill_impl(const uint16_t *x, int64_t N, int64_t M, int64_t
     }
     a.y = y;
     a.out_bf16 = out_bf16;
+    if (EPI)
+        a.ep = *epilogue;
     a.N = N;
     a.M = M;
     a.K = K;
@@ -1301,11 +1355,16 @@ static cudaError_t prefill_impl(const uint16_t *x, int64_t N, int64_t M, int64_t
         for (int i = 0; i < n_weights; ++i)
             if (!pf::encode_rows(encode, &wm.codes[i], codes[i], K / 4 * 3, M, pf::code_row_bytes<1>()))
                 return cudaErrorInvalidValue;
-        if (tn == 192)
-            return n_weights == 1 ? pf::launch_t<1, true, 1, true, 192>(map, wm, a, stream)
-                                  : pf::launch_t<2, true, 1, true, 192>(map, wm, a, stream);
-        return n_weights == 1 ? pf::launch_t<1, true, 1, true>(map, wm, a, stream)
-                              : pf::launch_t<2, true, 1, true>(map, wm, a, stream);
+        if constexpr (EPI) {
+            return tn == 192 ? pf::launch_t<1, true, 1, true, 192, false, true>(map, wm, a, stream)
+                             : pf::launch_t<1, true, 1, true, 256, false, true>(map, wm, a, stream);
+        } else {
+            if (tn == 192)
+                return n_weights == 1 ? pf::launch_t<1, true, 1, true, 192>(map, wm, a, stream)
+                                      : pf::launch_t<2, true, 1, true, 192>(map, wm, a, stream);
+            return n_weights == 1 ? pf::launch_t<1, true, 1, true>(map, wm, a, stream)
+                                  : pf::launch_t<2, true, 1, true>(map, wm, a, stream);
+        }
     }
     if (K % 256 == 0) {
         // Codes and scales by TMA: row pitches K/2 and K/16 are multiples of 16 bytes.
@@ -1320,39 +1379,51 @@ static cudaError_t prefill_impl(const uint16_t *x, int64_t N, int64_t M, int64_t
                 w.split = 0;
                 w.after_whole = 0;
                 w.grid = (int)(sp.dp_waves * num_sms);
-                const cudaError_t e = pf::launch_t<1, true, 0, true, 256>(map, wm, w, stream);
+                const cudaError_t e = pf::launch_t<1, true, 0, true, 256, false, EPI>(map, wm, w, stream);
                 if (e != cudaSuccess)
                     return e;
             }
-            const cudaError_t e = pf::launch_t<1, true, 0, true, 256, true>(map, wm, a, stream);
+            const cudaError_t e = pf::launch_t<1, true, 0, true, 256, true, EPI>(map, wm, a, stream);
             if (e != cudaSuccess)
                 return e;
-            return pf::launch_split_reduce(a, num_sms, stream);
+            return pf::launch_split_reduce<EPI>(a, num_sms, stream);
         }
-        if (tn == 192)
-            return n_weights == 1 ? pf::launch_t<1, true, 0, true, 192>(map, wm, a, stream)
-                                  : pf::launch_t<2, true, 0, true, 192>(map, wm, a, stream);
-        return n_weights == 1 ? pf::launch_t<1, true, 0, true>(map, wm, a, stream)
-                              : pf::launch_t<2, true, 0, true>(map, wm, a, stream);
+        if constexpr (EPI) {
+            return tn == 192 ? pf::launch_t<1, true, 0, true, 192, false, true>(map, wm, a, stream)
+                             : pf::launch_t<1, true, 0, true, 256, false, true>(map, wm, a, stream);
+        } else {
+            if (tn == 192)
+                return n_weights == 1 ? pf::launch_t<1, true, 0, true, 192>(map, wm, a, stream)
+                                      : pf::launch_t<2, true, 0, true, 192>(map, wm, a, stream);
+            return n_weights == 1 ? pf::launch_t<1, true, 0, true>(map, wm, a, stream)
+                                  : pf::launch_t<2, true, 0, true>(map, wm, a, stream);
+        }
     }
     const bool aligned = K % 32 == 0;
-    if (n_weights == 1)
-        return aligned ? pf::launch_t<1, true>(map, wm, a, stream) : pf::launch_t<1, false>(map, wm, a, stream);
-    return aligned ? pf::launch_t<2, true>(map, wm, a, stream) : pf::launch_t<2, false>(map, wm, a, stream);
+    if constexpr (EPI) {
+        return aligned ? pf::launch_t<1, true, 0, false, 256, false, true>(map, wm, a, stream)
+                       : pf::launch_t<1, false, 0, false, 256, false, true>(map, wm, a, stream);
+    } else {
+        if (n_weights == 1)
+            return aligned ? pf::launch_t<1, true>(map, wm, a, stream) : pf::launch_t<1, false>(map, wm, a, stream);
+        return aligned ? pf::launch_t<2, true>(map, wm, a, stream) : pf::launch_t<2, false>(map, wm, a, stream);
+    }
 }
 
 cudaError_t launch_prefill(const uint16_t *x, int64_t N, int64_t M, int64_t K, const uint8_t *const *codes,
                            const uint8_t *const *scales, const float *const *ts, int n_weights, void *y,
-                           int out_bf16, void *workspace, int num_sms, cudaStream_t stream)
+                           int out_bf16, void *workspace, int num_sms, cudaStream_t stream, const Epilogue *epilogue)
 {
-    return prefill_impl(x, N, M, K, codes, scales, ts, n_weights, y, out_bf16, workspace, 0, num_sms, stream);
+    const auto impl = epilogue && n_weights == 1 ? prefill_impl<true> : prefill_impl<false>;
+    return impl(x, N, M, K, codes, scales, ts, n_weights, y, out_bf16, workspace, 0, num_sms, stream, epilogue);
 }
 
 cudaError_t launch_prefill_fp6(const uint16_t *x, int64_t N, int64_t M, int64_t K, const uint8_t *const *codes,
                                const uint8_t *const *scales, int n_weights, void *y, int out_bf16,
-                               void *workspace, int num_sms, cudaStream_t stream)
+                               void *workspace, int num_sms, cudaStream_t stream, const Epilogue *epilogue)
 {
-    return prefill_impl(x, N, M, K, codes, scales, nullptr, n_weights, y, out_bf16, workspace, 1, num_sms, stream);
+    const auto impl = epilogue && n_weights == 1 ? prefill_impl<true> : prefill_impl<false>;
+    return impl(x, N, M, K, codes, scales, nullptr, n_weights, y, out_bf16, workspace, 1, num_sms, stream, epilogue);
 }
 
 // Failure-path self-test: one thread waits, with the same bounded wait as the

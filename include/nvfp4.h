@@ -95,7 +95,7 @@ typedef enum {
     NVFP4_ERR_WORKSPACE = 3,         /* workspace smaller than nvfp4_workspace_bytes() */
     NVFP4_ERR_CUDA = 4,              /* a CUDA runtime call or kernel launch failed */
     NVFP4_ERR_DEVICE_TIMEOUT = 5,    /* a kernel's bounded wait gave up (nvfp4_device_status) */
-    NVFP4_ERR_DEVICE_INDEX = 6       /* a KV-cache kernel met an index outside the cache (nvfp4_device_status) */
+    NVFP4_ERR_DEVICE_INDEX = 6       /* a KV-cache or attention kernel met an index outside its bounds (nvfp4_device_status) */
 } nvfp4_status;
 
 /* Operation ids for nvfp4_workspace_bytes. */
@@ -352,6 +352,53 @@ int nvfp4_fp6_gateup_swiglu(const uint16_t *x, int64_t N,
                             void *workspace, size_t workspace_bytes, nvfp4_stream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Products with an epilogue, any N >= 1:
+ *     y[n][m] = residual[n][m] + act(sum_k x[n][k] * W[m][k] + bias[m]),
+ * in fp32 from the product's sums on, rounded once to the output's type: a QKV product with
+ * its bias, an O or down product onto the residual stream, an ungated MLP's first product with its
+ * activation, without another pass over [N][M].  The product itself is that of
+ * nvfp4_gemm_prefill (nvfp4_fp6_gemm): the same kernels, sums, workspace and accuracy, so with
+ * the sum's error d = 1e-5 * sum |w * x| + 1e-7,
+ *     |y - exact| <= L * (d + 2^-23 * |sum + bias|) + 2^-20 * (1 + u) * |act| + 2^-24 * |y| + 1e-30, and
+ * the rounding of y, where L bounds the activation's slope around sum + bias (at most 1.13 but for
+ * RELU2's 2 v) and u is 0 but for GELU_TANH, whose exponent's magnitude it is: |2 sqrt(2 / pi) (v + 0.044715 v^3)|.
+ * ------------------------------------------------------------------------- */
+typedef enum {
+    NVFP4_ACT_NONE = 0,
+    NVFP4_ACT_SILU = 1,      /* v / (1 + exp(-v)) */
+    NVFP4_ACT_GELU = 2,      /* v * Phi(v), Phi the normal distribution */
+    NVFP4_ACT_GELU_TANH = 3, /* v / 2 * (1 + tanh(sqrt(2 / pi) * (v + 0.044715 v^3))) */
+    NVFP4_ACT_RELU = 4,      /* max(v, 0); NaN stays NaN */
+    NVFP4_ACT_RELU2 = 5      /* max(v, 0)^2 */
+} nvfp4_activation;
+
+typedef struct {
+    const void *bias;       /* device [M], or NULL for none */
+    const void *residual;   /* device [N][residual_ld], or NULL for none; may be y itself (same type,
+                               residual_ld = M: in place), and must not overlap it otherwise */
+    int64_t residual_ld;    /* elements between token rows, at least M */
+    int32_t bias_dtype;     /* nvfp4_out_dtype */
+    int32_t residual_dtype; /* nvfp4_out_dtype */
+    int32_t activation;     /* nvfp4_activation */
+    int32_t reserved;       /* 0 */
+} nvfp4_epilogue;
+
+/* Arguments, workspace (NVFP4_OP_GEMM_PREFILL; under the skinny calls' contract for N <= 16) and errors as for
+ * nvfp4_gemm_prefill; bias and residual aligned to their elements.  K = 0 is refused
+ * (NVFP4_ERR_UNSUPPORTED_SHAPE). */
+int nvfp4_gemm_epilogue(const uint16_t *x, int64_t N,
+                        const uint8_t *codes, const uint8_t *scales,
+                        const float *tensor_scale, int64_t M, int64_t K,
+                        const nvfp4_epilogue *epilogue, void *y, int out_dtype,
+                        void *workspace, size_t workspace_bytes, nvfp4_stream_t stream);
+
+/* The same for FP6 weights: arguments, workspace (NVFP4_OP_FP6_GEMM) and errors as for nvfp4_fp6_gemm. */
+int nvfp4_fp6_gemm_epilogue(const uint16_t *x, int64_t N,
+                            const uint8_t *codes, const uint8_t *scales, int64_t M, int64_t K,
+                            const nvfp4_epilogue *epilogue, void *y, int out_dtype,
+                            void *workspace, size_t workspace_bytes, nvfp4_stream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Quantised paged KV cache, and the attention that reads it: what a decoder
  * layer needs between its QKV product and its O product.  (The pages keep
  * their caches in 8 and 4 bits and attend to them in decode, in verify and in
@@ -504,6 +551,110 @@ size_t nvfp4_paged_attention_workspace_bytes(const nvfp4_paged_attention_args *a
 int nvfp4_paged_attention(const nvfp4_paged_attention_args *args, void *workspace, size_t workspace_bytes,
                           nvfp4_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Rotary positions: between a decoder layer's QKV product and its attention.
+ *
+ * A head's first 2 n_pairs elements are pairs of coordinates, and token t turns pair i
+ * by the angle a = positions[axis(i)][t] * inv_freq(i):
+ *     x' = scale * (x cos a - y sin a),   y' = scale * (x sin a + y cos a);
+ * with `inverse` by -a (which, with the same scale, is the transpose: it takes the
+ * outputs' gradients to the inputs').  Pair i is elements (i, i + n_pairs), or with
+ * `adjacent` (2 i, 2 i + 1); elements from 2 n_pairs on are not turned.  Text has one
+ * axis; images and video one each for height and width, and for time.
+ *
+ * Numerics: angles are exact to |position| * 2^-65 + 2^-27 turns for any position (a
+ * frequency is a 64-bit fraction of a turn, and whole turns fall away in the integer
+ * product); fp32 sines, cosines and products, one rounding to the output's type.
+ * ------------------------------------------------------------------------- */
+
+/* One pair's frequency and axis, in device memory for nvfp4_rope. */
+typedef struct {
+    uint64_t turn;     /* inv_freq / (2 pi) as a fraction of 2^64 */
+    uint32_t axis;     /* row of `positions` */
+    uint32_t reserved; /* 0 */
+} nvfp4_rope_pair;
+
+/* Host only: the table's entries for n_pairs frequencies (radians per position, any
+ * finite values below 2^31) and axes (0 to 255; NULL: all 0), to host memory `pairs`, which the
+ * caller copies to the device once. */
+int nvfp4_rope_pairs(const double *inv_freq, const int32_t *axis, int32_t n_pairs, nvfp4_rope_pair *pairs);
+
+/* Turn the heads of q and k: n_q_heads (n_k_heads) heads of head_dim elements side by side
+ * per token, so that inputs can be column ranges of one QKV product's output.
+ * An output may be its input (the same pointer and stride: in place); other overlaps race.
+ * Requirements: head_dim a multiple of 8, at most 512; 2 n_pairs <= head_dim; pointers
+ * 16-byte aligned and strides multiples of 16 bytes; axes in `pairs` below n_axes (a larger one
+ * reads the last axis).  No workspace.  Rows of q or k are not looked at where its number of heads
+ * is 0. */
+typedef struct {
+    const void *q, *k;        /* device [n_tokens][q_ld], [n_tokens][k_ld]: fp32, or bf16 bits */
+    int64_t q_ld, k_ld;
+    void *q_out, *k_out;      /* device [n_tokens][q_out_ld], [n_tokens][k_out_ld], same type */
+    int64_t q_out_ld, k_out_ld;
+    const int64_t *positions; /* device [n_axes][positions_ld] */
+    int64_t positions_ld;     /* at least n_tokens (not looked at with one axis) */
+    const nvfp4_rope_pair *pairs; /* device [n_pairs] */
+    int64_t n_tokens;         /* below 2^31 */
+    int32_t n_axes;           /* 1 to 256 */
+    int32_t n_pairs;
+    int32_t n_q_heads, n_k_heads; /* 0 to 8192 */
+    int32_t head_dim;
+    int32_t dtype;            /* nvfp4_out_dtype, of inputs and outputs */
+    int32_t adjacent;         /* 0 or 1 */
+    int32_t inverse;          /* 0 or 1 */
+    float scale;              /* finite; 1 for a plain rotation */
+    int32_t reserved;         /* 0 */
+} nvfp4_rope_args;
+
+int nvfp4_rope(const nvfp4_rope_args *args, nvfp4_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention over whole prompts: the packed tokens of n_seqs sequences attend to their own
+ * sequence's K and V in bf16 (nothing of it cached or quantised).  Sequence b is
+ * rows offsets[b] .. offsets[b + 1] - 1 of q, k, v and out; its token i sees
+ *   causal       tokens j <= i; with window > 0 only j > i - window;
+ *   not causal   every token of its sequence (encoders, images).
+ * out = sum_j softmax_j(scale * q_i . k_j) v_j over the tokens it sees, query head h
+ * reading KV head h / (n_q_heads / n_kv_heads).  K and V of tokens that a token does not see
+ * never reach its output, whatever they hold; a query, or a K or V row that it sees, with an infinity or
+ * a NaN gives outputs that are not finite.  Rows of out that belong to no sequence are left as they are.
+ *
+ * Numerics: q . k_j exact in its products with fp32 accumulation; softmax statistics in
+ * fp32 (2^x by the hardware's approximation, relative error about 2^-22); the weights enter
+ * the second product rounded to bf16, with a relative error of at most 2^-8 each, and fp32
+ * accumulation: |out - exact| <= (2^-8 + 2^-15 * S) * sum_j softmax_j |v_j|, plus the
+ * rounding of out, with S = max_j |scale| * sum_d |q_d k_jd|.  Scores have to stay within
+ * fp32's range.
+ *
+ * Requirements: head_dim 64 or 128; n_q_heads a multiple of n_kv_heads, at most 128 times as
+ * many; q, k, v, out 16-byte aligned, their strides multiples of 8 elements and at least a row of all
+ * heads (so that q, k and v can be column ranges of one QKV product's output).
+ * Offsets stay on the device: the call never synchronises and can be captured in a CUDA graph
+ * and replayed with other lengths.  A sequence whose two
+ * offsets do not ascend within 0 .. total stores code 44 in the status word and is left out.
+ * workspace  NULL, or at least 256 bytes with the status word (nvfp4_device_status): nothing
+ *            else is kept there, so calls on several streams may share it.
+ * Determinism: a token's result depends on its place in its sequence and on what it sees alone,
+ * never on timing. */
+typedef struct {
+    const uint16_t *q, *k, *v;  /* device bf16 bits [total][q_ld], [total][k_ld], [total][v_ld] */
+    int64_t q_ld, k_ld, v_ld;
+    void *out;                  /* device [total][out_ld], fp32 or bf16 bits; not q, k or v */
+    int64_t out_ld;
+    const int32_t *offsets;     /* device [n_seqs + 1]; NULL: one sequence of `total` tokens (n_seqs = 1) */
+    int64_t n_seqs;             /* at most 65535 */
+    int64_t total;              /* rows of q, k, v and out, below 2^31 / 8192 */
+    int64_t window;             /* 0: none */
+    int32_t n_q_heads, n_kv_heads;
+    int32_t head_dim;
+    int32_t out_dtype;          /* nvfp4_out_dtype */
+    int32_t causal;             /* 0 or 1 */
+    float scale;                /* finite */
+} nvfp4_prompt_attention_args;
+
+int nvfp4_prompt_attention(const nvfp4_prompt_attention_args *args, void *workspace, size_t workspace_bytes,
+                           nvfp4_stream_t stream);
+
 /* Skinny product without a caller workspace, for callers that cannot allocate
  * device memory.  The source pages have no counterpart for this call: it is an
  * addition of this library.  A plain C or Fortran host program with no
@@ -563,9 +714,9 @@ int nvfp4_noalloc_selftest_wait_timeout(nvfp4_stream_t stream);
  * whose bounded pipeline wait runs out (2 s) stores a nonzero code there and
  * returns: 1..8 from the prefill kernel, 10 from its split-mode reduction
  * (a contributor or tile outside the plan, which the host's plan rules out),
- * 11..25 from the skinny kernel, 51..54 from nvfp4_paged_attention, 127 from
- * nvfp4_selftest_wait_timeout.  No kernel clears the word, so it reports any
- * failure since it was last cleared; the codes 41..43 of the KV-cache calls are
+ * 11..25 from the skinny kernel, 51..54 from nvfp4_paged_attention, 61..64 from
+ * nvfp4_prompt_attention, 127 from nvfp4_selftest_wait_timeout.  No kernel clears the word, so it reports any
+ * failure since it was last cleared; the codes 41..44 of the KV-cache and attention calls are
  * stored only where it is zero, so that a timeout stays visible.  It starts clean when the workspace is
  * zero-filled (required for the skinny calls; do it for a prefill workspace
  * too before reading its status).  A quantise call overwrites the word. */
@@ -575,8 +726,8 @@ int nvfp4_noalloc_selftest_wait_timeout(nvfp4_stream_t stream);
  * NVFP4_STATUS_WORD_OFFSET + 4 bytes, 16-byte aligned) after the work enqueued
  * on `stream` so far: synchronises `stream`, stores the word in *code (if
  * code is not NULL) and returns NVFP4_OK when it is zero,
- * NVFP4_ERR_DEVICE_INDEX when it holds one of the codes 41..43 of the KV-cache
- * calls, else NVFP4_ERR_DEVICE_TIMEOUT.  With clear != 0 a nonzero word is
+ * NVFP4_ERR_DEVICE_INDEX when it holds one of the codes 41..44 of the KV-cache
+ * and attention calls, else NVFP4_ERR_DEVICE_TIMEOUT.  With clear != 0 a nonzero word is
  * reset to zero on `stream` afterwards.  NVFP4_ERR_INVALID_ARG for a null, misaligned or too
  * small workspace; NVFP4_ERR_CUDA if the copy or the synchronisation fails. */
 int nvfp4_device_status(const void *workspace, size_t workspace_bytes, int clear, uint32_t *code,
