@@ -60,6 +60,7 @@
 
 #include <cstdint>
 
+#include "attention_ops.cuh"
 #include "attention_plan.cuh"
 #include "skinny.cuh"
 
@@ -164,101 +165,12 @@ struct Shared {
 };
 static_assert(sizeof(Shared) <= kSharedBytes, "barriers");
 
-// One lane of a converged warp; unlike a test of the lane number this tells the
-// compiler that a single thread follows, and MMA operands can go to uniform
-// registers directly (measured: 83 instead of 170 clocks per tcgen05.mma
-// issued back to back by one thread, M = N = 128, A in tensor memory).
-NVFP4_DEVINL bool elect_one()
-{
-    uint32_t p;
-    asm volatile("{ .reg .pred q; .reg .b32 r; elect.sync r|q, 0xFFFFFFFF; selp.u32 %0, 1, 0, q; }" : "=r"(p));
-    return p != 0;
-}
-
-NVFP4_DEVINL uint32_t f32x2_to_f16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-NVFP4_DEVINL uint32_t f32x2_to_bf16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-template <int N>
-NVFP4_DEVINL void take_regs()
-{
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-NVFP4_DEVINL void give_regs()
-{
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// Pairs of fp32 in one instruction.
-NVFP4_DEVINL uint64_t pack2(float lo, float hi)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-NVFP4_DEVINL float2 unpack2(uint64_t v)
-{
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-    return f;
-}
-NVFP4_DEVINL uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-NVFP4_DEVINL uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-NVFP4_DEVINL float max3(float a, float b, float c)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-// Holds every later use of loaded registers behind the wait before it.
-NVFP4_DEVINL void settle(uint32_t (&r)[32])
-{
-    asm volatile(""
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
-                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
-                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31]));
-}
-
 // Address of 16-byte chunk `oc` (8 elements) of row `r` of a 128-row f16
 // operand: 64-element column blocks of 128 rows x 128 bytes, chunks of a row
 // permuted by the 128-byte swizzle.
 NVFP4_DEVINL uint32_t operand_chunk(uint32_t base, int r, int oc)
 {
     return base + (oc >> 3) * (128 * 128) + r * 128 + (((oc & 7) ^ (r & 7)) << 4);
-}
-
-// B operand read with the key index as the reduction: rows are keys, the other
-// index is contiguous.  Leading offset: between 64-element column blocks;
-// stride offset: between groups of 8 keys.
-NVFP4_DEVINL uint64_t desc_transposed(uint32_t addr)
-{
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | (uint64_t)(128 * 128 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
-           1ull << 46 | 2ull << 61;
 }
 
 // A softmax group's part of a tile's sequence: with SPLIT, group g takes the

@@ -20,16 +20,10 @@
 #pragma once
 
 #include "attention.h"
+#include "attention_ops.cuh"
 
 namespace nvfp4 {
 namespace attn {
-
-NVFP4_DEVINL float ex2(float x)
-{
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 
 // 2^x, down to fp32's smallest numbers.
 NVFP4_DEVINL float ex2_subnormal(float x)

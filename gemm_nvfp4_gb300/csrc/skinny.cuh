@@ -102,5 +102,10 @@ using tc::bulk_load;
 bool make_map(CUtensorMap *map, CUtensorMapDataType dt, const void *base, uint64_t inner, uint64_t outer,
               uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swz);
 
+// Host: the same for bf16 rows of `heads` heads side by side, `ld` elements apart: boxes of 64 elements (128
+// bytes, swizzled) of box_heads heads of box_rows rows.
+bool make_head_map(CUtensorMap *map, const uint16_t *base, int head_dim, int heads, int64_t rows, int64_t ld, int box_heads,
+                   int box_rows);
+
 }  // namespace sk
 }  // namespace nvfp4
