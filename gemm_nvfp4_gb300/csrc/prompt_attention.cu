@@ -14,7 +14,7 @@
 //                   over the scores.  A row's reference (an upper estimate of its largest score) moves
 //                   only when 64 weights sum to more than 2^15, so there is no pass for the maximum.
 //   warp 8          finds the items and loads Q, K and V by TMA.
-//   warps 9, 10     MMA issue for row tile 0 and 1.
+//   warp 9          MMA issue.
 //   warps 12-15     look through V tiles in which rows see different keys: an infinity or a NaN
 //                   there would reach every row through 0 * inf, so it is taken out of the tile, and
 //                   added at the end to the rows that do see it.
@@ -43,7 +43,7 @@ using namespace attn;
 constexpr int kMaxGroup = 128;  // query heads of a KV head
 constexpr int kTile = 128;      // keys of a tile, rows of a row tile
 constexpr int kThreads = 512;
-constexpr int kLoadWarp = 8, kMmaWarp = 9, kAllocWarp = 11, kScanWarp = 12;
+constexpr int kLoadWarp = 8, kMmaWarp = 9, kAllocWarp = 10, kScanWarp = 12;
 // Registers of a thread by role: what the launch gives every thread, shared out anew.
 constexpr int kLaunchRegs = 128, kSoftmaxRegs = 176, kOtherRegs = 80;
 static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= kThreads * kLaunchRegs,
@@ -95,7 +95,7 @@ struct Item {
 
 struct Shared {
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], v_ready[4];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2][2], pv_done[2][2], o_free[2], drain[2];
+    uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2][2], half_done[2], o_full[2], o_free[2], drain;
     uint64_t item_full[kItems], item_empty[kItems], scanned[kItems];
     Item item[kItems];
     uint32_t bad[kItems];                         // whether the item has bad keys
@@ -285,18 +285,36 @@ NVFP4_DEVINL bool load_role(const Call &c, const CUtensorMap *q_map, const CUten
 }
 
 // ---------------------------------------------------------------------------
-// MMA warps
+// MMA warp
 // ---------------------------------------------------------------------------
 
+// One thread issues every product, in the order
+//     S0(0) S1(0)  then for each key tile i:  PV0(i) S0(i+1) PV1(i) S1(i+1),
+// so that one row tile's products run while the other is in its softmax.  (With a thread for each row
+// tile both came to wait for their softmax at the same time.)  Products of one thread run in
+// the order of issue, which lets S(i+1) overwrite the scores that PV(i) reads as weights.
 template <int D>
-NVFP4_DEVINL bool mma_role(const Call &c, Shared *sh, uint32_t smem, uint32_t tmem, int t)
+NVFP4_DEVINL bool mma_role(const Call &c, Shared *sh, uint32_t smem, uint32_t tmem)
 {
     using C = Cfg<D>;
     constexpr uint32_t score_idesc = tc::idesc_f16kind(kTile, kTile, 1);
     constexpr uint32_t out_idesc = tc::idesc_f16kind(kTile, D, 1) | 1u << 16;  // B transposed
-    const uint32_t scores = tmem + t * kTile, out = tmem + C::kOutCols + t * D, q = smem + t * C::kOperand;
-    uint32_t ks = 0, vs = 0, items = 0, mine = 0;  // tiles of K and V so far, the row tile's items and tiles
+    uint32_t ks = 0, vs = 0, items[2] = {0, 0}, mine[2] = {0, 0};  // tiles of K and V so far, the row tiles' items and products P V
     bool ok = true;
+    const auto score = [&](const Part &part, int t, int i) {
+        const uint32_t k = smem + C::kKAt + (ks % C::kKs) * C::kOperand, q = smem + t * C::kOperand;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+            const uint32_t at = (d / 4) * (kTile * 128) + (d % 4) * 32;
+            const uint64_t base = 1ull << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+            tc::mma_bf16_ss(tmem + t * kTile, base | ((q + at) & 0x3FFFFu) >> 4, base | ((k + at) & 0x3FFFFu) >> 4, score_idesc,
+                            d > 0);
+        }
+        tc::mma_commit(&sh->s_full[t]);
+        if (i + 1 == part.end)
+            tc::mma_commit(&sh->q_empty[t]);
+    };
+    const auto uses = [](const Part &part, int i) { return part.active && i >= part.first && i < part.end; };
     for (uint32_t n = 0; ok; ++n) {
         const uint32_t slot = n % kItems;
         if (!(ok = tc::mbar_wait(&sh->item_full[slot], (n / kItems) & 1)))
@@ -305,63 +323,66 @@ NVFP4_DEVINL bool mma_role(const Call &c, Shared *sh, uint32_t smem, uint32_t tm
         tc::mbar_arrive(&sh->item_empty[slot]);
         if (it.len == 0)
             break;
-        const Part part = part_of(c, it, t);
-        if (part.active)
-            ok = tc::mbar_wait(&sh->q_full[t], items & 1);
+        const Part part[2] = {part_of(c, it, 0), part_of(c, it, 1)};
         const int tiles = it.tiles();
-        for (int i = 0; i < tiles && ok; ++i, ++ks, ++vs) {
-            const bool use = part.active && i >= part.first && i < part.end;
-            const uint32_t k_slot = ks % C::kKs, v_slot = vs % C::kVs;
-            ok = tc::mbar_wait(&sh->k_full[k_slot], (ks / C::kKs) & 1);
-            if (!use) {
-                ok = ok && tc::mbar_wait(&sh->v_full[v_slot], (vs / C::kVs) & 1) &&
-                     tc::mbar_wait(&sh->v_ready[v_slot], (vs / C::kVs) & 1);
-                tc::mbar_arrive(&sh->k_empty[k_slot]);
-                tc::mbar_arrive(&sh->v_empty[v_slot]);
-                continue;
-            }
-            // the weights of the tile before lie where its scores go
-            ok = ok && (mine == 0 || tc::mbar_wait(&sh->pv_done[t][1], (mine - 1) & 1));
-            if (!ok)
-                break;
-            tc::fence_after_sync();
-            const uint32_t k = smem + C::kKAt + k_slot * C::kOperand;
+        ok = tc::mbar_wait(&sh->k_full[ks % C::kKs], (ks / C::kKs) & 1);
 #pragma unroll
-            for (int d = 0; d < D / 16; ++d) {
-                const uint32_t at = (d / 4) * (kTile * 128) + (d % 4) * 32;
-                const uint64_t base = 1ull << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
-                tc::mma_bf16_ss(scores, base | ((q + at) & 0x3FFFFu) >> 4, base | ((k + at) & 0x3FFFFu) >> 4, score_idesc, d > 0);
-            }
-            tc::mma_commit(&sh->s_full[t]);
-            tc::mma_commit(&sh->k_empty[k_slot]);
-            if (i + 1 == part.end)
-                tc::mma_commit(&sh->q_empty[t]);
-            ok = tc::mbar_wait(&sh->v_full[v_slot], (vs / C::kVs) & 1) && tc::mbar_wait(&sh->v_ready[v_slot], (vs / C::kVs) & 1);
-            // the item before has been read out
-            if (i == part.first && items > 0)
-                ok = ok && tc::mbar_wait(&sh->o_free[t], (items - 1) & 1);
-            const uint32_t v = smem + C::kVAt + v_slot * C::kOperand;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                ok = ok && tc::mbar_wait(&sh->p_ready[t][h], mine & 1);
-                if (!ok)
-                    break;
-                tc::fence_after_sync();
-#pragma unroll
-                for (int j = 0; j < kTile / 32; ++j)
-                    tc::mma_f16_ts(out, scores + h * (kTile / 2) + 8 * j, desc_transposed(v + (h * (kTile / 32) + j) * 2048),
-                                   out_idesc, i > part.first || h > 0 || j > 0);
-                tc::mma_commit(&sh->pv_done[t][h]);
-            }
-            tc::mma_commit(&sh->v_empty[v_slot]);
-            ++mine;
+        for (int t = 0; t < 2; ++t) {
+            if (part[t].active)
+                ok = ok && tc::mbar_wait(&sh->q_full[t], items[t] & 1);
+            if (ok && uses(part[t], 0))
+                score(part[t], t, 0);
         }
-        if (part.active)
-            ++items;
+        tc::mma_commit(&sh->k_empty[ks++ % C::kKs]);
+        for (int i = 0; i < tiles && ok; ++i) {
+            const uint32_t v_slot = vs % C::kVs, v_phase = (vs / C::kVs) & 1;
+            const uint32_t v = smem + C::kVAt + v_slot * C::kOperand;
+            ++vs;
+            ok = tc::mbar_wait(&sh->v_full[v_slot], v_phase) && tc::mbar_wait(&sh->v_ready[v_slot], v_phase);
+            const bool more = i + 1 < tiles;
+            if (more)
+                ok = ok && tc::mbar_wait(&sh->k_full[ks % C::kKs], (ks / C::kKs) & 1);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (uses(part[t], i)) {
+                    // the item before has been read out
+                    if (i == part[t].first && items[t] > 0)
+                        ok = ok && tc::mbar_wait(&sh->o_free[t], (items[t] - 1) & 1);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        ok = ok && tc::mbar_wait(&sh->p_ready[t][h], mine[t] & 1);
+                        if (!ok)
+                            break;
+                        tc::fence_after_sync();
+#pragma unroll
+                        for (int j = 0; j < kTile / 32; ++j)
+                            tc::mma_f16_ts(tmem + C::kOutCols + t * D, tmem + t * kTile + h * (kTile / 2) + 8 * j,
+                                           desc_transposed(v + (h * (kTile / 32) + j) * 2048), out_idesc,
+                                           i > part[t].first || h > 0 || j > 0);
+                        if (h == 0)
+                            tc::mma_commit(&sh->half_done[t]);
+                    }
+                    if (!ok)
+                        break;
+                    ++mine[t];
+                    if (i + 1 == part[t].end)
+                        tc::mma_commit(&sh->o_full[t]);
+                }
+                if (t == 1)
+                    tc::mma_commit(&sh->v_empty[v_slot]);
+                if (more && uses(part[t], i + 1))
+                    score(part[t], t, i + 1);
+            }
+            if (more)
+                tc::mma_commit(&sh->k_empty[ks++ % C::kKs]);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+            items[t] += part[t].active;
     }
     // nothing of this thread's is in flight when it leaves
-    tc::mma_commit(&sh->drain[t]);
-    return tc::mbar_wait(&sh->drain[t], 0) && ok;
+    tc::mma_commit(&sh->drain);
+    return tc::mbar_wait(&sh->drain, 0) && ok;
 }
 
 // ---------------------------------------------------------------------------
@@ -461,7 +482,7 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const uint16_t *v, int64_t v_ld, S
     const uint32_t scores = tmem + t * kTile + lanes, out = tmem + C::kOutCols + t * D + lanes;
     const int my_token = r / c.group, my_head = r - my_token * c.group;
     bool ok = true;
-    uint32_t mine = 0;
+    uint32_t mine = 0, items = 0;  // the row tile's key tiles and items so far
     for (uint32_t n = 0; ok; ++n) {
         const uint32_t slot = n % kItems;
         ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&sh->item_full[slot], (n / kItems) & 1));
@@ -538,9 +559,9 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const uint16_t *v, int64_t v_ld, S
                         sum *= shrink;
                         const bool move = __any_sync(0xFFFFFFFFu, shrink != 1.f);
                         if (move && (i > part.first || h == 1)) {
-                            // the first half's product may be under way (the tile before's is done: its scores came after)
+                            // the first half's product may be under way (the tile before's is: these scores came after it)
                             if (h == 1)
-                                ok = ok && tc::mbar_wait(&sh->pv_done[t][0], mine & 1);
+                                ok = ok && tc::mbar_wait(&sh->half_done[t], mine & 1);
                             __syncwarp();
                             tc::fence_after_sync();
 #pragma unroll 1
@@ -585,7 +606,7 @@ NVFP4_DEVINL bool softmax_role(const Call &c, const uint16_t *v, int64_t v_ld, S
                     tc::mbar_arrive(&sh->p_ready[t][h]);
             }
         }
-        ok = ok && tc::mbar_wait(&sh->pv_done[t][1], (mine - 1) & 1) && tc::mbar_wait(&sh->scanned[slot], (n / kItems) & 1);
+        ok = ok && tc::mbar_wait(&sh->o_full[t], items++ & 1) && tc::mbar_wait(&sh->scanned[slot], (n / kItems) & 1);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok)
             break;
@@ -666,8 +687,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 4; ++i) {
             tc::mbar_init(&sh->k_full[i], 1);
             tc::mbar_init(&sh->v_full[i], 1);
-            tc::mbar_init(&sh->k_empty[i], 2);
-            tc::mbar_init(&sh->v_empty[i], 2);
+            tc::mbar_init(&sh->k_empty[i], 1);
+            tc::mbar_init(&sh->v_empty[i], 1);
             tc::mbar_init(&sh->v_ready[i], 4);
         }
         for (int t = 0; t < 2; ++t) {
@@ -675,15 +696,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(&sh->q_empty[t], 1);
             tc::mbar_init(&sh->s_full[t], 1);
             tc::mbar_init(&sh->o_free[t], 4);
-            tc::mbar_init(&sh->drain[t], 1);
-            for (int h = 0; h < 2; ++h) {
+            tc::mbar_init(&sh->half_done[t], 1);
+            tc::mbar_init(&sh->o_full[t], 1);
+            for (int h = 0; h < 2; ++h)
                 tc::mbar_init(&sh->p_ready[t][h], 4);
-                tc::mbar_init(&sh->pv_done[t][h], 1);
-            }
         }
+        tc::mbar_init(&sh->drain, 1);
         for (int i = 0; i < kItems; ++i) {
             tc::mbar_init(&sh->item_full[i], 1);
-            tc::mbar_init(&sh->item_empty[i], 2 + 8 + 4);  // MMA threads, softmax warps, scan warps
+            tc::mbar_init(&sh->item_empty[i], 1 + 8 + 4);  // MMA thread, softmax warps, scan warps
             tc::mbar_init(&sh->scanned[i], 4);
         }
         tc::fence_mbar_init();
@@ -707,9 +728,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp == kLoadWarp) {
             ok = load_role<D>(c, &q_map, &k_map, &v_map, sh, smem, lane);
             code = kTimeoutLoad;
-        } else if (warp < kAllocWarp) {
+        } else if (warp == kMmaWarp) {
             if (elect_one()) {
-                ok = mma_role<D>(c, sh, smem, tmem, warp - kMmaWarp);
+                ok = mma_role<D>(c, sh, smem, tmem);
                 code = kTimeoutMma;
             }
             __syncwarp();
