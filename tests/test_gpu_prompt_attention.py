@@ -178,6 +178,14 @@ def test_a_token_does_not_depend_on_its_neighbours():
         assert torch.equal(packed[at], alone)
 
 
+@pytest.mark.parametrize("hq,hk,d,causal", [(8, 1, 128, True), (4, 4, 64, False)])
+def test_repeated_calls_give_the_same_bits(hq, hk, d, causal):
+    p = Prompts([3000, 40, 1500], hq, hk, d, seed=6)
+    want = p.run(causal=causal)
+    for _ in range(20):
+        assert torch.equal(p.run(causal=causal), want)
+
+
 def test_offsets_out_of_bounds():
     """Offsets that descend or pass the end: code 44, nothing outside is touched, the others are computed."""
     p = Prompts([100, 60, 40], 4, 2, 64)
