@@ -11,6 +11,7 @@ import ctypes
 import functools
 import os
 import re
+import struct
 import threading
 from dataclasses import dataclass
 
@@ -194,9 +195,9 @@ def load_library():
         lib.nvfp4_rope_pairs.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_int32), ctypes.c_int32,
                                          P]
         lib.nvfp4_rope.restype = i32
-        lib.nvfp4_rope.argtypes = [ctypes.POINTER(RopeArgsC), P]
+        lib.nvfp4_rope.argtypes = [P, P]  # RopeArgsC, packed
         lib.nvfp4_prompt_attention.restype = i32
-        lib.nvfp4_prompt_attention.argtypes = [ctypes.POINTER(PromptAttentionArgsC), P, sz, P]
+        lib.nvfp4_prompt_attention.argtypes = [P, P, sz, P]  # PromptAttentionArgsC, packed
         lib.nvfp4_device_status.restype = i32
         lib.nvfp4_device_status.argtypes = [P, sz, i32, ctypes.POINTER(ctypes.c_uint32), P]
         lib.nvfp4_selftest_wait_timeout.restype = i32
@@ -690,6 +691,22 @@ def _head_rows(t, heads, head_dim, dtypes, what):
 _BF16 = (torch.bfloat16,)
 
 
+def _token_rows(t, tokens, heads, head_dim, dtype, what):
+    """Token stride (elements) of `tokens` such rows of one type."""
+    if t.is_contiguous() and t.dtype is dtype and t.shape == (tokens, heads, head_dim):
+        return heads * head_dim
+    ld = _head_rows(t, heads, head_dim, (dtype,), what)
+    if t.shape[0] != tokens:
+        raise ValueError(f"{what} has {t.shape[0]} tokens, not {tokens}")
+    return ld
+
+
+# Argument blocks of calls that take a few microseconds, field by field as in their ctypes.Structure (making one of
+# those takes longer than the rest of the call).
+_ROPE_ARGS = struct.Struct("@PPqqPPqqPqPqiiiiiiiifi")
+_PROMPT_ARGS = struct.Struct("@PPPqqqPqPqqqiiiiif")
+
+
 def _check_slots(slots, tokens):
     if slots.dtype != torch.int64 or slots.shape != (tokens,) or not slots.is_contiguous():
         raise ValueError(f"slots must be a contiguous int64 [{tokens}], got {slots.dtype} {list(slots.shape)}")
@@ -918,51 +935,51 @@ def nvfp4_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
     q [tokens, n_q_heads, head_dim] and k [tokens, n_k_heads, head_dim] (or None), both bf16 or fp32, token rows may be
     strided; positions int64 [tokens], or [axes, tokens] for a table with several axes.  out: two tensors of the
     inputs' shapes and type, which may be the inputs themselves (in place)."""
-    if q.dim() != 3:
-        raise ValueError(f"q must be [tokens, heads, head_dim], got {list(q.shape)}")
-    tokens, heads, head_dim = q.shape
-    dtype = (q.dtype,)
-    code = _out_code(q.dtype)
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3:
+        raise ValueError(f"q must be [tokens, heads, head_dim], got {list(shape)}")
+    tokens, heads, head_dim = shape
+    code = _out_code(dtype)
     k_heads = 0
     if k is not None:
         if k.dim() != 3:
             raise ValueError(f"k must be [tokens, heads, head_dim], got {list(k.shape)}")
         k_heads = k.shape[1]
     if out is None:
-        out = (_new(stream, tokens, heads, head_dim, dtype=q.dtype, device=q.device),
-               None if k is None else _new(stream, tokens, k_heads, head_dim, dtype=q.dtype, device=q.device))
+        out = (_new(stream, tokens, heads, head_dim, dtype=dtype, device=q.device),
+               None if k is None else _new(stream, tokens, k_heads, head_dim, dtype=dtype, device=q.device))
     q_out, k_out = out
     if (k is None) != (k_out is None):
         raise ValueError("out must hold a tensor for k if and only if k is given")
-    q_ld, q_out_ld = _head_rows(q, heads, head_dim, dtype, "q"), _head_rows(q_out, heads, head_dim, dtype, "out[0]")
-    k_ld = k_out_ld = 0
+    q_ld = _token_rows(q, tokens, heads, head_dim, dtype, "q")
+    q_out_ld = _token_rows(q_out, tokens, heads, head_dim, dtype, "out[0]")
+    k_ptr = k_out_ptr = k_ld = k_out_ld = 0
     if k is not None:
-        k_ld, k_out_ld = _head_rows(k, k_heads, head_dim, dtype, "k"), _head_rows(k_out, k_heads, head_dim, dtype, "out[1]")
-        if k.shape[0] != tokens or k_out.shape[0] != tokens:
-            raise ValueError(f"q has {tokens} tokens, k {k.shape[0]}, out[1] {k_out.shape[0]}")
-    if q_out.shape[0] != tokens:
-        raise ValueError(f"q has {tokens} tokens, out[0] {q_out.shape[0]}")
-    axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if positions.dtype != torch.int64 or positions.dim() not in (1, 2) or positions.shape[-1] != tokens or (
-            tokens > 1 and positions.stride(-1) != 1):
+        k_ld = _token_rows(k, tokens, k_heads, head_dim, dtype, "k")
+        k_out_ld = _token_rows(k_out, tokens, k_heads, head_dim, dtype, "out[1]")
+        k_ptr, k_out_ptr = k.data_ptr(), k_out.data_ptr()
+    at = positions.shape
+    axes = at[0] if len(at) == 2 else 1
+    if positions.dtype is not torch.int64 or len(at) not in (1, 2) or at[-1] != tokens or (
+            not positions.is_contiguous() and tokens > 1 and positions.stride(-1) != 1):
         raise ValueError(f"positions must be int64 [{tokens}] or [axes, {tokens}] with unit stride along the tokens, got "
-                         f"{positions.dtype} {list(positions.shape)}")
+                         f"{positions.dtype} {list(at)}")
     if axes < table.n_axes:
         raise ValueError(f"the table uses {table.n_axes} axes, positions have {axes}")
     pairs = table.pairs
-    if pairs.dtype != torch.uint8 or pairs.dim() != 2 or pairs.shape[1] != 16 or not pairs.is_contiguous():
+    n_pairs = pairs.shape[0]
+    if pairs.dtype is not torch.uint8 or pairs.shape != (n_pairs, 16) or not pairs.is_contiguous():
         raise ValueError(f"the table's pairs must be a contiguous uint8 [n_pairs, 16], got {pairs.dtype} {list(pairs.shape)}")
-    a = RopeArgsC(q.data_ptr(), None if k is None else k.data_ptr(), q_ld, k_ld, q_out.data_ptr(),
-                  None if k is None else k_out.data_ptr(), q_out_ld, k_out_ld, positions.data_ptr(),
-                  positions.stride(0) if axes > 1 else tokens, pairs.data_ptr(), tokens, axes, pairs.shape[0], heads, k_heads,
-                  head_dim, code, 1 if adjacent else 0, 1 if inverse else 0, scale, 0)
-    args = (ctypes.byref(a), _stream_of(q, stream))
+    a = _ROPE_ARGS.pack(q.data_ptr(), k_ptr, q_ld, k_ld, q_out.data_ptr(), k_out_ptr, q_out_ld, k_out_ld, positions.data_ptr(),
+                        positions.stride(0) if axes > 1 else tokens, pairs.data_ptr(), tokens, axes, n_pairs, heads, k_heads,
+                        head_dim, code, 1 if adjacent else 0, 1 if inverse else 0, scale, 0)
+    s = _stream_of(q, stream)
     if (q.is_cuda and q_out.is_cuda and positions.is_cuda and pairs.is_cuda and (k is None or (k.is_cuda and k_out.is_cuda))
             and _one_gpu()):
-        st = load_library().nvfp4_rope(*args)
+        st = load_library().nvfp4_rope(a, s)
     else:
         with _on_device_of("nvfp4_rope", q, q_out, k, k_out, positions, pairs):
-            st = load_library().nvfp4_rope(*args)
+            st = load_library().nvfp4_rope(a, s)
     if st:
         _check(st, "nvfp4_rope")
     return out
@@ -982,35 +999,37 @@ def nvfp4_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, of
     column ranges of a QKV output are); offsets int32 [n_seqs + 1]: where each sequence begins and the last one ends
     (None: one sequence).  scale defaults to head_dim ** -0.5.  Rows of `out` that belong to no sequence are left as
     they are."""
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError(f"q and k must be [tokens, heads, head_dim], got {list(q.shape)} and {list(k.shape)}")
-    total, heads, head_dim = q.shape
+    shape = q.shape
+    if len(shape) != 3 or k.dim() != 3:
+        raise ValueError(f"q and k must be [tokens, heads, head_dim], got {list(shape)} and {list(k.shape)}")
+    total, heads, head_dim = shape
     kv_heads = k.shape[1]
-    q_ld = _head_rows(q, heads, head_dim, _BF16, "q")
-    k_ld = _head_rows(k, kv_heads, head_dim, _BF16, "k")
-    v_ld = _head_rows(v, kv_heads, head_dim, _BF16, "v")
+    q_ld = _token_rows(q, total, heads, head_dim, torch.bfloat16, "q")
+    k_ld = _token_rows(k, total, kv_heads, head_dim, torch.bfloat16, "k")
+    v_ld = _token_rows(v, total, kv_heads, head_dim, torch.bfloat16, "v")
     if out is None:
         out = _new(stream, total, heads, head_dim, dtype=out_dtype, device=q.device)
-    out_ld = _head_rows(out, heads, head_dim, (torch.bfloat16, torch.float32), "out")
-    if k.shape[0] != total or v.shape[0] != total or out.shape[0] != total:
-        raise ValueError(f"q has {total} tokens, k {k.shape[0]}, v {v.shape[0]}, out {out.shape[0]}")
-    n_seqs = 1
+    if out.dtype is not torch.bfloat16 and out.dtype is not torch.float32:
+        _head_rows(out, heads, head_dim, (torch.bfloat16, torch.float32), "out")  # raises
+    code = _out_code(out.dtype)
+    out_ld = _token_rows(out, total, heads, head_dim, out.dtype, "out")
+    n_seqs, off = 1, 0
     if offsets is not None:
         if offsets.dim() != 1 or offsets.shape[0] < 1:
             raise ValueError(f"offsets must be [n_seqs + 1], got {list(offsets.shape)}")
         n_seqs = offsets.shape[0] - 1
-    a = PromptAttentionArgsC(
-        q.data_ptr(), k.data_ptr(), v.data_ptr(), q_ld, k_ld, v_ld, out.data_ptr(), out_ld,
-        None if offsets is None else _device_ints(offsets, torch.int32, (n_seqs + 1,), "offsets"), n_seqs, total, window,
-        heads, kv_heads, head_dim, _out_code(out.dtype), 1 if causal else 0, head_dim ** -0.5 if scale is None else scale)
+        off = _device_ints(offsets, torch.int32, (n_seqs + 1,), "offsets")
+    a = _PROMPT_ARGS.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), q_ld, k_ld, v_ld, out.data_ptr(), out_ld, off, n_seqs, total,
+                          window, heads, kv_heads, head_dim, code, 1 if causal else 0,
+                          head_dim ** -0.5 if scale is None else scale)
     ws, ws_bytes = _buffer(workspace)
-    args = (ctypes.byref(a), ws, ws_bytes, _stream_of(q, stream))
+    s = _stream_of(q, stream)
     if (q.is_cuda and k.is_cuda and v.is_cuda and out.is_cuda and (offsets is None or offsets.is_cuda)
             and (workspace is None or workspace.is_cuda) and _one_gpu()):
-        st = load_library().nvfp4_prompt_attention(*args)
+        st = load_library().nvfp4_prompt_attention(a, ws, ws_bytes, s)
     else:
         with _on_device_of("nvfp4_prompt_attention", q, k, v, out, offsets, workspace):
-            st = load_library().nvfp4_prompt_attention(*args)
+            st = load_library().nvfp4_prompt_attention(a, ws, ws_bytes, s)
     if st:
         _check(st, "nvfp4_prompt_attention")
     return out

@@ -160,3 +160,14 @@ def test_no_tokens():
     q = torch.empty(0, 8, 128, dtype=torch.bfloat16, device=DEV)
     out, _ = g.nvfp4_rope(q, None, torch.empty(0, dtype=torch.int64, device=DEV), table)
     assert out.shape == q.shape
+
+
+def test_many_axes():
+    """More axes than a warp has lanes."""
+    axis = [3, 40, 31, 32, 0, 63, 7, 62]
+    table = g.RopeTable.make(frequencies(8), axis)
+    positions = torch.randint(-5000, 5000, (64, 5))
+    for pairs_first in (16, 24):  # both kernels' heads: 8 pairs of 16 elements, and with elements that are not turned
+        q = rows(5, 3, pairs_first, torch.float32, 12)
+        got = g.nvfp4_rope(q, None, positions.to(DEV), table)[0]
+        check(got, q, angles(table, positions.tolist(), axis), 8)

@@ -144,3 +144,11 @@ def test_python_checks():
                             ((q.transpose(0, 1), k, k), {}, "side by side|tokens"), ((q, k, k), dict(offsets=off), "one CUDA device")):
         with pytest.raises(ValueError, match=match):
             g.nvfp4_prompt_attention(*args, **kw)
+
+
+def test_packed_argument_blocks_match_their_structures():
+    """The blocks that the binding packs have their ctypes.Structure's fields at the same places."""
+    for packed, structure in ((binding._ROPE_ARGS, binding.RopeArgsC), (binding._PROMPT_ARGS, binding.PromptAttentionArgsC)):
+        values = [float(i + 1) if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(structure._fields_)]
+        assert packed.size == ctypes.sizeof(structure)
+        assert packed.pack(*values) == bytes(structure(*values))
