@@ -355,17 +355,37 @@ __global__ void __launch_bounds__(kPrepThreads) skinny_prep_kernel(const uint16_
 // ---------------------------------------------------------------------------
 
 // Output value of row m, token n from the fp32 sums of the matrices.
-template <int NW, bool EPI>
+template <int NW>
 NVFP4_DEVINL void store_out(const Args &a, const float *fac, int n, int64_t m, float s0, float s1)
 {
-    float val = NW == 1 ? s0 * fac[n] : silu_mul(s0 * fac[n], s1 * fac[NTOK + n]);
-    if constexpr (EPI)
-        val = epilogue_value(a.ep, val, n, m);
+    const float val = NW == 1 ? s0 * fac[n] : silu_mul(s0 * fac[n], s1 * fac[NTOK + n]);
     const int64_t idx = (int64_t)n * a.M + m;
     if (a.out_bf16)
         reinterpret_cast<uint16_t *>(a.y)[idx] = f32_to_bf16(val);
     else
         reinterpret_cast<float *>(a.y)[idx] = val;
+}
+
+// EPI: the outputs of row m for every token, from the fp32 sums.
+NVFP4_DEVINL void store_row(const Args &a, const float *fac, int64_t m, const float (&sum)[NTOK])
+{
+    const float bias = epilogue_bias(a.ep, m);
+    float v[NTOK];
+#pragma unroll
+    for (int n = 0; n < NTOK; ++n)
+        v[n] = sum[n] * fac[n] + bias;
+    activate_all(a.ep.act, v, a.N);
+    add_residual(a.ep, v, 0, a.N, m);
+#pragma unroll
+    for (int n = 0; n < NTOK; ++n) {
+        if (n < a.N) {
+            const int64_t idx = (int64_t)n * a.M + m;
+            if (a.out_bf16)
+                reinterpret_cast<uint16_t *>(a.y)[idx] = f32_to_bf16(v[n]);
+            else
+                reinterpret_cast<float *>(a.y)[idx] = v[n];
+        }
+    }
 }
 
 // Split-K bookkeeping of one tile segment, shared by the epilogue threads
@@ -388,11 +408,13 @@ __device__ __noinline__ void publish_segment(const Args &a, const float *fac, co
     const uint32_t total = (uint32_t)a.total, P = (uint32_t)a.P, C = (uint32_t)a.C;
     const int64_t m = (int64_t)tile * BM + r;
     if (whole) {  // uniform across the epilogue threads
-        if (m < a.M)
+        if (EPI && m < a.M)
+            store_row(a, fac, m, v[0]);
+        else if (m < a.M)
 #pragma unroll
             for (int n = 0; n < NTOK; ++n)
                 if (n < a.N)
-                    store_out<NW, EPI>(a, fac, n, m, v[0][n], v[NW - 1][n]);
+                    store_out<NW>(a, fac, n, m, v[0][n], v[NW - 1][n]);
         if (r == 0)
             si->reduce = 0;
         return;
@@ -438,6 +460,22 @@ __device__ __noinline__ void reduce_tile(const Args &a, const float *fac, const 
 #pragma unroll
         for (int mi = 0; mi < NW; ++mi)
             acc[mi] = make_float4(0.f, 0.f, 0.f, 0.f);
+        // EPI: bias and residual on their way beside the partials
+        float bias[4], res[4];
+        if constexpr (EPI) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int64_t m = (int64_t)si.tile * BM + r4 + e;
+                const bool there = m < a.M;
+                bias[e] = there ? epilogue_bias(a.ep, m) : 0.f;
+                res[e] = 0.f;
+                if (a.ep.residual && there) {
+                    const int64_t at = n * a.ep.residual_ld + m;
+                    res[e] = a.ep.residual_bf16 ? bf16_value(static_cast<const uint16_t *>(a.ep.residual)[at])
+                                                : static_cast<const float *>(a.ep.residual)[at];
+                }
+            }
+        }
         for (int b0 = si.b_lo; b0 <= si.b_hi; b0 += kBatch) {
             float4 pv[kBatch][NW];
             float4 *src[kBatch];
@@ -462,12 +500,29 @@ __device__ __noinline__ void reduce_tile(const Args &a, const float *fac, const 
                     }
         }
         const int64_t m0 = (int64_t)si.tile * BM + r4;
+        if constexpr (EPI) {
+            float w[4] = {acc[0].x * fac[n] + bias[0], acc[0].y * fac[n] + bias[1], acc[0].z * fac[n] + bias[2],
+                          acc[0].w * fac[n] + bias[3]};
+            activate_all(a.ep.act, w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (m0 + e >= a.M)
+                    break;
+                const float val = a.ep.residual ? res[e] + w[e] : w[e];
+                const int64_t idx = (int64_t)n * a.M + m0 + e;
+                if (a.out_bf16)
+                    reinterpret_cast<uint16_t *>(a.y)[idx] = f32_to_bf16(val);
+                else
+                    reinterpret_cast<float *>(a.y)[idx] = val;
+            }
+            continue;
+        }
         const float g[4] = {acc[0].x, acc[0].y, acc[0].z, acc[0].w};
         const float h[4] = {acc[NW - 1].x, acc[NW - 1].y, acc[NW - 1].z, acc[NW - 1].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e)
             if (m0 + e < a.M)
-                store_out<NW, EPI>(a, fac, n, m0 + e, g[e], h[e]);
+                store_out<NW>(a, fac, n, m0 + e, g[e], h[e]);
     }
 }
 
@@ -525,11 +580,13 @@ __device__ __noinline__ void ck_epilogue(const Args &a, const float *fac, const 
             }
     }
     const int64_t m = tile * BM + r;
-    if (m < a.M)
+    if (EPI && m < a.M)
+        store_row(a, fac, m, acc[0]);
+    else if (m < a.M)
 #pragma unroll
         for (int n = 0; n < NTOK; ++n)
             if (n < a.N)
-                store_out<NW, EPI>(a, fac, n, m, acc[0][n], acc[NW - 1][n]);
+                store_out<NW>(a, fac, n, m, acc[0][n], acc[NW - 1][n]);
     tc::named_bar_sync(1, kEpiThreads);  // every read of the ranks' buffers is done
     if (et < a.cs)
         tc::mbar_arrive_remote(tc::mapa(ck_free, (uint32_t)et));
@@ -801,6 +858,11 @@ skinny_tc_kernel(const __grid_constant__ CUtensorMap m_codes0, const __grid_cons
         tc::griddep_wait();
         const int mode = load_mode(a);
         const int et = threadIdx.x - kEpiWarp0 * 32;  // 0..127
+        if constexpr (EPI) {
+            int64_t tile = tile_lo;
+            for (int left = n_units, j = j_lo; left > 0; left -= rg.je - j, j = rg.jb, tile += rg.tstep)
+                epilogue_prefetch(a.ep, 0, a.N, tile * BM, BM, a.M, et, kEpiThreads);
+        }
         if (et < NW * NTOK) {
             const int mi = et / NTOK, n = et % NTOK;
             if (FMT == 1) {

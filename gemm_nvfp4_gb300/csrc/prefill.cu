@@ -316,36 +316,32 @@ struct WeightMaps {
     CUtensorMap scales[2];
 };
 
-// EPI: row m of 32 tokens from n0 on, from the accumulators (without TA: two halves of
-// each sum).  Residuals are loaded eight at a time before the stores, which may alias them.
+// EPI: row m of kEpiCols tokens from n0 on, from the accumulators (without TA: two halves of each sum).  Few columns at
+// a time: each tile runs this code once, and much of its time is the instruction cache's.
+constexpr int kEpiCols = 16;
 template <bool TA>
-NVFP4_DEVINL void store_column(const Args &a, const uint32_t (&r)[2][32], float ts, int64_t n0, int64_t m)
+NVFP4_DEVINL void store_column(const Args &a, const uint32_t (&r)[2][kEpiCols], float ts, float bias, int64_t n0, int64_t m)
 {
-    const float bias = epilogue_bias(a.ep, m);
+    float v[kEpiCols];
 #pragma unroll
-    for (int j0 = 0; j0 < 32; j0 += 8) {
-        float res[8];
-        if (a.ep.residual) {
+    for (int j = 0; j < kEpiCols; ++j)
+        v[j] = (TA ? __uint_as_float(r[0][j]) : __uint_as_float(r[0][j]) + __uint_as_float(r[1][j])) * ts + bias;
+    activate_all(a.ep.act, v);
+    add_residual(a.ep, v, n0, a.N, m);
+    const int64_t at = n0 * a.M + m;
+    const int n = a.N - n0 < kEpiCols ? (int)(a.N - n0) : kEpiCols;
+    if (a.out_bf16) {
+        uint16_t *y = reinterpret_cast<uint16_t *>(a.y) + at;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                res[j] = n0 + j0 + j < a.N ? epilogue_residual(a.ep, n0 + j0 + j, m) : 0.f;
-        }
+        for (int j = 0; j < kEpiCols; ++j, y += a.M)
+            if (j < n)
+                *y = f32_to_bf16(v[j]);
+    } else {
+        float *y = reinterpret_cast<float *>(a.y) + at;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t n = n0 + j0 + j;
-            if (n < a.N) {
-                const float sum = TA ? __uint_as_float(r[0][j0 + j])
-                                     : __uint_as_float(r[0][j0 + j]) + __uint_as_float(r[1][j0 + j]);
-                float v = activate(a.ep.act, sum * ts + bias);
-                if (a.ep.residual)
-                    v += res[j];
-                const int64_t idx = n * a.M + m;
-                if (a.out_bf16)
-                    reinterpret_cast<uint16_t *>(a.y)[idx] = f32_to_bf16(v);
-                else
-                    reinterpret_cast<float *>(a.y)[idx] = v;
-            }
-        }
+        for (int j = 0; j < kEpiCols; ++j, y += a.M)
+            if (j < n)
+                *y = v[j];
     }
 }
 
@@ -621,16 +617,37 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
 #pragma unroll
                 for (int mi = 0; mi < NW; ++mi)
                     ts[mi] = FMT == 0 ? __ldg(a.ts[mi]) * 256.0f : 1.0f;
+                const float bias = EPI && mrow < a.M ? epilogue_bias(a.ep, mrow) : 0.f;
                 // a partial segment is the first (slot 0) or last (slot 1) of the
                 // CTA's stream-K range
                 float *slot = a.partial +
                               (size_t)(2 * blockIdx.x + (SPLIT && sg.tile != sk_first_tile(a, blockIdx.x) ? 1 : 0)) *
                                   TN * BM +
                               quarter * 32 + lane;
+                if constexpr (EPI) {
+#pragma unroll 1
+                    for (int c = 0; c < TN / 2 && sn0 + chalf * (TN / 2) + c < a.N; c += kEpiCols) {
+                        const int col = chalf * (TN / 2) + c;
+                        const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + col;
+                        uint32_t r[2][kEpiCols];
+                        tc::tmem_ld_32x32b_x16(taddr, r[0]);
+                        if (!TA)
+                            tc::tmem_ld_32x32b_x16(taddr + TN, r[1]);
+                        tc::tmem_ld_wait();
+                        if (SPLIT && split_seg) {
+#pragma unroll
+                            for (int j = 0; j < kEpiCols; ++j)
+                                slot[(size_t)(col + j) * BM] = __uint_as_float(r[0][j]);
+                        } else if (mrow < a.M) {
+                            store_column<TA>(a, r, ts[0], bias, (int64_t)sn0 + col, mrow);
+                        }
+                        __syncwarp();
+                    }
+                }
                 // TA: only column chunks holding at least one real token
                 // (warp-uniform; a runtime bound also keeps this loop rolled)
 #pragma unroll 1
-                for (int cc = 0; cc < TN / 64 && (!TA || sn0 + chalf * (TN / 2) + cc * 32 < a.N); ++cc) {
+                for (int cc = EPI ? TN / 64 : 0; cc < TN / 64 && (!TA || sn0 + chalf * (TN / 2) + cc * 32 < a.N); ++cc) {
                     const int col = chalf * (TN / 2) + cc * 32;
                     const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + col;
                     // two accumulators: gate and up, or (one matrix) K steps 0-1 and 2-3
@@ -643,8 +660,6 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             slot[(size_t)(col + j) * BM] = __uint_as_float(r[0][j]);
-                    } else if (EPI && mrow < a.M) {
-                        store_column<TA>(a, r, ts[0], (int64_t)sn0 + col, mrow);
                     } else if (mrow < a.M) {
 #pragma unroll
                         for (int j = 0; j < 32; ++j) {
@@ -678,6 +693,9 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
                     tc::mbar_arrive(tmem_empty);
             }
         };
+        if constexpr (EPI && !SPLIT)
+            epilogue_prefetch(a.ep, c0.n0, c0.n0 + TN < a.N ? c0.n0 + TN : a.N, m0, BM, a.M, threadIdx.x - kFirstDqWarp * 32,
+                              kDqWarps * 32);
         SegCursor dcur = c0;  // the dequantisers' stage cursor
         if constexpr (TMAC && FMT == 1) {
             // FP6 codes from the TMA ring; the scale byte of a row (one per
@@ -915,14 +933,25 @@ template <bool EPI>
 NVFP4_DEVINL void store_rows4(const Args &a, int64_t n, int64_t mq, float4 v)
 {
     if constexpr (EPI) {
-        if (mq < a.M)
-            v.x = epilogue_value(a.ep, v.x, n, mq);
-        if (mq + 1 < a.M)
-            v.y = epilogue_value(a.ep, v.y, n, mq + 1);
-        if (mq + 2 < a.M)
-            v.z = epilogue_value(a.ep, v.z, n, mq + 2);
-        if (mq + 3 < a.M)
-            v.w = epilogue_value(a.ep, v.w, n, mq + 3);
+        const int rows = a.M - mq < 4 ? (int)(a.M - mq) : 4;
+        float w[4] = {v.x, v.y, v.z, v.w}, r[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            w[e] += e < rows ? epilogue_bias(a.ep, mq + e) : 0.f;
+            r[e] = 0.f;
+            if (a.ep.residual && e < rows) {
+                const int64_t at = n * a.ep.residual_ld + mq + e;
+                r[e] = a.ep.residual_bf16 ? bf16_value(static_cast<const uint16_t *>(a.ep.residual)[at])
+                                          : static_cast<const float *>(a.ep.residual)[at];
+            }
+        }
+        activate_all(a.ep.act, w);
+        if (a.ep.residual) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = r[e] + w[e];
+        }
+        v = make_float4(w[0], w[1], w[2], w[3]);
     }
     const int64_t idx = n * a.M + mq;
     if ((a.M & 3) == 0 && mq + 3 < a.M) {  // 16- / 8-byte aligned, all in range
