@@ -67,8 +67,38 @@ NVFP4_DEVINL float epilogue_bias(const Epilogue &e, int64_t m)
     return e.bias_bf16 ? bf16_value(__ldg(static_cast<const uint16_t *>(e.bias) + m)) : __ldg(static_cast<const float *>(e.bias) + m);
 }
 
-// Adds the residual of row m to the values of tokens n0 .. n0 + N - 1, below n_end: every load before the first use (and
-// before the stores, whose memory may be the residual's: ordinary loads).
+// The residual of row m of tokens n0 .. n0 + N - 1 (below M and n_end), as it is stored: ordinary loads, whose memory may
+// be the output's, and all before the first use.
+template <int N>
+NVFP4_DEVINL void load_residual(const Epilogue &e, uint32_t (&r)[N], int64_t n0, int64_t n_end, int64_t m, int64_t M)
+{
+    if (!e.residual || m >= M)
+        return;
+    const int64_t at = n0 * e.residual_ld + m;
+    if (e.residual_bf16) {
+        const uint16_t *p = static_cast<const uint16_t *>(e.residual) + at;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            r[j] = n0 + j < n_end ? p[j * e.residual_ld] : 0u;
+    } else {
+        const uint32_t *p = static_cast<const uint32_t *>(e.residual) + at;
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            r[j] = n0 + j < n_end ? p[j * e.residual_ld] : 0u;
+    }
+}
+
+template <int N>
+NVFP4_DEVINL void add_residual(const Epilogue &e, float (&v)[N], const uint32_t (&r)[N])
+{
+    if (!e.residual)
+        return;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+        v[j] = __uint_as_float(e.residual_bf16 ? r[j] << 16 : r[j]) + v[j];
+}
+
+// Adds the residual of row m to the values of tokens n0 .. n0 + N - 1, below n_end: every load before the first use.
 template <int N>
 NVFP4_DEVINL void add_residual(const Epilogue &e, float (&v)[N], int64_t n0, int64_t n_end, int64_t m)
 {
