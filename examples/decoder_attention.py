@@ -1,14 +1,15 @@
-"""The attention half of a decoder layer on the library: QKV product, KV-cache
-append, attention over the pages, O product.
+"""The attention half of a decoder layer on the library: QKV product with its
+bias, rotary positions, KV-cache append, attention (over the prompt itself, or
+over the pages), O product onto the residual stream.
 
     python examples/decoder_attention.py [--format e4m3|nvfp4]
 
 Random NVFP4 weights of the 9B-class layer (32 query and 8 KV heads of 128)
-serve three sequences the way a server does: a prefill in chunks, decode steps
+serve three sequences the way a server does: a prefill in two chunks (the first
+attends to the prompt's own K and V, the second to the pages), decode steps
 replayed from one CUDA graph, and a speculative verify of a token tree.  Each
 stage prints how far its attention output is from the fp64 definition on the
-cache's values.  (No rotary embedding: the library has none; a program that
-needs it rotates q and k between the QKV product and the append.)
+values that it attends to.
 """
 from __future__ import annotations
 
@@ -35,10 +36,10 @@ class PagedSequences:
         self.table = pages.view(n_seqs, self.width).to(device)
         self.lens = torch.zeros(n_seqs, dtype=torch.int32, device=device)
 
-    def slots(self, new: int) -> torch.Tensor:
-        """Slots of the `new` tokens that follow each sequence's last one, [n_seqs * new]."""
+    def next(self, new: int) -> tuple[torch.Tensor, torch.Tensor]:
+        """Positions and slots of the `new` tokens that follow each sequence's last one, [n_seqs * new]."""
         at = self.lens[:, None].long() + torch.arange(new, device=self.lens.device)
-        return (self.table.long().gather(1, at // PAGE) * PAGE + at % PAGE).flatten()
+        return at.flatten(), (self.table.long().gather(1, at // PAGE) * PAGE + at % PAGE).flatten()
 
 
 class Attention:
@@ -48,7 +49,9 @@ class Attention:
         gen = torch.Generator(device).manual_seed(seed)
         rand = lambda *s: torch.randn(*s, device=device, generator=gen) * 0.02  # noqa: E731
         self.qkv = g.nvfp4_quantize(rand((HQ + 2 * HK) * D, HIDDEN))
+        self.qkv_bias = rand((HQ + 2 * HK) * D).to(torch.bfloat16)
         self.o = g.nvfp4_quantize(rand(HIDDEN, HQ * D))
+        self.rope = g.RopeTable.make([1e6 ** (-2 * i / D) for i in range(D // 2)], device=device)
         self.workspaces: dict = {}
 
     def workspace(self, key, need: int, device) -> torch.Tensor:
@@ -56,36 +59,43 @@ class Attention:
             self.workspaces[key] = torch.zeros(need, dtype=torch.uint8, device=device)
         return self.workspaces[key]
 
-    def product(self, x, w):
-        n = x.shape[0]
-        op = g.NVFP4_OP_GEMV_SKINNY if n <= 16 else g.NVFP4_OP_GEMM_PREFILL
-        call = g.nvfp4_gemv_skinny if n <= 16 else g.nvfp4_gemm_prefill
-        ws = self.workspace((op, w.M), g.nvfp4_workspace_bytes(op, n, w.M, w.K), x.device)
-        return call(x, w, out_dtype=torch.bfloat16, workspace=ws)
+    def product(self, x, w, **epilogue):
+        n = x.shape[0]  # few tokens: a workspace of their own, with counters that other calls must not touch
+        ws = self.workspace((w.M, n <= 16), g.nvfp4_workspace_bytes(g.NVFP4_OP_GEMM_PREFILL, n, w.M, w.K), x.device)
+        return g.nvfp4_gemm_epilogue(x, w, out_dtype=torch.bfloat16, workspace=ws, **epilogue)
 
-    def __call__(self, x, seqs: PagedSequences, new: int, slots, lens, tree=None):
-        """x [n_seqs * new, HIDDEN]; lens counts the new tokens.  Returns (y, q, attention output)."""
-        qkv = self.product(x, self.qkv).unflatten(1, (HQ + 2 * HK, D))
+    def __call__(self, x, seqs: PagedSequences, new: int, positions, slots, lens, tree=None, prompt=None):
+        """x [n_seqs * new, HIDDEN], the residual stream; lens counts the new tokens; prompt: the offsets of sequences
+        that begin with these tokens.  Returns (y, (q, k, v) after the rotation, attention output)."""
+        qkv = self.product(x, self.qkv, bias=self.qkv_bias).unflatten(1, (HQ + 2 * HK, D))
         q, k, v = qkv[:, :HQ], qkv[:, HQ:HQ + HK], qkv[:, HQ + HK:]
+        g.nvfp4_rope(q, k, positions, self.rope, out=(q, k))
         ws = self.workspace("attention", g.nvfp4_paged_attention_workspace_bytes(seqs.cache, q, len(lens), new), x.device)
         g.nvfp4_kv_append(seqs.cache, k, v, slots, workspace=ws)
-        a = g.nvfp4_paged_attention(q, seqs.cache, seqs.table, lens, max_q_len=new, tree=tree, workspace=ws)
-        return self.product(a.flatten(1), self.o), q, a
+        if prompt is not None:
+            a = g.nvfp4_prompt_attention(q, k, v, prompt, workspace=ws)
+        else:
+            a = g.nvfp4_paged_attention(q, seqs.cache, seqs.table, lens, max_q_len=new, tree=tree, workspace=ws)
+        return self.product(a.flatten(1), self.o, residual=x), (q, k, v), a
 
 
-def error(seqs, q, a, new, lens, tree=None) -> float:
-    """Relative distance of attention outputs from softmax(q K^T / sqrt(D)) V in fp64 on the cached values."""
+def error(seqs, qkv, a, new, lens, tree=None, prompt=False) -> float:
+    """Relative distance of attention outputs from softmax(q K^T / sqrt(D)) V in fp64, on the cached values or (prompt)
+    on the new tokens' own."""
     off = total = 0.0
     for b, n in enumerate(lens.tolist()):
         at = torch.arange(n, device=a.device)
-        slots = seqs.table[b].long()[at // PAGE] * PAGE + at % PAGE
-        k, v = (x.double().repeat_interleave(HQ // HK, 1).transpose(0, 1) for x in g.nvfp4_kv_read(seqs.cache, slots))
         rows = slice(b * new, (b + 1) * new)
+        if prompt:
+            kv = (t[rows] for t in qkv[1:])
+        else:
+            kv = g.nvfp4_kv_read(seqs.cache, seqs.table[b].long()[at // PAGE] * PAGE + at % PAGE)
+        k, v = (t.double().repeat_interleave(HQ // HK, 1).transpose(0, 1) for t in kv)
         past, i = n - new, torch.arange(new, device=a.device)[:, None]
         see = at <= past + i
         if tree is not None:
             see = (at < past) | ((tree[rows, None] >> (at - past).clamp(min=0)) & 1 == 1)
-        z = q[rows].double().transpose(0, 1) @ k.transpose(1, 2) / D ** 0.5
+        z = qkv[0][rows].double().transpose(0, 1) @ k.transpose(1, 2) / D ** 0.5
         want = (torch.softmax(z.masked_fill(~see, float("-inf")), -1) @ v).transpose(0, 1)
         off += float((a[rows].double() - want).square().sum())
         total += float(want.square().sum())
@@ -105,33 +115,37 @@ def main(argv=None) -> dict:
 
     # prefill: 400 tokens of each sequence in two chunks
     for chunk in (250, 150):
-        slots = seqs.slots(chunk)
+        positions, slots = seqs.next(chunk)
+        first = chunk == 250
+        prompt = torch.arange(n_seqs + 1, dtype=torch.int32, device=dev) * chunk if first else None
         seqs.lens += chunk
-        _, q, a = layer(rand(n_seqs * chunk), seqs, chunk, slots, seqs.lens)
-        errors[f"prefill chunk of {chunk}"] = error(seqs, q, a, chunk, seqs.lens)
+        _, qkv, a = layer(rand(n_seqs * chunk), seqs, chunk, positions, slots, seqs.lens, prompt=prompt)
+        errors[f"prefill chunk of {chunk}"] = error(seqs, qkv, a, chunk, seqs.lens, prompt=first)
 
-    # decode: one captured step, replayed; lengths and slots are device buffers that change between replays
-    x, slots = rand(n_seqs), seqs.slots(1)
+    # decode: one captured step, replayed; lengths, positions and slots are device buffers that change between replays
+    x, (positions, slots) = rand(n_seqs), seqs.next(1)
     seqs.lens += 1
-    layer(x, seqs, 1, slots, seqs.lens)  # warm-up: workspaces are there before the capture
+    layer(x, seqs, 1, positions, slots, seqs.lens)  # warm-up: workspaces are there before the capture
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        y, q, a = layer(x, seqs, 1, slots, seqs.lens)
+        y, qkv, a = layer(x, seqs, 1, positions, slots, seqs.lens)
     for _ in range(8):
         x.copy_(rand(n_seqs))
-        slots.copy_(seqs.slots(1))
+        for buffer, value in zip((positions, slots), seqs.next(1)):
+            buffer.copy_(value)
         seqs.lens += 1
         graph.replay()
-        errors["decode"] = max(errors.get("decode", 0.0), error(seqs, q, a, 1, seqs.lens))
+        errors["decode"] = max(errors.get("decode", 0.0), error(seqs, qkv, a, 1, seqs.lens))
 
     # verify: the last token and a tree of drafts: 1 and 2 follow 0, 3 follows 1, 4 follows 2
-    words = [0b00001, 0b00011, 0b00101, 0b01011, 0b10101]
+    words, depth = [0b00001, 0b00011, 0b00101, 0b01011, 0b10101], [0, 1, 1, 2, 2]
     tree = torch.tensor(words * n_seqs, device=dev)
-    slots = seqs.slots(5)
+    _, slots = seqs.next(5)
+    positions = (seqs.lens[:, None].long() + torch.tensor(depth, device=dev)).flatten()
     lens = seqs.lens + 5
-    _, q, a = layer(rand(5 * n_seqs), seqs, 5, slots, lens, tree=tree)
-    errors["verify of a tree of 5"] = error(seqs, q, a, 5, lens, tree)
+    _, qkv, a = layer(rand(5 * n_seqs), seqs, 5, positions, slots, lens, tree=tree)
+    errors["verify of a tree of 5"] = error(seqs, qkv, a, 5, lens, tree)
 
     assert g.nvfp4_device_status(layer.workspaces["attention"]) == (g.NVFP4_OK, 0)
     for stage, e in errors.items():
