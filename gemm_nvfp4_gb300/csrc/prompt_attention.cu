@@ -10,8 +10,8 @@
 // its softmax.  Warps by role:
 //
 //   warps 0-3, 4-7  softmax of row tile 0 and 1, a row to a thread: scores come from tensor
-//                   memory, the weights P go back there in bf16 as the A operand of the second product,
-//                   over the scores.  A row's reference (an estimate of its largest score) moves only where a
+//                   memory, the weights P go back there in bf16 as the A operand of the second product
+//                   (heads of 128: over the scores).  A row's reference (an estimate of its largest score) moves only where a
 //                   weight would exceed 2^15, so that the sums so far are hardly ever multiplied.
 //   warp 8          finds the items and loads Q, K and V by TMA.
 //   warp 9          MMA issue of both row tiles.
@@ -25,10 +25,11 @@
 //
 // Measured on one GB300: 16384 tokens (40 and 8 heads of 128, causal, 2.75 TFLOP) 1.70 ms, 1.62 PFLOP/s, 0.83 of the
 // measured bf16 rate; 24 packed prompts of 19 to 2500 tokens (32 and 8 heads) 136 us, 0.56 of it; 8191 tokens in a
-// window of 1024 (16 and 4 heads of 64) 57 us, 5 images of 577 to 2305 tokens (16 heads of 64) 65 us.
+// window of 1024 (16 and 4 heads of 64) 57 us, 5 images of 577 to 2305 tokens (16 heads of 64) 62 us.
 // For a key tile of 256 rows and heads of 128 the MMAs take 2048 clocks and the whole 2800: after each S the
 // MMA thread stands still until the pipe has come to it, and some 130 clocks longer before the next product begins.  With
-// heads of 64 the MMAs would take 1024 and the exponentials as much; 2400 go by, half of them in waits for the other side.
+// heads of 64 the MMAs would take 1300 and the exponentials 1024; 2300 go by: the softmax warps, two to a scheduler, issue in
+// half of the clocks and wait for their own results in most others.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -82,7 +83,10 @@ struct Cfg {
     static constexpr int kKs = D == 128 ? 2 : 4, kVs = D == 128 ? 3 : 4;
     static constexpr int kKAt = 2 * kOperand, kVAt = kKAt + kKs * kOperand, kBarAt = kVAt + kVs * kOperand;
     static constexpr int kSmem = kBarAt + kSharedBytes;
-    static constexpr int kOutCols = 2 * kTile;  // of tensor memory, behind the scores
+    // Columns of tensor memory: scores from 0, and behind them the weights, where they fit (else over the scores), and the sums.
+    static constexpr bool kApart = 2 * (kTile + kTile / 2 + D) <= 512;
+    static constexpr int kWeightCols = kApart ? 2 * kTile : 0, kWeightStep = kApart ? kTile / 2 : kTile;
+    static constexpr int kOutCols = kApart ? 3 * kTile : 2 * kTile;
     static_assert(kSmem <= 227 * 1024, "shared memory");
 };
 
@@ -105,7 +109,7 @@ struct Item {
 
 struct Shared {
     uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], v_ready[4];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2][2], sums_ready[2], o_full[2], o_free[2], drain;
+    uint64_t q_full[2], q_empty[2], s_full[2], p_ready[2][2], sums_ready[2], o_full[2], o_free[2], s_free[2], pv_done[2], drain;
     uint64_t item_full[kItems], item_empty[kItems], scanned[kItems];
     Item item[kItems];
     uint32_t bad[kItems];                         // whether the item has bad keys
@@ -427,6 +431,122 @@ NVFP4_DEVINL bool mma_role(const Call &c, Shared *sh, uint32_t smem, uint32_t tm
     return wait(&sh->drain, 0) && ok;
 }
 
+// The same where the weights have columns of their own (heads of 64): a row tile's next scores are made as soon as its
+// softmax has read the last ones, in the order
+//     S0(s+1) PV1(s-1) S1(s+1) PV0(s)
+// of key tiles s, on through all items.  The scores are not waited for at once, so that one commit tells of them and of the
+// other row tile's sums: two stops a step instead of four.  5 images of 577 to 2305 tokens 65 -> 62 us (with four stops 64), a
+// window of 1024 57.6 -> 57.2.
+template <int D>
+NVFP4_DEVINL bool mma_apart_role(const Call &c, Shared *sh, uint32_t smem, uint32_t tmem)
+{
+    using C = Cfg<D>;
+    constexpr uint32_t score_idesc = tc::idesc_f16kind(kTile, kTile, 1);
+    constexpr uint32_t out_idesc = tc::idesc_f16kind(kTile, D, 1) | 1u << 16;  // B transposed
+    // of a step, for row tile t: bit 3 t that it uses the keys, 3 t + 1 that they are its first, 3 t + 2 its last
+    uint32_t flags[3] = {0, 0, 0};  // of the steps before the last one, of the last one, and of the next one
+    uint32_t items[2] = {0, 0}, scored[2] = {0, 0}, summed[2] = {0, 0}, outs[2] = {0, 0};  // of the row tiles, so far
+    bool ok = true;
+    const auto scores = [&](int t, uint32_t step, uint32_t f) {
+        f >>= 3 * t;
+        if (!(f & 1))
+            return;
+        ok = ok && (scored[t] == 0 || wait(&sh->s_free[t], (scored[t] - 1) & 1));
+        ++scored[t];
+        if (f & 2)
+            ok = ok && wait(&sh->q_full[t], items[t]++ & 1);
+        if (!ok)
+            return;
+        tc::fence_after_sync();
+        const uint32_t k = row_desc(smem + C::kKAt + (step % C::kKs) * C::kOperand), q = row_desc(smem + t * C::kOperand);
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+            const uint32_t at = ((d / 4) * (kTile * 128) + (d % 4) * 32) >> 4;
+            tc::mma_bf16_ss(tmem + t * kTile, desc(q + at), desc(k + at), score_idesc, d > 0);
+        }
+    };
+    const auto sums = [&](int t, uint32_t step, uint32_t f) {
+        f >>= 3 * t;
+        if (!(f & 1))
+            return;
+        const uint32_t v_slot = step % C::kVs, v_phase = (step / C::kVs) & 1;
+        const uint32_t v = column_desc(smem + C::kVAt + v_slot * C::kOperand);
+        ok = ok && wait(&sh->v_full[v_slot], v_phase) && wait(&sh->v_ready[v_slot], v_phase);
+        // the item before has been read out
+        if (f & 2 && outs[t]++ > 0)
+            ok = ok && wait(&sh->o_free[t], outs[t] & 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            ok = ok && wait(&sh->p_ready[t][h], summed[t] & 1);
+            if (!ok)
+                return;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int j = 0; j < kTile / 32; ++j)
+                tc::mma_f16_ts(tmem + C::kOutCols + t * D, tmem + C::kWeightCols + t * C::kWeightStep + h * (kTile / 4) + 8 * j,
+                               desc(v + ((h * (kTile / 32) + j) * 2048 >> 4)), out_idesc, !(f & 2) || h > 0 || j > 0);
+        }
+        ++summed[t];
+    };
+    const auto commit = [&](int t, uint32_t fs, uint32_t fp) {  // scores of t, and sums of the other
+        fs >>= 3 * t;
+        fp >>= 3 * (1 - t);
+        if (!ok)
+            return;
+        if (fs & 1)
+            tc::mma_commit(&sh->s_full[t]);
+        if (fp & 1)
+            tc::mma_commit(&sh->pv_done[1 - t]);
+        if ((fs & 5) == 5)
+            tc::mma_commit(&sh->q_empty[t]);
+        if ((fp & 5) == 5)
+            tc::mma_commit(&sh->o_full[1 - t]);
+    };
+    Item it;
+    int tile = 0, tiles = 0, drain = 0;
+    uint32_t n = 0;
+#pragma unroll 1
+    for (uint32_t step = 0; ok && drain < 2; ++step) {  // the next one
+        if (drain == 0 && tile == tiles) {
+            const uint32_t slot = n % kItems;
+            if (!(ok = wait(&sh->item_full[slot], (n / kItems) & 1)))
+                break;
+            it = sh->item[slot];
+            tc::mbar_arrive(&sh->item_empty[slot]);
+            ++n;
+            tile = 0;
+            tiles = it.len ? it.tiles() : 0;
+        }
+        flags[2] = 0;
+        const bool more = drain == 0 && tiles > 0;
+        if (more) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                if (it.uses(t, tile))
+                    flags[2] |= (1u | (tile == it.first[t] ? 2u : 0u) | (tile + 1 == it.end[t] ? 4u : 0u)) << 3 * t;
+            ++tile;
+            ok = wait(&sh->k_full[step % C::kKs], (step / C::kKs) & 1);
+        } else {
+            ++drain;
+        }
+        scores(0, step, flags[2]);
+        sums(1, step - 2, flags[0]);
+        commit(0, flags[2], flags[0]);
+        if (step >= 2 && ok)
+            tc::mma_commit(&sh->v_empty[(step - 2) % C::kVs]);
+        scores(1, step, flags[2]);
+        sums(0, step - 1, flags[1]);
+        commit(1, flags[2], flags[1]);
+        if (more && ok)
+            tc::mma_commit(&sh->k_empty[step % C::kKs]);
+        flags[0] = flags[1];
+        flags[1] = flags[2];
+    }
+    // nothing of this thread's is in flight when it leaves
+    tc::mma_commit(&sh->drain);
+    return wait(&sh->drain, 0) && ok;
+}
+
 // ---------------------------------------------------------------------------
 // Helper warps
 // ---------------------------------------------------------------------------
@@ -723,10 +843,13 @@ struct RowState {
     float top, sum;
 };
 
-// Weights of a tile's keys.  signals: of one lane of each warp.  begun: the row has sums already.
+// Weights of a tile's keys.  signals: of one lane of each warp.  begun: the row has sums already.  mine: the row tile's key
+// tiles before.  False if a wait ran out.
 template <int D>
-NVFP4_DEVINL void tile_weights(Shared *sh, int t, uint32_t scores, uint32_t out, bool signals, bool begun, float f, RowState &row)
+NVFP4_DEVINL bool tile_weights(Shared *sh, int t, uint32_t scores, uint32_t weights, uint32_t out, bool signals, bool begun,
+                               uint32_t mine, float f, RowState &row)
 {
+    bool ok = true;
     uint32_t s[4][32];  // first the largest
 #pragma unroll
     for (int q = 0; q < 4; ++q)
@@ -735,6 +858,12 @@ NVFP4_DEVINL void tile_weights(Shared *sh, int t, uint32_t scores, uint32_t out,
 #pragma unroll
     for (int q = 0; q < 4; ++q)
         settle(s[q]);
+    if (Cfg<D>::kApart) {
+        tc::fence_before_sync();
+        __syncwarp();
+        if (signals)
+            tc::mbar_arrive(&sh->s_free[t]);
+    }
     float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
@@ -743,6 +872,10 @@ NVFP4_DEVINL void tile_weights(Shared *sh, int t, uint32_t scores, uint32_t out,
             m[q] = max3(m[q], __uint_as_float(s[q][j]), __uint_as_float(s[q][j + 1]));
     }
     const float largest = max3(fmaxf(m[0], m[1]), m[2], m[3]) * f;
+    if (Cfg<D>::kApart && mine > 0) {
+        ok = __all_sync(0xFFFFFFFFu, tc::mbar_wait(&sh->pv_done[t], (mine - 1) & 1));
+        tc::fence_after_sync();
+    }
     const bool over = largest - row.top > kSlack;  // (true for the first reference, false for a NaN)
     if (__builtin_expect(__any_sync(0xFFFFFFFFu, over), 0)) {
         // move the row's reference, and with it what was summed up (the tile before's products are done: these
@@ -770,7 +903,7 @@ NVFP4_DEVINL void tile_weights(Shared *sh, int t, uint32_t scores, uint32_t out,
                 l2[j & 1] = add2(l2[j & 1], pack2(a, b));
                 p[j] = f32x2_to_bf16x2(a, b);
             }
-            tc::tmem_st_32x32b_x16(scores + 16 * q, p);
+            tc::tmem_st_32x32b_x16(weights + 16 * q, p);
         }
         const float2 l = unpack2(add2(l2[0], l2[1]));
         row.sum += l.x + l.y;
@@ -780,6 +913,7 @@ NVFP4_DEVINL void tile_weights(Shared *sh, int t, uint32_t scores, uint32_t out,
         if (signals)
             tc::mbar_arrive(&sh->p_ready[t][h]);
     }
+    return ok;
 }
 
 template <int D>
@@ -816,7 +950,10 @@ NVFP4_DEVINL bool softmax_role(const Call &c, Shared *sh, uint32_t tmem, int tid
             tc::fence_after_sync();
             if (__builtin_expect(!__all_sync(0xFFFFFFFFu, c.flip == 0 && key0 >= lo && key0 + kTile <= hi), 0))
                 mask_scores(scores, lo - key0, hi - key0, c.flip);
-            tile_weights<D>(sh, t, scores, out, r % 32 == 0, i > first, c.factor, row);
+            ok = tile_weights<D>(sh, t, scores, tmem + C::kWeightCols + t * C::kWeightStep + lanes, out, r % 32 == 0, i > first,
+                                 mine, c.factor, row);
+            if (!ok)
+                break;
         }
         if (end > 0 && ok) {
             // (the helper warps have read the item before's sums)
@@ -860,6 +997,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(&sh->o_free[t], 4);
             tc::mbar_init(&sh->sums_ready[t], 4);
             tc::mbar_init(&sh->o_full[t], 1);
+            tc::mbar_init(&sh->s_free[t], 4);
+            tc::mbar_init(&sh->pv_done[t], 1);
             for (int h = 0; h < 2; ++h)
                 tc::mbar_init(&sh->p_ready[t][h], 4);
         }
@@ -892,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             code = kTimeoutLoad;
         } else if (warp == kMmaWarp) {
             if (elect_one()) {
-                ok = mma_role<D>(c, sh, smem, tmem);
+                ok = C::kApart ? mma_apart_role<D>(c, sh, smem, tmem) : mma_role<D>(c, sh, smem, tmem);
                 code = kTimeoutMma;
             }
             __syncwarp();
@@ -920,7 +1059,7 @@ int check_args(const nvfp4_prompt_attention_args *a)
     if (!a || a->n_seqs < 0 || a->total < 0 || a->window < 0)
         return NVFP4_ERR_INVALID_ARG;
     if ((a->out_dtype != NVFP4_OUT_F32 && a->out_dtype != NVFP4_OUT_BF16) || (a->causal != 0 && a->causal != 1) ||
-        (a->window > 0 && !a->causal) || !std::isfinite(a->scale) || (!a->offsets && a->n_seqs != 1))
+        (a->window > 0 && !a->causal) || !std::isfinite(a->scale * 1.4426950408889634f) || (!a->offsets && a->n_seqs != 1))
         return NVFP4_ERR_INVALID_ARG;
     if (a->head_dim != 64 && a->head_dim != 128)
         return NVFP4_ERR_UNSUPPORTED_SHAPE;
