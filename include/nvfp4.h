@@ -649,7 +649,7 @@ typedef struct {
     int32_t head_dim;
     int32_t out_dtype;          /* nvfp4_out_dtype */
     int32_t causal;             /* 0 or 1 */
-    float scale;                /* finite */
+    float scale;                /* finite, as scale * log2(e) is */
 } nvfp4_prompt_attention_args;
 
 int nvfp4_prompt_attention(const nvfp4_prompt_attention_args *args, void *workspace, size_t workspace_bytes,

@@ -107,7 +107,8 @@ def test_prompt_attention_refuses_bad_arguments(lib):
     for kw in (dict(q=None), dict(k=None), dict(v=None), dict(out=None), dict(q=FAKE + 8), dict(k=FAKE + 8), dict(v=FAKE + 2),
                dict(out=FAKE + 8), dict(offsets=FAKE + 2), dict(offsets=None), dict(q_ld=4088), dict(k_ld=1016), dict(v_ld=1028),
                dict(out_ld=0), dict(q_ld=1 << 40), dict(n_seqs=-1), dict(total=-1), dict(window=-1), dict(window=4, causal=0),
-               dict(causal=2), dict(out_dtype=2), dict(scale=math.nan), dict(scale=-math.inf), dict(ws=FAKE + 8, wsb=256)):
+               dict(causal=2), dict(out_dtype=2), dict(scale=math.nan), dict(scale=-math.inf), dict(scale=3e38),
+               dict(ws=FAKE + 8, wsb=256)):
         assert run(**kw) == BAD, kw
     for kw in (dict(head_dim=96), dict(head_dim=0), dict(n_q_heads=12), dict(n_q_heads=0), dict(n_kv_heads=0), dict(n_seqs=65536),
                dict(n_q_heads=129, n_kv_heads=1), dict(total=1 << 20)):
