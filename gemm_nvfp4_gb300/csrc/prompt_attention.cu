@@ -58,7 +58,7 @@ static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= kThreads * kLaunchRegs,
               "setmaxnreg would wait for registers that nobody gives back");
 constexpr int kItems = 4;      // items that the load warp may be ahead
 constexpr int kMostMixed = 8;  // tiles of an item in which rows see different keys: at most 6
-constexpr int kSharedBytes = 3072;
+constexpr int kSharedBytes = 3 * 1024;
 // A row's reference is 2^kHeadroom below its largest weight when it moves, and moves when one exceeds 2^kSlack.
 constexpr float kHeadroom = 7.f, kSlack = 15.f;
 
