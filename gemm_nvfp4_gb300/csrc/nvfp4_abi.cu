@@ -107,8 +107,8 @@ int run_products(const uint16_t *x, int64_t N, int64_t M, int64_t K, const uint8
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
-// Checks an epilogue of an [N][M] output, and makes the kernels' form of it.
-int make_epilogue(const nvfp4_epilogue *e, int64_t N, int64_t M, Epilogue *out)
+// Checks an epilogue of the [N][M] output y, and makes the kernels' form of it.
+int make_epilogue(const nvfp4_epilogue *e, int64_t N, int64_t M, const void *y, int out_dtype, Epilogue *out)
 {
     if (!e || e->activation < NVFP4_ACT_NONE || e->activation > NVFP4_ACT_RELU2)
         return NVFP4_ERR_INVALID_ARG;
@@ -118,6 +118,8 @@ int make_epilogue(const nvfp4_epilogue *e, int64_t N, int64_t M, Epilogue *out)
         return NVFP4_ERR_INVALID_ARG;
     if (e->residual && (!dtype_ok(e->residual_dtype) || !aligned(e->residual, element(e->residual_dtype)) ||
                         e->residual_ld < M || !size_ok(N, e->residual_ld)))
+        return NVFP4_ERR_INVALID_ARG;
+    if (e->residual && e->residual == y && (e->residual_dtype != out_dtype || (N > 1 && e->residual_ld != M)))
         return NVFP4_ERR_INVALID_ARG;
     out->bias = e->bias;
     out->residual = e->residual;
@@ -430,7 +432,7 @@ int nvfp4_gemm_epilogue(const uint16_t *x, int64_t N, const uint8_t *codes, cons
     int rc = check_product(x, N, M, K, codes, scales, tensor_scale, y, out_dtype);
     Epilogue e;
     if (rc == NVFP4_OK)
-        rc = make_epilogue(epilogue, N, M, &e);
+        rc = make_epilogue(epilogue, N, M, y, out_dtype, &e);
     if (rc != NVFP4_OK)
         return rc;
     if (K == 0)
@@ -453,7 +455,7 @@ int nvfp4_fp6_gemm_epilogue(const uint16_t *x, int64_t N, const uint8_t *codes, 
     if (N < 0 || M < 0)
         return NVFP4_ERR_INVALID_ARG;
     Epilogue e;
-    const int rc = make_epilogue(epilogue, N, M, &e);
+    const int rc = make_epilogue(epilogue, N, M, y, out_dtype, &e);
     if (rc != NVFP4_OK)
         return rc;
     if (K == 0)

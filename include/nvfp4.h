@@ -375,7 +375,8 @@ typedef enum {
 typedef struct {
     const void *bias;       /* device [M], or NULL for none */
     const void *residual;   /* device [N][residual_ld], or NULL for none; may be y itself (same type,
-                               residual_ld = M: in place), and must not overlap it otherwise */
+                               residual_ld = M: in place; other forms of y itself are refused), and must
+                               not overlap it otherwise */
     int64_t residual_ld;    /* elements between token rows, at least M */
     int32_t bias_dtype;     /* nvfp4_out_dtype */
     int32_t residual_dtype; /* nvfp4_out_dtype */

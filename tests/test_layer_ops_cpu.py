@@ -41,6 +41,9 @@ def test_epilogue_refuses_bad_arguments(lib):
         assert run(fp6, wsb=16) == binding.NVFP4_ERR_WORKSPACE
         assert run(fp6, N=0, x=None, y=None) == binding.NVFP4_OK
         assert run(fp6, M=0, y=None, ws=None, wsb=0) == binding.NVFP4_OK
+        # in place, but with another type or stride than the output's
+        assert run(fp6, residual_dtype=1) == BAD
+        assert run(fp6, residual_ld=72) == BAD
     assert run(ts=None) == BAD
 
 
