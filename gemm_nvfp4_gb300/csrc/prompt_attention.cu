@@ -19,7 +19,7 @@
 //                   there would reach every row through 0 * inf, so it is taken out of the tile, and
 //                   added at the end to the rows that do see it; and write the output rows, beside the next item's softmax.
 //
-// Items are taken heaviest first (the last tokens of the sequences, then those before them), CTA c of P taking
+// Items are taken heaviest first (the last tokens of the sequences, then those before them; of 32 sequences at a time), CTA c of P taking
 // the c-th of every P, in alternating directions: for one long causal prompt every CTA then has the same
 // number of keys to within a tile.  The lengths are on the device, so each CTA finds its items itself.
 //
@@ -133,17 +133,17 @@ NVFP4_DEVINL void key_range(const Call &c, int len, int token, int *lo, int *hi)
 // Load warp
 // ---------------------------------------------------------------------------
 
-// Items of a call in order, heaviest first: by place in the sequence (a sequence's last ones first), then by sequence, then by
-// head; without a causal mask, where all items of a sequence cost the same, by sequence, the longest first (if there are
-// no more than 32).
+// Items of a call in order: 32 sequences after the other (each chunk of them is looked at once, however many there are),
+// and among those the heaviest first: by place in the sequence (a sequence's last ones first), then by sequence, then by
+// head; without a causal mask, where all items of a sequence cost the same, by sequence, the longest first.
 struct Cursor {
     int level, chunk;  // place, and 32 sequences of which lane i holds the i-th
     int begin, len, places;  // the lane's: places of two row tiles
     uint32_t with;     // lanes whose sequence has the level's place
-    uint32_t pos;      // number of the first item of the level and chunk (a call has less than 2^31)
+    uint32_t pos;      // number of the first item of the level (a call has less than 2^31)
     uint32_t rank;     // by sequence: places and lane of the one at hand
 
-    __device__ __noinline__ void load(const Call &c, int lane, bool report)
+    __device__ __noinline__ void load(const Call &c, int lane)
     {
         const int b = chunk + lane;
         begin = len = 0;
@@ -152,7 +152,7 @@ struct Cursor {
             if (c.offsets) {
                 const int from = c.offsets[b], to = c.offsets[b + 1];
                 const bool ok = from >= 0 && to >= from && to <= c.total;
-                if (!ok && report)
+                if (!ok && blockIdx.x == 0)
                     kv::report_index(c.status, kStatusPromptOffsets);
                 begin = from;
                 len = ok ? to - from : 0;
@@ -160,22 +160,20 @@ struct Cursor {
         }
         places = (int)((uint32_t)(len + 2 * c.tokens - 1) / (2u * c.tokens));
     }
-    NVFP4_DEVINL void start(const Call &c, int lane)
+    // To the chunk's first item.
+    NVFP4_DEVINL void open(const Call &c, int lane)
     {
-        level = 0;
-#pragma unroll 1
-        for (chunk = 0; chunk < c.n_seqs; chunk += 32) {
-            load(c, lane, blockIdx.x == 0);
-            level = max(level, places);
-        }
-        level = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)level) - 1;
-        chunk = 0;
-        pos = 0;
-        if (c.n_seqs > 32)
-            load(c, lane, false);
+        load(c, lane);
+        level = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)places) - 1;
         with = __ballot_sync(0xFFFFFFFFu, places > level);
         rank = 0xFFFFFFFFu;
         next_rank(lane);
+    }
+    NVFP4_DEVINL void start()
+    {
+        chunk = -32;
+        pos = rank = 0;
+        level = -1;
     }
     // The next sequence by length.
     NVFP4_DEVINL void next_rank(int lane)
@@ -188,32 +186,32 @@ struct Cursor {
     {
         uint32_t k;
         int src, place;
-        if (c.causal || c.n_seqs > 32) {
 #pragma unroll 1
-            for (;;) {
-                if (level < 0)
+        for (;;) {
+            if (c.causal ? level < 0 : rank == 0) {
+                if (chunk + 32 >= c.n_seqs)
                     return false;
-                const uint32_t count = __popc(with) * c.kv_heads;
-                if (want < pos + count)
-                    break;
-                if (c.n_seqs > 32) {
-                    pos += count;
-                    chunk += 32;
-                    if (chunk >= c.n_seqs) {
-                        chunk = 0;
-                        --level;
-                    }
-                    load(c, lane, false);
-                } else {
-                    // on by as many levels as have the same sequences, or to the one that has the item
-                    const int last = (int)__reduce_max_sync(0xFFFFFFFFu, places > level ? 0u : (unsigned)places);
-                    const uint32_t skip = min((uint32_t)(level - last + 1), (want - pos) / count);
-                    pos += skip * count;
-                    level -= (int)skip;
-                }
-                with = __ballot_sync(0xFFFFFFFFu, places > level);
+                chunk += 32;
+                open(c, lane);
+                continue;
             }
-            k = want - pos;
+            const uint32_t count = (c.causal ? __popc(with) : rank >> 5) * c.kv_heads;
+            if (want < pos + count)
+                break;
+            if (c.causal) {
+                // on by as many levels as have the same sequences, or to the one that has the item
+                const int last = (int)__reduce_max_sync(0xFFFFFFFFu, places > level ? 0u : (unsigned)places);
+                const uint32_t skip = min((uint32_t)(level - last + 1), (want - pos) / count);
+                pos += skip * count;
+                level -= (int)skip;
+                with = __ballot_sync(0xFFFFFFFFu, places > level);
+            } else {
+                pos += count;
+                next_rank(lane);
+            }
+        }
+        k = want - pos;
+        if (c.causal) {
             const uint32_t which = k / (uint32_t)c.kv_heads;
             k -= which * c.kv_heads;
             // the lane that has `which` others before it
@@ -221,17 +219,6 @@ struct Cursor {
             src = __ffs(__ballot_sync(0xFFFFFFFFu, (with >> lane & 1) && __popc(before) == (int)which)) - 1;
             place = level;
         } else {
-#pragma unroll 1
-            for (;;) {
-                if (rank == 0)
-                    return false;
-                const uint32_t count = (rank >> 5) * c.kv_heads;
-                if (want < pos + count)
-                    break;
-                pos += count;
-                next_rank(lane);
-            }
-            k = want - pos;
             src = 31 - (int)(rank & 31);
             place = (int)(k / (uint32_t)c.kv_heads);
             k -= place * c.kv_heads;
@@ -269,7 +256,7 @@ NVFP4_DEVINL bool load_role(const Call &c, const CUtensorMap *q_map, const CUten
 {
     using C = Cfg<D>;
     Cursor cur;
-    cur.start(c, lane);
+    cur.start();
     uint32_t loaded = 0, q_items = 0, q_items_1 = 0;  // tiles of K (and V), and queries of row tile 0 and 1
     const uint32_t ctas = gridDim.x;
     bool ok = true;

@@ -223,6 +223,20 @@ def test_many_sequences(n_seqs):
             assert ((got[lo:hi, h].double() - want).abs() <= tol + BF16_REL * (want.abs() + tol)).all()
 
 
+@pytest.mark.parametrize("n_seqs,at,hq,causal", [(65535, 65534, 128, True), (65535, 40000, 2, False), (40, 0, 8, True), (70, 69, 4, False)])
+def test_one_long_sequence_among_many(n_seqs, at, hq, causal):
+    """Chunks of sequences without a token, and one with many places in the order of the work."""
+    n = 700
+    p = Prompts([n], hq, 1, 64, seed=n_seqs)
+    offsets = torch.zeros(n_seqs + 1, dtype=torch.int32, device=DEV)
+    offsets[at + 1:] = n
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    got = p.run(offsets=offsets, causal=causal, workspace=ws)
+    assert g.nvfp4_device_status(ws) == (g.NVFP4_OK, 0)
+    p.check(got, causal=causal)
+    assert torch.equal(got, p.run(causal=causal))
+
+
 def test_strides_and_output_views():
     """q, k, v and out in buffers of their own strides."""
     p = Prompts([130, 7], 4, 2, 64)
