@@ -57,6 +57,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "attention_ops.cuh"
 #include "epilogue.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"
@@ -73,6 +74,14 @@ constexpr int kFirstDqWarp = 1 + kIssuers;
 constexpr int kThreads = kFirstDqWarp * 32 + kDqWarps * 32;
 constexpr int kCodeWarp = kFirstDqWarp + kDqWarps;  // code / scale TMA producer (TMA-code mode)
 constexpr int kThreadsTma = kThreads + 32;
+// PARTS: warps that add up parts of the sums, and how many stages a part has (2048 products).
+constexpr int kSumWarp = kCodeWarp + 1, kSumWarps = 8, kPartStages = 32;
+constexpr int kThreadsParts = kThreadsTma + 32 * kSumWarps;
+static_assert(kSumWarp % 4 == 0, "a warp reads the quarter of the tensor-memory lanes that its number says");
+// Registers of a thread: what the launch gives every thread, shared out anew.
+constexpr int kPartsRegs = 96, kSumRegs = 144, kNoSumRegs = 64;
+static_assert(32 * kSumWarps * kSumRegs + kThreadsTma * kNoSumRegs <= kThreadsParts * kPartsRegs,
+              "setmaxnreg would wait for registers that nobody gives back");
 constexpr int kSBytes = BM * 16;         // NVFP4 scales of four stages: 128 rows x 16 bytes
 // codes of one stage: 128 rows x 32 bytes (NVFP4) or 48 bytes (FP6)
 template <int FMT> constexpr int code_row_bytes() { return FMT == 0 ? BK / 2 : BK / 4 * 3; }
@@ -348,8 +357,14 @@ NVFP4_DEVINL void store_column(const Args &a, const uint32_t (&r)[2][kEpiCols], 
 
 // TN: tokens per tile (MMA N), 256 or 192; the host picks it per call so that
 // the grid fills the SMs' waves (the accumulation order does not depend on it).
-template <int NW, bool ALIGNED, int FMT = 0, bool TMAC = false, int TN = BN, bool SPLIT = false, bool EPI = false>
-__global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
+//
+// PARTS: the tensor core's own accumulation over 17408 products is off by 3.7e-6 of the outputs' norm (the error grows with
+// their number; NVFP4 products that split K are at 2e-7).  So warps of their own add up parts of 2048 in registers, 96
+// columns a thread, from two accumulators that the MMAs take by turns (hence TN = 192): 2.3e-7.  2048 tokens of 17408 ->
+// 5120 with an fp32 residual take 374 us instead of 352 (441 with the parts added up by the dequantisers).
+template <int NW, bool ALIGNED, int FMT = 0, bool TMAC = false, int TN = BN, bool SPLIT = false, bool EPI = false,
+          bool PARTS = false>
+__global__ void __launch_bounds__(PARTS ? kThreadsParts : TMAC ? kThreadsTma : kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ WeightMaps wmaps, Args a)
 {
     using C = Cfg<NW, TMAC, FMT, TN>;
@@ -370,8 +385,9 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
     uint64_t *full_a = bars, *full_b = bars + S, *empty = bars + 2 * S, *tmem_full = bars + 3 * S;
     uint64_t *cfull = bars + 3 * S + 1, *cempty = cfull + SC, *sfull = cempty + SC, *sempty = sfull + 2;
     uint64_t *tmem_empty = sempty + 2;  // split mode: segment 0's accumulator has been read
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(tmem_empty + 1);
-    static_assert(3 * S + 1 + 2 * SC + 4 + 1 <= 128, "barriers and TMEM slot in the 1024-byte barrier area");
+    uint64_t *part_full = tmem_empty + 1, *part_empty = part_full + 2;  // PARTS: by accumulator
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(part_empty + 2);
+    static_assert(3 * S + 1 + 2 * SC + 4 + 1 + 4 + 1 <= 128, "barriers and TMEM slot in the 1024-byte barrier area");
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // The CTA's k blocks: one whole tile (raster order: the host picks the
@@ -379,6 +395,9 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
     // L2), or in split mode the segments of its unit range.  Stage i of the
     // CTA runs the cursor's k block; ring positions follow i.
     static_assert(!SPLIT || (NW == 1 && TMAC && FMT == 0), "split mode: one NVFP4 matrix, A in tensor memory");
+    static_assert(!PARTS || (EPI && !SPLIT && TA && TN == 192), "sums in parts");
+    constexpr int kAcol0 = PARTS ? 2 * TN : C::kAcol0;  // of tensor memory: the A ring's first column
+    constexpr int kEpiWarp = PARTS ? kSumWarp : kFirstDqWarp;  // the first of eight warps that store the outputs
     int num_kb;
     const SegCursor c0 = cta_cursor<TN, SPLIT>(a, blockIdx.x, num_kb);
     const int64_t m0 = c0.m0;
@@ -391,6 +410,10 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
         }
         tc::mbar_init(tmem_full, C::kIssue);
         tc::mbar_init(tmem_empty, kDqWarps);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(&part_full[i], 1);
+            tc::mbar_init(&part_empty[i], kSumWarps);
+        }
         if (TMAC) {
             for (int c = 0; c < SC; ++c) {
                 tc::mbar_init(&cfull[c], 1);
@@ -423,6 +446,10 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
     if (SPLIT && !a.after_whole)
         tc::griddep_wait();
     tc::griddep_launch_dependents();
+    if constexpr (PARTS) {
+        if (warp < kSumWarp)
+            attn::give_regs<kNoSumRegs>();
+    }
 
     if (warp == 0) {
         // ---------------- TMA producer (x tiles) ----------------
@@ -463,6 +490,13 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
                 for (int kt = k0; kt < k1; ++kt, ++kb) {
                     const int s = kb % S;
                     const uint32_t ph = (kb / S) & 1;
+                    const int part = kt / kPartStages;
+                    if (PARTS && part > 1 && kt % kPartStages == 0 &&
+                        !tc::mbar_wait(&part_empty[part & 1], ((uint32_t)(part >> 1) & 1) ^ 1)) {
+                        fail(a, 8);
+                        ok = false;
+                        break;
+                    }
                     if (!tc::mbar_wait(&full_a[s], ph) || !tc::mbar_wait(&full_b[s], ph)) {
                         fail(a, 2);
                         ok = false;
@@ -470,11 +504,14 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
                     }
                     tc::fence_after_sync();
                     const uint64_t bdesc = tc::smem_desc_sw128(sb + (size_t)s * kBBytes);
-                    const uint32_t acol = tmem_base + C::kAcol0 + s * (BK / 2);
+                    const uint32_t acol = tmem_base + kAcol0 + s * (BK / 2);
 #pragma unroll
                     for (int k = 0; k < BK / 16; ++k)
-                        tc::mma_f16_ts(tmem_base, acol + 8 * k, bdesc + 2 * k, idesc, (kt > k0 || k > 0) ? 1u : 0u);
+                        tc::mma_f16_ts(tmem_base + (PARTS ? (part & 1) * TN : 0), acol + 8 * k, bdesc + 2 * k, idesc,
+                                       ((PARTS ? kt % kPartStages > 0 : kt > k0) || k > 0) ? 1u : 0u);
                     tc::mma_commit(&empty[s]);
+                    if (PARTS && (kt % kPartStages == kPartStages - 1 || kt + 1 == k1))
+                        tc::mma_commit(&part_full[part & 1]);
                 }
                 if (!SPLIT || !ok || !seg_skip<TN>(a, cur))
                     break;
@@ -577,7 +614,7 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
         auto put_a_tmem = [&](int s, const uint4 (&v)[4]) {
             const uint32_t w[16] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w,
                                     v[2].x, v[2].y, v[2].z, v[2].w, v[3].x, v[3].y, v[3].z, v[3].w};
-            tc::tmem_st_32x32b_x16(tmem_base + ((uint32_t)(32 * (warp & 3)) << 16) + C::kAcol0 + s * (BK / 2) +
+            tc::tmem_st_32x32b_x16(tmem_base + ((uint32_t)(32 * (warp & 3)) << 16) + kAcol0 + s * (BK / 2) +
                                        half * 16,
                                    w);
         };
@@ -608,7 +645,7 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
             // these are used (FP6, 2048 tokens, 17408 -> 5120, fp32: 413 -> 404 us)
             uint32_t res[EPI ? kEpiCols : 1];
             if (EPI && !split_seg)
-                load_residual(a.ep, res, (int64_t)sg.n0 + ((warp - kFirstDqWarp) >> 2) * (TN / 2), a.N,
+                load_residual(a.ep, res, (int64_t)sg.n0 + ((warp - kEpiWarp) >> 2) * (TN / 2), a.N,
                               sg.m0 + (warp & 3) * 32 + lane, a.M);
             const bool have = tc::mbar_wait(tmem_full, (uint32_t)sg.seg & 1);
             if (!have)
@@ -618,7 +655,7 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
             const int sn0 = sg.n0;
             if (have) {
                 const int quarter = warp & 3;          // TMEM lanes this warp may access
-                const int chalf = (warp - kFirstDqWarp) >> 2;  // which half of the TN token columns
+                const int chalf = (warp - kEpiWarp) >> 2;  // which half of the TN token columns
                 const int64_t mrow = sm0 + quarter * 32 + lane;
                 float ts[NW];
 #pragma unroll
@@ -706,11 +743,57 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
                     tc::mbar_arrive(tmem_empty);
             }
         };
-        if constexpr (EPI && !SPLIT)
-            epilogue_prefetch(a.ep, c0.n0, c0.n0 + TN < a.N ? c0.n0 + TN : a.N, m0, BM, a.M, threadIdx.x - kFirstDqWarp * 32,
+        if (EPI && !SPLIT && warp >= kEpiWarp)
+            epilogue_prefetch(a.ep, c0.n0, c0.n0 + TN < a.N ? c0.n0 + TN : a.N, m0, BM, a.M, threadIdx.x - kEpiWarp * 32,
                               kDqWarps * 32);
         SegCursor dcur = c0;  // the dequantisers' stage cursor
-        if constexpr (TMAC && FMT == 1) {
+        const bool sums_parts = PARTS && warp >= kSumWarp;
+        if constexpr (PARTS) {
+            if (sums_parts) {
+                attn::take_regs<kSumRegs>();
+                // this thread's row and half of the tile's columns
+                const uint32_t at = tmem_base + ((uint32_t)(32 * (warp & 3)) << 16) + ((warp - kSumWarp) >> 2) * (TN / 2);
+                float sum[TN / 2];
+#pragma unroll
+                for (int j = 0; j < TN / 2; ++j)
+                    sum[j] = 0.f;
+                for (int part = 0; part * kPartStages < num_kb; ++part) {
+                    if (!tc::mbar_wait(&part_full[part & 1], (uint32_t)(part >> 1) & 1)) {
+                        fail(a, 4);
+                        break;
+                    }
+                    tc::fence_after_sync();
+#pragma unroll
+                    for (int c = 0; c < TN / 2; c += 32) {
+                        uint32_t r[32];
+                        tc::tmem_ld_32x32b_x32(at + (part & 1) * TN + c, r);
+                        tc::tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            asm volatile("" : "+r"(r[j]));  // (not before the wait)
+                            sum[c + j] += __uint_as_float(r[j]);
+                        }
+                    }
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive(&part_empty[part & 1]);
+                }
+                // to the first accumulator, whose parts this warp has read
+#pragma unroll
+                for (int c = 0; c < TN / 2; c += 16) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        r[j] = __float_as_uint(sum[c + j]);
+                    tc::tmem_st_32x32b_x16(at + c, r);
+                }
+                tc::tmem_st_wait();
+                epilogue(dcur);
+            }
+        }
+        if constexpr (TMAC && FMT == 1)
+        if (!sums_parts) {
             // FP6 codes from the TMA ring; the scale byte of a row (one per
             // 128 k = two stages) through a small register prefetch ring.
             const uint32_t fp6_ring_a = tc::smem_addr(sc_ring) + (uint32_t)(row * kCRow + half * 24);
@@ -727,7 +810,7 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
             uint32_t scl[NW];
             // Unrolled, so that the ring positions and sring's registers are constants: 2048 tokens of 17408 -> 5120 take
             // 322 us instead of 395 (with bias, activation or residual 352 instead of 444; 362 unrolled by 8).
-#pragma unroll (EPI ? 16 : 8)
+#pragma unroll (EPI && !PARTS ? 16 : 8)
             for (int kb = 0; kb < num_kb; ++kb) {
                 if ((kb & 1) == 0) {
                     const int blk = kb >> 1;
@@ -922,9 +1005,11 @@ __global__ void __launch_bounds__(TMAC ? kThreadsTma : kThreads, 1)
         // early: the epilogues of the segments it did not reach still run
         // (their waits give up too), so that every dequantiser warp meets the
         // epilogues' named barriers the same number of times.
-        do {
-            epilogue(dcur);
-        } while (SPLIT && seg_skip<TN>(a, dcur));
+        if constexpr (!PARTS) {
+            do {
+                epilogue(dcur);
+            } while (SPLIT && seg_skip<TN>(a, dcur));
+        }
     }
 
     // Lane 0 of warps 0 and 1 ran the producer / MMA loops alone: reconverge
@@ -1109,14 +1194,23 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-template <int NW, bool ALIGNED, int FMT = 0, bool TMAC = false, int TN = BN, bool SPLIT = false, bool EPI = false>
+template <int NW, bool ALIGNED, int FMT = 0, bool TMAC = false, int TN = BN, bool SPLIT = false, bool EPI = false,
+          bool PARTS = false>
 cudaError_t launch_t(const CUtensorMap &map, const WeightMaps &wm, const Args &a, cudaStream_t stream)
 {
     using C = Cfg<NW, TMAC, FMT, TN>;
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr_errs[kMaxDevices];
     const cudaError_t attr_err = once_per_device(once, attr_errs, [] {
-        return cudaFuncSetAttribute(prefill_kernel<NW, ALIGNED, FMT, TMAC, TN, SPLIT, EPI>,
+        if constexpr (PARTS) {
+            cudaFuncAttributes attr;
+            const cudaError_t e = cudaFuncGetAttributes(&attr, prefill_kernel<NW, ALIGNED, FMT, TMAC, TN, SPLIT, EPI, PARTS>);
+            if (e != cudaSuccess)
+                return e;
+            if (attr.numRegs != kPartsRegs)  // the roles share out what the launch gives: never launch with less
+                return cudaErrorInvalidConfiguration;
+        }
+        return cudaFuncSetAttribute(prefill_kernel<NW, ALIGNED, FMT, TMAC, TN, SPLIT, EPI, PARTS>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmemBytes);
     });
     if (attr_err != cudaSuccess)
@@ -1135,10 +1229,10 @@ cudaError_t launch_t(const CUtensorMap &map, const WeightMaps &wm, const Args &a
         attr[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, prefill_kernel<NW, ALIGNED, FMT, TMAC, TN, SPLIT, EPI>, map, wm, a);
+        return cudaLaunchKernelEx(&cfg, prefill_kernel<NW, ALIGNED, FMT, TMAC, TN, SPLIT, EPI, PARTS>, map, wm, a);
     }
-    prefill_kernel<NW, ALIGNED, FMT, TMAC, TN, SPLIT, EPI>
-        <<<grid, TMAC ? kThreadsTma : kThreads, C::kSmemBytes, stream>>>(map, wm, a);
+    prefill_kernel<NW, ALIGNED, FMT, TMAC, TN, SPLIT, EPI, PARTS>
+        <<<grid, PARTS ? kThreadsParts : TMAC ? kThreadsTma : kThreads, C::kSmemBytes, stream>>>(map, wm, a);
     return cudaGetLastError();
 }
 
@@ -1313,6 +1407,10 @@ size_t prefill_workspace_bytes(int64_t N, int64_t M, int64_t K, int n_weights, i
     return 256 + (size_t)2 * ctas * pf::BN * pf::BM * sizeof(float);
 }
 
+// FP6 products with an epilogue and fp32 outputs add their sums up in parts (PARTS) above this K.  Up to it they are within
+// 1.3e-6 of the outputs' norm, and TN = 256 may be worth more: 512 tokens of 5120 -> 17408 take 92 us, in parts 132.
+constexpr int64_t kPartsFrom = 8192;
+
 // EPI: with an epilogue (one matrix).
 template <bool EPI>
 static cudaError_t prefill_impl(const uint16_t *x, int64_t N, int64_t M, int64_t K, const uint8_t *const *codes,
@@ -1327,7 +1425,8 @@ static cudaError_t prefill_impl(const uint16_t *x, int64_t N, int64_t M, int64_t
     const int64_t row_tiles = (M + pf::BM - 1) / pf::BM;
     SplitPlan sp{};
     const bool split = split_plan(N, M, K, n_weights, fmt, num_sms, &sp);
-    const int tn = split ? pf::BN : tma_weights ? pf::pick_token_tile(N, row_tiles, num_sms) : pf::BN;
+    const bool parts = EPI && fmt == 1 && !out_bf16 && K > kPartsFrom;
+    const int tn = parts ? 192 : split ? pf::BN : tma_weights ? pf::pick_token_tile(N, row_tiles, num_sms) : pf::BN;
     const int64_t token_tiles = (N + tn - 1) / tn;
     if (row_tiles * token_tiles > 0x7FFFFFFF)
         return cudaErrorInvalidValue;
@@ -1401,6 +1500,8 @@ static cudaError_t prefill_impl(const uint16_t *x, int64_t N, int64_t M, int64_t
             if (!pf::encode_rows(encode, &wm.codes[i], codes[i], K / 4 * 3, M, pf::code_row_bytes<1>()))
                 return cudaErrorInvalidValue;
         if constexpr (EPI) {
+            if (parts)
+                return pf::launch_t<1, true, 1, true, 192, false, true, true>(map, wm, a, stream);
             return tn == 192 ? pf::launch_t<1, true, 1, true, 192, false, true>(map, wm, a, stream)
                              : pf::launch_t<1, true, 1, true, 256, false, true>(map, wm, a, stream);
         } else {

@@ -104,6 +104,25 @@ def test_every_kernel(fmt, N, M, K):
         assert_close(to_np(y), ref, tol, f"{act} {b} {r} {out}")
 
 
+@pytest.mark.parametrize("fmt,N,M,K", [("nvfp4", 200, 260, 8448), ("fp6", 17, 129, 8320), ("fp6", 193, 260, 8448),
+                                       ("fp6", 300, 131, 9216), ("fp6", 40, 3, 10240)])
+def test_fp32_outputs_of_long_sums(fmt, N, M, K):
+    """FP6 sums are added up in parts of 2048 products: a whole number of them, and last ones of 128 to 1024."""
+    p = Product(fmt, N, M, K, seed=N)
+    bias, residual = p.vector(torch.bfloat16, 5), p.rows(torch.float32, 6, pad=1)
+    for act in ("none", "gelu_tanh"):
+        y = p.run(bias=bias, activation=ACTS[act], residual=residual)
+        assert_close(to_np(y), *reference(p.s, p.A, bias, act, residual, torch.float32))
+        assert torch.equal(p.run(bias=bias, activation=ACTS[act], residual=residual), y)
+    if fmt == "fp6":  # (without a tensor scale the parts are products of their own, to the bit)
+        total = torch.zeros_like(y)
+        for k in range(0, K, 2048):
+            at = slice(k, min(k + 2048, K))
+            W = g.FP6Weight(p.W.codes[:, k // 4 * 3:at.stop // 4 * 3].contiguous(), p.W.scales[:, k // 128:at.stop // 128].contiguous())
+            total += g.nvfp4_fp6_gemm_epilogue(p.x[:, at].contiguous(), W)
+        assert torch.equal(p.run(), total)
+
+
 @pytest.mark.parametrize("act", ACTS)
 @pytest.mark.parametrize("N", [2, 33])
 def test_every_activation(act, N):
