@@ -251,7 +251,12 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(Call c)
     }
 }
 
-// Any number of pairs, an element at a time.
+// Any number of pairs: a warp has one token and c.heads_per_warp heads of q and k as above, whose pairs (and elements that are
+// not turned) its lanes take one after the other, kAny pairs at a time.  8192 tokens of 40 and 8 bf16 heads of 80, 20 pairs:
+// 62 us (8 at a time 68, with all heads to one warp and a pair at a time 66), 2000 of 16 and 16 fp32 heads 18.3 (54), one token
+// 4.3 (36).  An element to a load, so it is bound by instructions.
+constexpr int kAny = 4;
+
 template <class T>
 __global__ void __launch_bounds__(kThreads) rope_any_kernel(Call c)
 {
@@ -259,9 +264,10 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(Call c)
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     tc::griddep_launch_dependents();
     tc::griddep_wait();
-    const int64_t token = (int64_t)blockIdx.x * kWarps + warp;
+    const int64_t id = (int64_t)blockIdx.x * kWarps + warp, token = id / c.parts;
     if (token >= c.tokens)
         return;
+    const int begin = (int)(id - token * c.parts) * c.heads_per_warp, end = min(begin + c.heads_per_warp, c.side[0].heads + c.side[1].heads);
     const int64_t position = lane_position(c, token, lane);
     for (int p = lane; p < (c.n_pairs + 31) / 32 * 32; p += 32) {
         const float2 t = turn_of(c, token, position, p);
@@ -269,30 +275,73 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(Call c)
             turns[warp][p] = t;
     }
     __syncwarp();
-    for (int s = 0; s < 2; ++s) {
-        const Side &side = c.side[s];
-        for (int h = 0; h < side.heads; ++h) {
-            const T *in = static_cast<const T *>(side.in) + token * side.in_ld + (int64_t)h * c.head_dim;
-            T *out = static_cast<T *>(side.out) + token * side.out_ld + (int64_t)h * c.head_dim;
-            for (int p = lane; p < c.n_pairs; p += 32) {
-                const float2 t = turns[warp][p];
-                const int a = c.adjacent ? 2 * p : p, b = c.adjacent ? 2 * p + 1 : p + c.n_pairs;
-                const float x = load(in + a), y = load(in + b);
-                store(out + a, x * t.x - y * t.y);
-                store(out + b, x * t.y + y * t.x);
+    const int nq = c.side[0].heads, dim = c.head_dim;
+    const T *const q = static_cast<const T *>(c.side[0].in) + token * c.side[0].in_ld;
+    const T *const k = static_cast<const T *>(c.side[1].in) + token * c.side[1].in_ld;
+    T *const q_out = static_cast<T *>(c.side[0].out) + token * c.side[0].out_ld;
+    T *const k_out = static_cast<T *>(c.side[1].out) + token * c.side[1].out_ld;
+    // f(number, whether of q, element of the token's q or k from which on, i) for each i of [0, width) of the heads, kAny of them
+    // at a time: first `loads`, then `stores`
+    const auto each = [&](int width, auto &&loads, auto &&stores) {
+        int h = begin + lane / width, i = lane % width;
+        while (__any_sync(0xFFFFFFFFu, h < end)) {
+            int hs[kAny], is[kAny];
+#pragma unroll
+            for (int n = 0; n < kAny; ++n) {
+                hs[n] = h;
+                is[n] = i;
+                if (h < end)
+                    loads(n, h < nq, (h < nq ? h : h - nq) * dim, i);
+                for (i += 32; i >= width; i -= width)
+                    ++h;
             }
-            if (in != out)
-                for (int i = 2 * c.n_pairs + lane; i < c.head_dim; i += 32)
-                    out[i] = in[i];
+#pragma unroll
+            for (int n = 0; n < kAny; ++n)
+                if (hs[n] < end)
+                    stores(n, hs[n] < nq, (hs[n] < nq ? hs[n] : hs[n] - nq) * dim, is[n]);
         }
+    };
+    const int step = c.adjacent ? 2 : 1, apart = c.adjacent ? 1 : c.n_pairs;  // from pair to pair, within one
+    if (c.n_pairs > 0) {
+        float x[kAny], y[kAny];
+        each(
+            c.n_pairs,
+            [&](int n, bool of_q, int at, int p) {
+                const T *in = (of_q ? q : k) + at + step * p;
+                x[n] = load(in);
+                y[n] = load(in + apart);
+            },
+            [&](int n, bool of_q, int at, int p) {
+                const float2 t = turns[warp][p];
+                T *out = (of_q ? q_out : k_out) + at + step * p;
+                store(out, x[n] * t.x - y[n] * t.y);
+                store(out + apart, x[n] * t.y + y[n] * t.x);
+            });
+    }
+    // what is not turned
+    const int turned = 2 * c.n_pairs;
+    if (turned < dim && (q != q_out || k != k_out)) {
+        T rest[kAny];
+        each(
+            dim - turned, [&](int n, bool of_q, int at, int i) { rest[n] = (of_q ? q : k)[at + turned + i]; },
+            [&](int n, bool of_q, int at, int i) {
+                if (of_q ? q != q_out : k != k_out)
+                    (of_q ? q_out : k_out)[at + turned + i] = rest[n];
+            });
     }
 }
 
 template <class T>
 cudaError_t launch(Call c, int num_sms, cudaStream_t stream)
 {
-    if (c.n_pairs % 8 != 0 || c.n_pairs == 0 || c.n_pairs > 256)
-        return launch_dependent(rope_any_kernel<T>, dim3((unsigned)((c.tokens + kWarps - 1) / kWarps)), kThreads, 0, stream, c);
+    if (c.n_pairs % 8 != 0 || c.n_pairs == 0 || c.n_pairs > 256) {
+        // few tokens: a token's heads to as many warps as fill the GPU
+        const int all = c.side[0].heads + c.side[1].heads;
+        const int64_t fill = ((int64_t)num_sms * kWarpsPerSm + c.tokens - 1) / c.tokens;
+        c.heads_per_warp = (int)((all + fill - 1) / fill);
+        c.parts = (all + c.heads_per_warp - 1) / c.heads_per_warp;
+        return launch_dependent(rope_any_kernel<T>, dim3((unsigned)((c.tokens * c.parts + kWarps - 1) / kWarps)), kThreads, 0, stream, c);
+    }
     // A warp takes as many heads as its lanes load at once; fewer, down to one each, while there are fewer than kWarpsPerSm
     // warps an SM (4999 tokens of 32 fp32 heads: 20.0 us at 24, 18.0 at 64, 17.9 at 128, where 8192 tokens of 48 bf16 heads
     // take 37.1 instead of 33.7).

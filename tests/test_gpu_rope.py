@@ -78,6 +78,22 @@ def test_turns(dtype, adjacent, tokens, hq, hk, d, rotary, axes):
     assert torch.equal(q, before)
 
 
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("tokens,hq,hk,rotary", [(3000, 5, 2, 10), (12000, 2, 1, 20), (2500, 0, 7, 6)])
+def test_odd_pairs_of_many_tokens(tokens, hq, hk, rotary, adjacent):
+    """Numbers of pairs that are no multiple of 8, several heads to a warp (one of q and one of k among them)."""
+    pairs = rotary // 2
+    table = g.RopeTable.make(frequencies(pairs))
+    positions = torch.arange(tokens)
+    q, k = rows(tokens, hq, 24, torch.bfloat16, 2), rows(tokens, hk, 24, torch.bfloat16, 3)
+    got_q, got_k = g.nvfp4_rope(q, k, positions.to(DEV), table, adjacent=adjacent)
+    angle = angles(table, [positions.tolist()], [0] * pairs)
+    check(got_q, q, angle, pairs, adjacent)
+    check(got_k, k, angle, pairs, adjacent)
+    g.nvfp4_rope(q, k, positions.to(DEV), table, adjacent=adjacent, out=(q, k))
+    assert torch.equal(q, got_q) and torch.equal(k, got_k)
+
+
 def test_far_and_negative_positions():
     """Where fp32 angles would be off by many turns."""
     freq = [1.0, 0.37, 1e-3, -0.8, 2.0 ** 20 + 0.3, 1e-9, 0.0, math.pi]
