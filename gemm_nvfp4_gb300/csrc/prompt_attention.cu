@@ -11,8 +11,8 @@
 //
 //   warps 0-3, 4-7  softmax of row tile 0 and 1, a row to a thread: scores come from tensor
 //                   memory, the weights P go back there in bf16 as the A operand of the second product
-//                   (heads of 128: over the scores).  A row's reference (an estimate of its largest score) moves only where a
-//                   weight would exceed 2^15, so that the sums so far are hardly ever multiplied.
+//                   (heads of 128: over the scores).  A row's reference (2^27 times its largest weight, as far as it is known)
+//                   moves only where that has grown by 2^8, so that the sums so far are hardly ever multiplied.
 //   warp 8          finds the items and loads Q, K and V by TMA.
 //   warp 9          MMA issue of both row tiles.
 //   warps 12-15     look through V tiles in which rows see different keys: an infinity or a NaN
@@ -59,8 +59,11 @@ static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= kThreads * kLaunchRegs,
 constexpr int kItems = 4;      // items that the load warp may be ahead
 constexpr int kMostMixed = 8;  // tiles of an item in which rows see different keys: at most 6
 constexpr int kSharedBytes = 3 * 1024;
-// A row's reference is 2^kHeadroom below its largest weight when it moves, and moves when one exceeds 2^kSlack.
-constexpr float kHeadroom = 7.f, kSlack = 15.f;
+// A row's reference is such that its largest weight is 2^kHeadroom when it moves, and moves when one exceeds 2^kSlack.  A
+// call has less than 2^18 keys (check_args), so a row's weights add up to 1/2 at most and no finite V overflows the sums that
+// are divided by them in the end.  What that costs lies at the other end: weights below 2^-126, 2^-99 of the largest, are zero.
+constexpr float kHeadroom = -27.f, kSlack = -19.f;
+static_assert((INT32_MAX / 8192) >> 18 == 0, "weights of 2^18 keys at most");
 
 // Codes of the status word (waits that ran out).
 enum : uint32_t { kTimeoutSoftmax = 61, kTimeoutLoad = 62, kTimeoutMma = 63, kTimeoutHelper = 64 };

@@ -624,9 +624,10 @@ int nvfp4_rope(const nvfp4_rope_args *args, nvfp4_stream_t stream);
  * Numerics: q . k_j exact in its products with fp32 accumulation; softmax statistics in
  * fp32 (2^x by the hardware's approximation, relative error about 2^-22); the weights enter
  * the second product rounded to bf16, with a relative error of at most 2^-8 each, and fp32
- * accumulation: |out - exact| <= (2^-8 + 2^-15 * S) * sum_j softmax_j |v_j|, plus the
- * rounding of out, with S = max_j |scale| * sum_d |q_d k_jd|.  Scores have to stay within
- * fp32's range.
+ * accumulation: |out - exact| <= (2^-8 + 2^-15 * S) * sum_j softmax_j |v_j| + 2^-80 * (1 + max_j |v_j|),
+ * plus the rounding of out, with S = max_j |scale| * sum_d |q_d k_jd|.  (The last term: weights below 2^-99 of a
+ * row's largest count as none, and so do products with V that are below 2^-126 of 2^-27.)  No finite V overflows on the
+ * way (S below 2^22): out is finite wherever that bound is within its type.  Scores have to stay within fp32's range.
  *
  * Requirements: head_dim 64 or 128; n_q_heads a multiple of n_kv_heads, at most 128 times as
  * many; q, k, v, out 16-byte aligned, their strides multiples of 8 elements and at least a row of all

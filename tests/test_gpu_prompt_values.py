@@ -1,0 +1,69 @@
+"""Attention over whole prompts (nvfp4_prompt_attention): V of any finite magnitude, and infinities in K."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import gemm_nvfp4_gb300 as g
+from helpers import BF16_REL, DEV
+from test_gpu_prompt_attention import Prompts
+
+pytestmark = pytest.mark.gpu
+
+# magnitudes of V: up to 2^127 (the largest bf16 numbers but for the last rounding), and down to where the bound's absolute
+# term, 2^-80, is as large as the rounding of the weights
+MAGNITUDES = [2.0 ** e for e in (126, 121, 107, 0, -60, -72)]
+
+
+def with_magnitude(p, size):
+    """V rows of magnitudes in [1, 2) * size (their signs kept)."""
+    m = 1 + p.v.float().abs() % 1
+    p.v.copy_(torch.copysign(m.clamp(max=1.99), p.v.float()) * size)
+
+
+def check(p, got, **kw):
+    """Against include/nvfp4.h's bound with its absolute term."""
+    want, tol = p.reference(**kw)
+    assert torch.isfinite(want).all() and torch.isfinite(got).all()
+    tol = tol + 2.0 ** -80 * (1 + p.v.double().abs().amax())
+    tol = tol + (BF16_REL * (want.abs() + tol) if got.dtype == torch.bfloat16 else 2.0 ** -24 * want.abs())
+    bad = ~((got.double() - want).abs() <= tol)
+    assert not bad.any(), (int(bad.sum()), got[bad][0], want[bad][0], tol[bad][0])
+
+
+@pytest.mark.parametrize("size", MAGNITUDES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_values_of_any_magnitude(size, d, causal):
+    """One key (its own weight alone), and some hundred."""
+    p = Prompts([1, 300, 2], 4, 2, d, seed=3)
+    with_magnitude(p, size)
+    for out_dtype in (torch.bfloat16, torch.float32):
+        check(p, p.run(causal=causal, out_dtype=out_dtype), causal=causal)
+
+
+@pytest.mark.parametrize("size", MAGNITUDES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_of_any_magnitude_under_equal_scores(size, d):
+    """Thousands of equal weights on values of one sign: the largest sums there are before the division."""
+    p = Prompts([5000], 2, 1, d, seed=4)
+    with_magnitude(p, size)
+    p.v.abs_()
+    p.q.zero_()
+    check(p, p.run(causal=False), causal=False)
+
+
+@pytest.mark.parametrize("size", MAGNITUDES)
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_of_any_magnitude_under_a_lagging_reference(size, d):
+    """Scores that rise after the first key tile by almost as much as the row's reference lets them: by 2^7.9."""
+    p = Prompts([3000], 2, 1, d, seed=5)
+    with_magnitude(p, size)
+    p.v.abs_()
+    p.q.zero_()
+    p.q[..., 0] = 1.0
+    p.k[..., 0] = 0.0
+    p.k[128:, :, 0] = 7.9
+    check(p, p.run(causal=False, scale=math.log(2)), causal=False, scale=math.log(2))
