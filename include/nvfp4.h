@@ -618,8 +618,10 @@ int nvfp4_rope(const nvfp4_rope_args *args, nvfp4_stream_t stream);
  *   not causal   every token of its sequence (encoders, images).
  * out = sum_j softmax_j(scale * q_i . k_j) v_j over the tokens it sees, query head h
  * reading KV head h / (n_q_heads / n_kv_heads).  K and V of tokens that a token does not see
- * never reach its output, whatever they hold; a query, or a K or V row that it sees, with an infinity or
- * a NaN gives outputs that are not finite.  Rows of out that belong to no sequence are left as they are.
+ * never reach its output, whatever they hold.  A query with an infinity or a NaN gives outputs that are not finite, and so does
+ * an element of a V row that it sees in its element of the output.  Infinities and NaN in a K row that it sees count by the
+ * score that they make: NaN or +infinity gives NaN, -infinity gives its key no weight (NaN if it sees no key with another
+ * score).  Rows of out that belong to no sequence are left as they are.
  *
  * Numerics: q . k_j exact in its products with fp32 accumulation; softmax statistics in
  * fp32 (2^x by the hardware's approximation, relative error about 2^-22); the weights enter

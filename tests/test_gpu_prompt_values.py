@@ -67,3 +67,33 @@ def test_values_of_any_magnitude_under_a_lagging_reference(size, d):
     p.k[..., 0] = 0.0
     p.k[128:, :, 0] = 7.9
     check(p, p.run(causal=False, scale=math.log(2)), causal=False, scale=math.log(2))
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 150), (False, 0)])
+@pytest.mark.parametrize("scale", [0.125, -0.125])
+@pytest.mark.parametrize("d", [64, 128])
+def test_infinities_in_keys(bad, causal, window, scale, d):
+    """A score of +infinity makes the row NaN, one of -infinity gives its key no weight, as the softmax has it: among keys
+    that every row of a tile sees, and among masked ones."""
+    n, at = 500, 20
+    p = Prompts([n], 4, 2, d, seed=6)
+    p.k[at, :, 3] = bad
+    p.k[0, 1, 5] = bad  # (all that the first token sees)
+    got = p.run(causal=causal, window=window, scale=scale).double()
+    i = torch.arange(n, device=DEV)
+    see = i <= i[:, None] if causal else torch.ones(n, n, dtype=torch.bool, device=DEV)
+    if window:
+        see = see & (i > i[:, None] - window)
+    for h in range(4):
+        q, k, v = p.q[:, h].double(), p.k[:, h // 2].double(), p.v[:, h // 2].double()
+        z = (q @ k.T * scale).masked_fill(~see, -math.inf)
+        assert not torch.isnan(z).any()
+        w = torch.softmax(z, -1)  # (NaN beside +infinity, and of nothing but -infinity)
+        lost = torch.isnan(w).any(-1)
+        assert lost.any() and not lost.all()
+        assert torch.isnan(got[lost, h]).all()
+        size = abs(scale) * torch.where(see & torch.isfinite(z), q.abs() @ k.abs().T, 0.0).amax(-1, keepdim=True)
+        want, tol = w @ v, (2.0 ** -8 + 2.0 ** -15 * size) * (w @ v.abs()) + 2.0 ** -80 * (1 + v.abs().amax())
+        tol = tol + BF16_REL * (want.abs() + tol)
+        assert ((got[:, h] - want).abs() <= tol)[~lost].all()
