@@ -133,8 +133,8 @@ NVFP4_DEVINL void store8(float *p, const float (&x)[8])
 }
 
 // A warp has one token and c.heads_per_warp heads of q and k (those of k behind those of q): lane = slot + slots * head
-// turns the same 8 pairs of every (32 / slots)-th head, with 16-byte loads and stores.  The loads of its first kBatch heads
-// (all it has, as a rule) come before the cosines and sines, which pass through shared memory into registers.
+// turns the same 8 pairs of every (32 / slots)-th head, kBatch heads at most, with 16-byte loads and stores.  All its loads
+// come before the cosines and sines, which pass through shared memory into registers.
 template <class T> constexpr int kBatch = sizeof(T) == 2 ? 6 : 2;
 constexpr int kTail = 2;
 
@@ -159,19 +159,16 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(Call c)
     const int a = ADJACENT ? 16 * slot : 8 * slot, b = ADJACENT ? a + 8 : a + c.n_pairs;
     constexpr int B = kBatch<T>;
     Eight<T> x[B], y[B];
-    const auto load_heads = [&](int h0) {
-#pragma unroll
-        for (int i = 0; i < B; ++i) {
-            const int h = h0 + i * step, hk = h - c.side[0].heads;
-            const T *in = hk < 0 ? q + h * c.head_dim : k + hk * c.head_dim;
-            if (first < step && h < end) {
-                x[i].load(in + a);
-                y[i].load(in + b);
-            }
-        }
-    };
     const int64_t position = lane_position(c, token, lane);
-    load_heads(begin + first);
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+        const int h = begin + first + i * step, hk = h - c.side[0].heads;
+        const T *in = hk < 0 ? q + h * c.head_dim : k + hk * c.head_dim;
+        if (first < step && h < end) {
+            x[i].load(in + a);
+            y[i].load(in + b);
+        }
+    }
     // what is not turned, eight elements at a time and kTail of those in flight
     const int rest = c.head_dim / 8 - 2 * slots, n_rest = (end - begin) * rest;
     Eight<T> tail[kTail];
@@ -205,33 +202,28 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(Call c)
         si[j] = t.y;
     }
     if (first < step) {
-#pragma unroll 1
-        for (int h0 = begin + first; h0 < end; h0 += B * step) {
-            if (h0 != begin + first)
-                load_heads(h0);
 #pragma unroll
-            for (int i = 0; i < B; ++i) {
-                const int h = h0 + i * step, hk = h - c.side[0].heads;
-                T *out = hk < 0 ? q_out + h * c.head_dim : k_out + hk * c.head_dim;
-                if (h >= end)
-                    break;
-                float m[8], n[8], u[8], v[8];
-                x[i].values(m);
-                y[i].values(n);
+        for (int i = 0; i < B; ++i) {
+            const int h = begin + first + i * step, hk = h - c.side[0].heads;
+            T *out = hk < 0 ? q_out + h * c.head_dim : k_out + hk * c.head_dim;
+            if (h >= end)
+                break;
+            float m[8], n[8], u[8], v[8];
+            x[i].values(m);
+            y[i].values(n);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if constexpr (ADJACENT) {  // pair j: elements 2 j and 2 j + 1 of 16
-                        const float xa = j < 4 ? m[(2 * j) & 7] : n[(2 * j) & 7], xb = j < 4 ? m[(2 * j + 1) & 7] : n[(2 * j + 1) & 7];
-                        (j < 4 ? u : v)[(2 * j) & 7] = xa * co[j] - xb * si[j];
-                        (j < 4 ? u : v)[(2 * j + 1) & 7] = xa * si[j] + xb * co[j];
-                    } else {
-                        u[j] = m[j] * co[j] - n[j] * si[j];
-                        v[j] = m[j] * si[j] + n[j] * co[j];
-                    }
+            for (int j = 0; j < 8; ++j) {
+                if constexpr (ADJACENT) {  // pair j: elements 2 j and 2 j + 1 of 16
+                    const float xa = j < 4 ? m[(2 * j) & 7] : n[(2 * j) & 7], xb = j < 4 ? m[(2 * j + 1) & 7] : n[(2 * j + 1) & 7];
+                    (j < 4 ? u : v)[(2 * j) & 7] = xa * co[j] - xb * si[j];
+                    (j < 4 ? u : v)[(2 * j + 1) & 7] = xa * si[j] + xb * co[j];
+                } else {
+                    u[j] = m[j] * co[j] - n[j] * si[j];
+                    v[j] = m[j] * si[j] + n[j] * co[j];
                 }
-                store8(out + a, u);
-                store8(out + b, v);
             }
+            store8(out + a, u);
+            store8(out + b, v);
         }
     }
 #pragma unroll 1
@@ -342,7 +334,7 @@ cudaError_t launch(Call c, int num_sms, cudaStream_t stream)
         c.parts = (all + c.heads_per_warp - 1) / c.heads_per_warp;
         return launch_dependent(rope_any_kernel<T>, dim3((unsigned)((c.tokens * c.parts + kWarps - 1) / kWarps)), kThreads, 0, stream, c);
     }
-    // A warp takes as many heads as its lanes load at once; fewer, down to one each, while there are fewer than kWarpsPerSm
+    // A warp takes as many heads as its lanes load at once (kBatch rounds of heads, and never more); fewer, down to one each, while there are fewer than kWarpsPerSm
     // warps an SM (4999 tokens of 32 fp32 heads: 20.0 us at 24, 18.0 at 64, 17.9 at 128, where 8192 tokens of 48 bf16 heads
     // take 37.1 instead of 33.7).
     const int heads = c.side[0].heads + c.side[1].heads, round = 32 / (c.n_pairs / 8), most = (heads + round - 1) / round;

@@ -187,3 +187,30 @@ def test_many_axes():
         q = rows(5, 3, pairs_first, torch.float32, 12)
         got = g.nvfp4_rope(q, None, positions.to(DEV), table)[0]
         check(got, q, angles(table, positions.tolist(), axis), 8)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("tokens,hq,hk,d,rotary", [
+    (8192, 40, 8, 128, 128), (20001, 5, 3, 128, 128), (10001, 11, 4, 96, 48), (10002, 20, 3, 80, 32), (9733, 0, 9, 512, 512),
+    (9999, 70, 1, 24, 16)])
+def test_many_tokens(dtype, adjacent, tokens, hq, hk, d, rotary):
+    """Several heads to a lane (of q and of k in one warp), elements that are not turned in several rounds, and a last block
+    that is not full: some tokens against the definition, all of them against calls of few tokens, and in place."""
+    pairs = rotary // 2
+    axis = [i % 3 for i in range(pairs)]
+    table = g.RopeTable.make(frequencies(pairs), axis)
+    positions = torch.randint(0, 200000, (3, tokens), generator=torch.Generator().manual_seed(1))
+    at = positions.to(DEV)
+    q, k = rows(tokens, hq, d, dtype, 2, pad=8), rows(tokens, hk, d, dtype, 3, pad=16)
+    got = g.nvfp4_rope(q, k, at, table, adjacent=adjacent)
+    some = list(range(0, tokens, 997)) + [tokens - 2, tokens - 1]
+    angle = angles(table, positions[:, some].tolist(), axis)
+    check(got[0][some], q[some], angle, pairs, adjacent)
+    check(got[1][some], k[some], angle, pairs, adjacent)
+    for lo in range(0, tokens, 700):
+        part = slice(lo, min(lo + 700, tokens))
+        few = g.nvfp4_rope(q[part], k[part], at[:, part], table, adjacent=adjacent)
+        assert torch.equal(got[0][part], few[0]) and torch.equal(got[1][part], few[1])
+    g.nvfp4_rope(q, k, at, table, adjacent=adjacent, out=(q, k))
+    assert torch.equal(q, got[0]) and torch.equal(k, got[1])
