@@ -933,7 +933,8 @@ def nvfp4_rope(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
     """(q, k) turned by their tokens' positions.
 
     q [tokens, n_q_heads, head_dim] and k [tokens, n_k_heads, head_dim] (or None), both bf16 or fp32, token rows may be
-    strided; positions int64 [tokens], or [axes, tokens] for a table with several axes.  out: two tensors of the
+    strided; positions int64 [tokens], or [axes, tokens] for a table with several axes (text, whose tokens have one
+    position for all axes, may pass positions.expand(axes, -1)).  out: two tensors of the
     inputs' shapes and type, which may be the inputs themselves (in place)."""
     shape, dtype = q.shape, q.dtype
     if len(shape) != 3:

@@ -417,7 +417,7 @@ int nvfp4_rope(const nvfp4_rope_args *args, nvfp4_stream_t stream)
     if (a->n_tokens == 0 || a->n_q_heads + a->n_k_heads == 0)
         return NVFP4_OK;
     if (!a->positions || !rope::aligned(a->positions, 8) ||
-        (a->n_axes > 1 && (a->positions_ld < a->n_tokens || a->positions_ld > (INT64_C(1) << 60) / a->n_axes)) ||
+        (a->n_axes > 1 && ((a->positions_ld < a->n_tokens && a->positions_ld != 0) || a->positions_ld > (INT64_C(1) << 60) / a->n_axes)) ||
         (a->n_pairs > 0 && (!a->pairs || !rope::aligned(a->pairs, 16))))
         return NVFP4_ERR_INVALID_ARG;
     if ((a->n_q_heads > 0 && !rope::side_ok(a->q, a->q_ld, a->q_out, a->q_out_ld, a->n_q_heads, a)) ||

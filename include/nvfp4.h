@@ -594,7 +594,7 @@ typedef struct {
     void *q_out, *k_out;      /* device [n_tokens][q_out_ld], [n_tokens][k_out_ld], same type */
     int64_t q_out_ld, k_out_ld;
     const int64_t *positions; /* device [n_axes][positions_ld] */
-    int64_t positions_ld;     /* at least n_tokens (not looked at with one axis) */
+    int64_t positions_ld;     /* at least n_tokens, or 0: one row for every axis (not looked at with one axis) */
     const nvfp4_rope_pair *pairs; /* device [n_pairs] */
     int64_t n_tokens;         /* below 2^31 */
     int32_t n_axes;           /* 1 to 256 */

@@ -214,3 +214,16 @@ def test_many_tokens(dtype, adjacent, tokens, hq, hk, d, rotary):
         assert torch.equal(got[0][part], few[0]) and torch.equal(got[1][part], few[1])
     g.nvfp4_rope(q, k, at, table, adjacent=adjacent, out=(q, k))
     assert torch.equal(q, got[0]) and torch.equal(k, got[1])
+
+
+@pytest.mark.parametrize("dtype,d,pairs", [(torch.bfloat16, 64, 32), (torch.float32, 40, 10)])
+def test_one_row_of_positions_for_every_axis(dtype, d, pairs):
+    """Text in a model with several axes: positions.expand(axes, tokens), whose rows are one row."""
+    table = g.RopeTable.make(frequencies(pairs), [i % 40 for i in range(pairs)])
+    for tokens in (1, 33):
+        at = torch.arange(7000, 7000 + tokens, device=DEV)
+        q, k = rows(tokens, 4, d, dtype, 2), rows(tokens, 2, d, dtype, 3)
+        want = g.nvfp4_rope(q, k, at.repeat(40, 1), table)
+        got = g.nvfp4_rope(q, k, at.expand(40, tokens), table)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        check(got[0], q, angles(table, at.repeat(40, 1).tolist(), [i % 40 for i in range(pairs)]), pairs)

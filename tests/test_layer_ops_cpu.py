@@ -156,3 +156,11 @@ def test_packed_argument_blocks_match_their_structures():
         values = [float(i + 1) if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(structure._fields_)]
         assert packed.size == ctypes.sizeof(structure)
         assert packed.pack(*values) == bytes(structure(*values))
+
+
+def test_rope_refuses_strides_between_one_row_and_all(lib):
+    """One row of positions for every axis (0) is taken, and whole rows are; nothing between or below."""
+    a = dict(q=FAKE, q_ld=512, q_out=FAKE, q_out_ld=512, positions=FAKE, pairs=FAKE, n_tokens=3, n_axes=2, n_pairs=64,
+             n_q_heads=4, head_dim=128, dtype=1, scale=1.0)
+    for ld in (-1, 1, 2, 1 << 60):
+        assert lib.nvfp4_rope(ctypes.byref(binding.RopeArgsC(**a, positions_ld=ld)), None) == BAD, ld
