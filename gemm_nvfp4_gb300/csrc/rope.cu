@@ -354,6 +354,8 @@ bool side_ok(const void *in, int64_t in_ld, const void *out, int64_t out_ld, int
 {
     const int64_t width = (int64_t)heads * a->head_dim;
     const int unit = a->dtype == NVFP4_OUT_BF16 ? 8 : 4;
+    if (in == out && in_ld != out_ld && a->n_tokens > 1)  // in place, but a row would overwrite others
+        return false;
     return in && out && aligned(in, 16) && aligned(out, 16) && in_ld >= width && out_ld >= width && in_ld % unit == 0 &&
            out_ld % unit == 0 && in_ld <= (INT64_C(1) << 60) / a->n_tokens && out_ld <= (INT64_C(1) << 60) / a->n_tokens;
 }

@@ -583,7 +583,8 @@ int nvfp4_rope_pairs(const double *inv_freq, const int32_t *axis, int32_t n_pair
 
 /* Turn the heads of q and k: n_q_heads (n_k_heads) heads of head_dim elements side by side
  * per token, so that inputs can be column ranges of one QKV product's output.
- * An output may be its input (the same pointer and stride: in place); other overlaps race.
+ * An output may be its input (the same pointer and stride: in place; the same pointer with another stride is refused);
+ * other overlaps race.
  * Requirements: head_dim a multiple of 8, at most 512; 2 n_pairs <= head_dim; pointers
  * 16-byte aligned and strides multiples of 16 bytes; axes in `pairs` below n_axes (a larger one
  * reads the last axis).  No workspace.  Rows of q or k are not looked at where its number of heads

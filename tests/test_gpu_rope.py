@@ -227,3 +227,12 @@ def test_one_row_of_positions_for_every_axis(dtype, d, pairs):
         got = g.nvfp4_rope(q, k, at.expand(40, tokens), table)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
         check(got[0], q, angles(table, at.repeat(40, 1).tolist(), [i % 40 for i in range(pairs)]), pairs)
+
+
+def test_one_token_in_place_through_views_of_other_strides():
+    """The stride of a single row is not looked at: in place through another view of it."""
+    table = g.RopeTable.make(frequencies(32))
+    x = rows(1, 2, 64, torch.bfloat16, 4, pad=8)
+    want = g.nvfp4_rope(x, None, torch.tensor([9], device=DEV), table)[0]
+    g.nvfp4_rope(x, None, torch.tensor([9], device=DEV), table, out=(x.as_strided((1, 2, 64), (128, 64, 1)), None))
+    assert torch.equal(x, want)

@@ -164,3 +164,14 @@ def test_rope_refuses_strides_between_one_row_and_all(lib):
              n_q_heads=4, head_dim=128, dtype=1, scale=1.0)
     for ld in (-1, 1, 2, 1 << 60):
         assert lib.nvfp4_rope(ctypes.byref(binding.RopeArgsC(**a, positions_ld=ld)), None) == BAD, ld
+
+
+def test_rope_refuses_an_output_that_is_its_input_with_another_stride(lib):
+    a = dict(positions=FAKE, pairs=FAKE, n_axes=1, n_pairs=64, n_q_heads=4, n_k_heads=4, head_dim=128, dtype=1, scale=1.0,
+             q=FAKE, q_ld=512, q_out=FAKE, q_out_ld=512, k=2 * FAKE, k_ld=520, k_out=2 * FAKE, k_out_ld=520)
+
+    def run(**kw):
+        return lib.nvfp4_rope(ctypes.byref(binding.RopeArgsC(**{**a, **kw})), None)
+
+    for kw in (dict(q_ld=520), dict(q_out_ld=1024), dict(k_ld=512), dict(k_out_ld=512)):
+        assert run(n_tokens=2, **kw) == BAD, kw
