@@ -1118,6 +1118,8 @@ extern "C" int nvfp4_prompt_attention(const nvfp4_prompt_attention_args *args, v
         return NVFP4_ERR_WORKSPACE;
     if (args->total == 0 || args->n_seqs == 0)
         return NVFP4_OK;
+    if (args->out == args->q || args->out == args->k || args->out == args->v)  // other CTAs read them after rows are written
+        return NVFP4_ERR_INVALID_ARG;
     prompt::Call c;
     c.out = args->out;
     c.out_ld = args->out_ld;

@@ -645,7 +645,7 @@ int nvfp4_rope(const nvfp4_rope_args *args, nvfp4_stream_t stream);
 typedef struct {
     const uint16_t *q, *k, *v;  /* device bf16 bits [total][q_ld], [total][k_ld], [total][v_ld] */
     int64_t q_ld, k_ld, v_ld;
-    void *out;                  /* device [total][out_ld], fp32 or bf16 bits; not q, k or v */
+    void *out;                  /* device [total][out_ld], fp32 or bf16 bits; not q, k or v (refused), nor rows of theirs */
     int64_t out_ld;
     const int32_t *offsets;     /* device [n_seqs + 1]; NULL: one sequence of `total` tokens (n_seqs = 1) */
     int64_t n_seqs;             /* at most 65535 */

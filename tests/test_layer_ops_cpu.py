@@ -175,3 +175,10 @@ def test_rope_refuses_an_output_that_is_its_input_with_another_stride(lib):
 
     for kw in (dict(q_ld=520), dict(q_out_ld=1024), dict(k_ld=512), dict(k_out_ld=512)):
         assert run(n_tokens=2, **kw) == BAD, kw
+
+
+def test_prompt_attention_refuses_an_output_that_is_an_input(lib):
+    a = dict(q=FAKE, k=2 * FAKE, v=3 * FAKE, q_ld=4096, k_ld=1024, v_ld=1024, out_ld=4096, n_seqs=1, total=9, n_q_heads=32,
+             n_kv_heads=8, head_dim=128, out_dtype=1, causal=1, scale=0.1)
+    for out in (FAKE, 2 * FAKE, 3 * FAKE):
+        assert lib.nvfp4_prompt_attention(ctypes.byref(binding.PromptAttentionArgsC(**a, out=out)), None, 0, None) == BAD
