@@ -145,22 +145,34 @@ struct Cursor {
     uint32_t with;     // lanes whose sequence has the level's place
     uint32_t pos;      // number of the first item of the level (a call has less than 2^31)
     uint32_t rank;     // by sequence: places and lane of the one at hand
+    int reached;       // end of the sequences so far
+    bool descended;    // whether an offset did
 
     __device__ __noinline__ void load(const Call &c, int lane)
     {
         const int b = chunk + lane;
-        begin = len = 0;
-        if (b < c.n_seqs) {
-            len = c.total;
-            if (c.offsets) {
-                const int from = c.offsets[b], to = c.offsets[b + 1];
-                const bool ok = from >= 0 && to >= from && to <= c.total;
-                if (!ok && blockIdx.x == 0)
-                    kv::report_index(c.status, kStatusPromptOffsets);
-                begin = from;
-                len = ok ? to - from : 0;
-            }
+        int end = c.total;
+        begin = b < c.n_seqs ? 0 : c.total;
+        bool ok = true;
+        if (c.offsets && b < c.n_seqs) {
+            begin = c.offsets[b];
+            end = c.offsets[b + 1];
+            ok = begin >= 0 && end >= begin && end <= c.total;
         }
+        // where offsets descend, later sequences may lie on earlier ones: the rows belong to the first
+        descended |= __any_sync(0xFFFFFFFFu, !ok);
+        if (__builtin_expect(descended, 0)) {
+#pragma unroll 1
+            for (int i = 0; i < 32; ++i) {
+                ok = ok && (lane != i || begin >= reached);
+                reached = max(reached, __shfl_sync(0xFFFFFFFFu, ok ? end : 0, i));
+            }
+        } else {
+            reached = (int)__reduce_max_sync(0xFFFFFFFFu, (unsigned)end);
+        }
+        if (!ok && blockIdx.x == 0)
+            kv::report_index(c.status, kStatusPromptOffsets);
+        len = ok ? end - begin : 0;
         places = (int)((uint32_t)(len + 2 * c.tokens - 1) / (2u * c.tokens));
     }
     // To the chunk's first item.
@@ -176,6 +188,8 @@ struct Cursor {
     {
         chunk = -32;
         pos = rank = 0;
+        reached = 0;
+        descended = false;
         level = -1;
     }
     // The next sequence by length.

@@ -637,7 +637,8 @@ int nvfp4_rope(const nvfp4_rope_args *args, nvfp4_stream_t stream);
  * heads (so that q, k and v can be column ranges of one QKV product's output).
  * Offsets stay on the device: the call never synchronises and can be captured in a CUDA graph
  * and replayed with other lengths.  A sequence whose two
- * offsets do not ascend within 0 .. total stores code 44 in the status word and is left out.
+ * offsets do not ascend within 0 .. total stores code 44 in the status word and is left out, and so is one that then
+ * begins before the end of an earlier one.
  * workspace  NULL, or at least 256 bytes with the status word (nvfp4_device_status): nothing
  *            else is kept there, so calls on several streams may share it.
  * Determinism: a token's result depends on its place in its sequence and on what it sees alone,

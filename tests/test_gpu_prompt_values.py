@@ -97,3 +97,19 @@ def test_infinities_in_keys(bad, causal, window, scale, d):
         want, tol = w @ v, (2.0 ** -8 + 2.0 ** -15 * size) * (w @ v.abs()) + 2.0 ** -80 * (1 + v.abs().amax())
         tol = tol + BF16_REL * (want.abs() + tol)
         assert ((got[:, h] - want).abs() <= tol)[~lost].all()
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("empty", [0, 30, 75])
+def test_sequences_on_the_rows_of_earlier_ones(causal, empty):
+    """Behind offsets that descend: a sequence that begins on an earlier one's rows is left out, also 32 sequences and more
+    later, and those behind are computed."""
+    p = Prompts([100, 50, 50], 4, 2, 64, seed=7)
+    want = p.run(causal=causal)
+    ws = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    out = torch.full(p.q.shape, 7.0, dtype=torch.bfloat16, device=DEV)
+    offsets = [0, 100, 50] + [50] * empty + [150, 200]
+    p.run(causal=causal, offsets=torch.tensor(offsets, dtype=torch.int32, device=DEV), out=out, workspace=ws)
+    assert g.nvfp4_device_status(ws) == (g.NVFP4_ERR_DEVICE_INDEX, 44)
+    assert torch.equal(out[:100], want[:100]) and torch.equal(out[150:], want[150:])
+    assert (out[100:150] == 7).all()
