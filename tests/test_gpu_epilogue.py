@@ -207,3 +207,63 @@ def test_another_stream():
     got = p.run(bias=bias, stream=s)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(got, want)
+
+
+class Sampled:
+    """A product too large for the oracle: its sums at some tokens and rows."""
+
+    def __init__(self, N, M, K, tokens, rows):
+        gen = torch.Generator(DEV).manual_seed(N)
+        self.x = torch.randn(N, K, device=DEV, generator=gen).to(torch.bfloat16)
+        self.W = g.nvfp4_quantize(0.02 * torch.randn(M, K, device=DEV, generator=gen))
+        self.at = torch.tensor(tokens)[:, None], torch.tensor(rows)
+        self.s, self.A = oracle.gemv(inputs.bf16_bits(self.x[tokens].cpu()), self.W.codes[rows].cpu().numpy(),
+                                     self.W.scales[rows].cpu().numpy(), self.W.tensor_scale.cpu().numpy()[0])
+
+    def check(self, y, bias, act, residual):
+        part = lambda t, at: None if t is None else t.cpu()[at]  # noqa: E731
+        ref, tol = reference(self.s, self.A, part(bias, self.at[1]), act, part(residual, self.at), y.dtype)
+        assert_close(to_np(y.cpu()[self.at]), ref, tol, act)
+
+
+# Operands beyond what L2 holds, and a number of tiles that leaves few for the last wave: whole tiles in a launch of their
+# own, the last ones split behind them in a second one that does not wait for it, and a reduction.  One token tile (tiles
+# behind row 152 * 128 are the split ones), two of them, and a 27B-class layer's down product of 2048 tokens.
+@pytest.mark.parametrize("N,M,K", [(200, 20400, 12032), (300, 19500, 12032), (2048, 5120, 17408)])
+def test_split_tiles_behind_whole_ones(N, M, K):
+    tokens = sorted({0, 1, N // 2, N - 1, *range(255, N, 256), *range(256, N, 256)})
+    rows = sorted({*range(0, M, 97), *range(max(M - 1100, 0), M, 13), M - 1})
+    p = Sampled(N, M, K, tokens, rows)
+    gen = torch.Generator(DEV).manual_seed(7)
+    ws = torch.zeros(g.nvfp4_workspace_bytes(g.NVFP4_OP_GEMM_PREFILL, N, M, K), dtype=torch.uint8, device=DEV)
+    for dtype in (torch.float32, torch.bfloat16):
+        assert torch.equal(g.nvfp4_gemm_epilogue(p.x, p.W, out_dtype=dtype), g.nvfp4_gemm_prefill(p.x, p.W, out_dtype=dtype))
+        wide = 2 * torch.randn(N, M + 3, device=DEV, generator=gen).to(dtype)
+        residual = wide[:, :M]
+        for act, bias in (("none", None), ("gelu_tanh", torch.randn(M, device=DEV, generator=gen)),
+                          ("silu", torch.randn(M, device=DEV, generator=gen).to(torch.bfloat16))):
+            call = lambda **kw: g.nvfp4_gemm_epilogue(p.x, p.W, bias=bias, activation=ACTS[act], workspace=ws, **kw)  # noqa: E731
+            y = call(residual=residual, out_dtype=dtype)
+            p.check(y, bias, act, residual)
+            p.check(call(out_dtype=dtype), bias, act, None)
+            # in place, on the residual that the launch before has just written
+            for _ in range(3):
+                z = residual * 1
+                assert call(residual=z, out=z) is z
+                assert torch.equal(z, y)
+    assert g.nvfp4_device_status(ws) == (g.NVFP4_OK, 0)
+
+
+def test_rotary_positions_right_behind_split_tiles():
+    """The launch after a product with three launches, a programmatic dependent of the last one, reads tiles of the first."""
+    N, M, K = 200, 20480, 12032
+    p = Sampled(N, M, K, [0, N - 1], [0, M - 1])
+    table = g.RopeTable.make([1e6 ** (-i / 64) for i in range(64)])
+    at = torch.arange(N, device=DEV)
+    y = g.nvfp4_gemm_epilogue(p.x, p.W, out_dtype=torch.bfloat16)
+    torch.cuda.synchronize()
+    want = g.nvfp4_rope(y.view(N, 160, 128), None, at, table)[0]
+    for _ in range(20):
+        y.zero_()
+        g.nvfp4_gemm_epilogue(p.x, p.W, out=y)
+        assert torch.equal(g.nvfp4_rope(y.view(N, 160, 128), None, at, table)[0], want)
