@@ -358,10 +358,12 @@ NVFP4_DEVINL void store_column(const Args &a, const uint32_t (&r)[2][kEpiCols], 
 // TN: tokens per tile (MMA N), 256 or 192; the host picks it per call so that
 // the grid fills the SMs' waves (the accumulation order does not depend on it).
 //
-// PARTS: the tensor core's own accumulation over 17408 products is off by 3.7e-6 of the outputs' norm (the error grows with
-// their number; NVFP4 products that split K are at 2e-7).  So warps of their own add up parts of 2048 in registers, 96
-// columns a thread, from two accumulators that the MMAs take by turns (hence TN = 192): 2.3e-7.  2048 tokens of 17408 ->
-// 5120 with an fp32 residual take 374 us instead of 352 (441 with the parts added up by the dequantisers).
+// PARTS: the tensor core's own accumulation over 17408 products is off by 3.7e-6 of the outputs' norm (FP6; NVFP4's whole
+// tiles by 6.6e-6, its tiles split in nine by 3.9e-7): the error grows with their number.  So warps of their own add up parts of
+// 2048 in registers, 96 columns a thread, from two accumulators that the MMAs take by turns (hence TN = 192): 2.3e-7.  2048 tokens
+// of 17408 -> 5120 with an fp32 residual take 374 us instead of 352 (441 with the parts added up by the dequantisers).  FP6 products
+// without an epilogue, and NVFP4's, keep the sums that they had, which are well within the library's bound (6.6e-6 of the norm is
+// about 8e-8 sum |w x| there, of 1e-5).
 template <int NW, bool ALIGNED, int FMT = 0, bool TMAC = false, int TN = BN, bool SPLIT = false, bool EPI = false,
           bool PARTS = false>
 __global__ void __launch_bounds__(PARTS ? kThreadsParts : TMAC ? kThreadsTma : kThreads, 1)
@@ -809,7 +811,9 @@ __global__ void __launch_bounds__(PARTS ? kThreadsParts : TMAC ? kThreadsTma : k
                     sring[p][mi] = scale_at(mi, p);
             uint32_t scl[NW];
             // Unrolled, so that the ring positions and sring's registers are constants: 2048 tokens of 17408 -> 5120 take
-            // 322 us instead of 395 (with bias, activation or residual 352 instead of 444; 362 unrolled by 8).
+            // 322 us instead of 395.  With an epilogue 16 is better than 8 for every shape tried (cold, by 16 / 8 / 4): bf16 with
+            // a residual 2048 tokens 349 / 357 / 402 us, 512 tokens 120 / 124 / 140; 5120 -> 17408 with bias and tanh GELU 2048
+            // tokens 310 / 318 / 355, 512 tokens 83 / 85 / 95; 64 tokens with bias 42 / 44 / 48.
 #pragma unroll (EPI && !PARTS ? 16 : 8)
             for (int kb = 0; kb < num_kb; ++kb) {
                 if ((kb & 1) == 0) {

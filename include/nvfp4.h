@@ -358,7 +358,8 @@ int nvfp4_fp6_gateup_swiglu(const uint16_t *x, int64_t N,
  * its bias, an O or down product onto the residual stream, an ungated MLP's first product with its
  * activation, without another pass over [N][M].  The product itself is that of
  * nvfp4_gemm_prefill (nvfp4_fp6_gemm): the same kernels, workspace and accuracy, and the same sums to the bit
- * (but for FP6 with fp32 outputs, N > 16 and K > 8192, which are added up in parts and nearer), so with
+ * (but for FP6 with fp32 outputs, N > 16 and K > 8192, which are added up in parts and are nearer: at K = 17408 off by 2e-7
+ * of the outputs' norm, where nvfp4_fp6_gemm is by 4e-6 and nvfp4_gemm_prefill by up to 7e-6), so with
  * the sum's error d = 1e-5 * sum |w * x| + 1e-7,
  *     |y - exact| <= L * (d + 2^-23 * |sum + bias|) + 2^-20 * (1 + u) * |act| + 2^-24 * |y| + 1e-30, and
  * the rounding of y, where L bounds the activation's slope around sum + bias (at most 1.13 but for
