@@ -23,9 +23,11 @@
 // the c-th of every P, in alternating directions: for one long causal prompt every CTA then has the same
 // number of keys to within a tile.  The lengths are on the device, so each CTA finds its items itself.
 //
-// Measured on one GB300: 16384 tokens (40 and 8 heads of 128, causal, 2.75 TFLOP) 1.70 ms, 1.62 PFLOP/s, 0.83 of the
-// measured bf16 rate; 24 packed prompts of 19 to 2500 tokens (32 and 8 heads) 136 us, 0.56 of it; 8191 tokens in a
-// window of 1024 (16 and 4 heads of 64) 57 us, 5 images of 577 to 2305 tokens (16 heads of 64) 62 us.
+// Measured on one GB300, calls among others: 16384 tokens (40 and 8 heads of 128, causal, 2.75 TFLOP) 1.85 ms, 1.49 PFLOP/s,
+// 0.76 of the measured bf16 rate (1.70 ms alone, before the power limit tells); 24 packed prompts of 19 to 2500 tokens (32 and 8
+// heads) 143 us, 0.53 of it; 8191 tokens in a window of 1024 (16 and 4 heads of 64) 55 us, 5 images of 577 to 2305 tokens (16
+// heads of 64) 61 us.  The weights' rounding to bf16, V's type and so the MMA's, is most of the outputs' error: 0.0008 to 0.0015 of
+// their norm in fp32, 0.0018 to 0.0023 in bf16 (exact weights: 0.0016).  Two bf16 numbers a weight would double the second product.
 // For a key tile of 256 rows and heads of 128 the MMAs take 2048 clocks and the whole 2800: after each S the
 // MMA thread stands still until the pipe has come to it, and some 130 clocks longer before the next product begins.  With
 // heads of 64 the MMAs would take 1300 and the exponentials 1024; 2300 go by: the softmax warps, two to a scheduler, issue in
