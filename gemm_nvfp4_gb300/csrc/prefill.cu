@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(PARTS ? kThreadsParts : TMAC ? kThreadsTma : k
         }
         tc::mbar_init(tmem_full, C::kIssue);
         tc::mbar_init(tmem_empty, kDqWarps);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; PARTS && i < 2; ++i) {
             tc::mbar_init(&part_full[i], 1);
             tc::mbar_init(&part_empty[i], kSumWarps);
         }
